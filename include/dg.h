@@ -320,6 +320,70 @@ dg_status dg_m_grouped_fp4_fp4_gemm_nt_masked(const void *A, const int32_t *sfa,
                                               int num_groups, void *stream);
 
 /*
+ * Tokens to experts and back: the steps between a router's choice of topk
+ * experts a token and the grouped products above, and from their rows back to
+ * the tokens.  BF16 token states X, Y [T][width]; a router's expert_ids int32
+ * [T][topk] and weights float [T][topk].
+ *
+ * dg_moe_sort_*: sorts the T * topk assignments by expert, stably (within an
+ * expert in the order of t * topk + j), and gives each its row: pos int32
+ * [T][topk].  An id outside [0, num_experts) (an expert of another rank) gets
+ * pos -1: that assignment is dropped.  At most 1024 experts.
+ *   contiguous: the rows are those of the contiguous layout, expert after
+ *     expert, every expert's segment a multiple of 128 rows (none for an expert
+ *     without tokens).  m_indices int32 [rows]: expert of each row, -1 in a
+ *     segment's padding rows, -2 past the last segment (every form above skips
+ *     both); ks int32 [num_experts]: rows of each segment, the K counts of the
+ *     K-grouped products.  rows is the caller's capacity, a multiple of 128;
+ *     dg_moe_sorted_rows() gives one that no choice of experts exceeds.
+ *     Assignments past the capacity are dropped, and ks is cut there.
+ *   masked: expert g's rows start at g * M_max; masked_m int32 [num_experts] is
+ *     the count of each, at most M_max; assignments past it are dropped.
+ * dg_moe_dispatch_*: rows_out[pos[t][j]] = X[t].  m_indices (contiguous layout;
+ *   NULL for masked) names the rows: those with -1 are cleared (zeros, scale
+ *   1), as a weight gradient over whole segments needs; all others that no
+ *   token goes to are untouched.  pos outside [0, rows) is skipped.
+ *   bf16: rows_out BF16 [rows][H], any H.
+ *   fp8: rows_out E4M3 [rows][H], H a multiple of 128, quantised with one scale
+ *     per 1x128 block: s = amax / 448 (at least 2^-126; 1 for a block of zeros),
+ *     code = E4M3(x / s), round-to-nearest-even.  sf is the LHS scale tensor of
+ *     the grouped forms: float [H/128][rows] or, masked, [G][H/128][M_max], with
+ *     group_rows = rows or M_max; ue8m0 != 0: int32 words [ceil(H/512)][...] of
+ *     four power-of-two scales, s rounded up to the next (a last word's bytes
+ *     past H stand for scale 1).  A block that holds an infinity or NaN gives
+ *     NaN or infinite scales and values, never a fault.
+ * dg_moe_combine: Y[t] = residual[t] + sum_j weights[t][j] * rows_in[pos[t][j]]
+ *   over the assignments whose pos is in [0, rows), added in j order in FP32 and
+ *   rounded once to BF16.  residual [T][N] and weights may be NULL (none; 1).
+ *   Any N.  Gradient of dg_moe_dispatch_bf16: dX = combine of dRows without
+ *   weights and residual.
+ * dg_moe_combine_backward: d_rows[pos[t][j]] = weights[t][j] * dY[t] (BF16), and
+ *   d_weights[t][j] = <dY[t], rows_in[pos[t][j]]> (FP32; 0 for a dropped
+ *   assignment; d_weights NULL: not wanted, and rows_in may be NULL).  Rows
+ *   with m_indices -1 are cleared.  The residual's gradient is dY itself.
+ * X, Y, residual and row arrays must be 16-byte aligned, the rest 4-byte; an
+ * array without elements (T or rows 0) may be NULL.  Two
+ * assignments never share a row in a pos that dg_moe_sort_* made; given one in
+ * which they do, either may win.  dg_moe_sort_contiguous and _masked of more
+ * than 2048 assignments use the stream's workspace.
+ */
+int64_t dg_moe_sorted_rows(int T, int topk, int num_experts);
+dg_status dg_moe_sort_contiguous(const int32_t *expert_ids, int32_t *pos, int32_t *m_indices, int32_t *ks,
+                                 int T, int topk, int num_experts, int rows, void *stream);
+dg_status dg_moe_sort_masked(const int32_t *expert_ids, int32_t *pos, int32_t *masked_m, int T, int topk,
+                             int num_experts, int M_max, void *stream);
+dg_status dg_moe_dispatch_bf16(const void *X, const int32_t *pos, const int32_t *m_indices, void *rows_out,
+                               int T, int topk, int rows, int H, void *stream);
+dg_status dg_moe_dispatch_fp8(const void *X, const int32_t *pos, const int32_t *m_indices, void *rows_out,
+                              void *sf, int T, int topk, int rows, int group_rows, int H, int ue8m0,
+                              void *stream);
+dg_status dg_moe_combine(const void *rows_in, const int32_t *pos, const float *weights, const void *residual,
+                         void *Y, int T, int topk, int rows, int N, void *stream);
+dg_status dg_moe_combine_backward(const void *dY, const void *rows_in, const int32_t *pos, const float *weights,
+                                  const int32_t *m_indices, void *d_rows, float *d_weights, int T, int topk,
+                                  int rows, int N, void *stream);
+
+/*
  * Health of the current device's kernels.  The producer/consumer kernel
  * variant (one wave streams the A tiles into an LDS ring, the others wait on
  * per-slot LDS flags; chosen for few rows, e.g. M <= 128) bounds every such

@@ -21,3 +21,5 @@ from .dg import (DGError, describe_config, dg_fp8_gemm_nt, dg_m_grouped_fp8_gemm
                  m_grouped_bf16_gemm_nt_contiguous, m_grouped_bf16_gemm_nt_masked, SCALE_FP4_FP4,
                  dg_fp4_fp4_gemm_nt, dg_m_grouped_fp4_fp4_gemm_nt_contiguous, dg_m_grouped_fp4_fp4_gemm_nt_masked,
                  fp4_fp4_gemm_nt, m_grouped_fp4_fp4_gemm_nt_contiguous, m_grouped_fp4_fp4_gemm_nt_masked)
+from .dg import (dg_moe_combine, dg_moe_combine_backward, dg_moe_dispatch_bf16, dg_moe_dispatch_fp8,  # noqa: F401
+                 dg_moe_sort_contiguous, dg_moe_sort_masked, moe_sorted_rows)

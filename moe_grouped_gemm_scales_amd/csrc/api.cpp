@@ -415,6 +415,18 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
 
 }  // namespace
 
+dg_status stream_scratch(void* stream, size_t bytes, float** out) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* st = nullptr;
+    int dev = 0;
+    dg_status s = device_state(&st, &dev);
+    if (s != DG_OK) return s;
+    Workspace* w = nullptr;
+    s = ensure_workspace(*st, static_cast<hipStream_t>(stream), bytes, 0, &w);
+    if (s == DG_OK) *out = w->partials;
+    return s;
+}
+
 dg_status set_error(dg_status s, const std::string& msg) {
     t_last_error = msg;
     if (env_flag("DG_DEBUG")) std::fprintf(stderr, "[dg] error %d: %s\n", (int)s, msg.c_str());

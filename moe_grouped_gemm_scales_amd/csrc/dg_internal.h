@@ -129,6 +129,10 @@ dg_status scratch_address(void** out);
 // call can be captured in a graph)
 dg_status clear_words(uint32_t* p, int n, void* stream);
 
+// The stream's scratch buffer on the current device, at least `bytes` large (api.cpp; the
+// split-K partials' buffer: work on one stream runs in order, so its calls share it).
+dg_status stream_scratch(void* stream, size_t bytes, float** out);
+
 // Errors (api.cpp).
 dg_status set_error(dg_status s, const std::string& msg);
 bool env_flag(const char* name);

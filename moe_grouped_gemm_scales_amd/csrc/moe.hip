@@ -1,0 +1,714 @@
+// Tokens to experts and back (hipcc, gfx950): the steps between a router's
+// top-k choice and the grouped products, and from their rows back to the
+// tokens.  The operations and their layouts are specified in include/dg.h.
+//
+//   sort      a counting sort of T * k expert ids: stable, so that a token's
+//             place depends on the ids alone and every run gives the same rows
+//   dispatch  rows[pos[t][j]] = X[t] (BF16 copies, or quantised to E4M3)
+//   combine   Y[t] = residual[t] + sum_j w[t][j] rows[pos[t][j]]
+//   combine backward   dRows[pos[t][j]] = w[t][j] dY[t],  dw[t][j] = <dY[t], rows[pos[t][j]]>
+//
+// All of it moves data: nothing here has more than a few operations a byte, so
+// each kernel is built to read and write every byte once, 16 bytes a lane.
+// Work is cut by token, not by row: a token's hidden state is then read (and
+// quantised) once for its k copies, and a token's k rows meet in one wave's
+// registers, where the sum over j has a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+typedef unsigned char u8;
+typedef unsigned short u16;
+typedef unsigned int u32;
+typedef unsigned long long u64;
+typedef u32 u32x4 __attribute__((ext_vector_type(4)));
+typedef u32 u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kAlign = 128;            // rows an expert's segment starts on a multiple of
+constexpr int kMaxExperts = 1024;      // the sort's per-wave counters live in LDS
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortBlocks = 256;       // at most, so that one pass over their counts stays short
+constexpr int kPadding = -1;           // m_indices of a padding row inside a segment
+constexpr int kUnused = -2;            // ... of a row past the last segment
+
+__device__ __forceinline__ float bf16_lo(u32 w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+__device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
+__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
+
+// ---------------------------------------------------------------- sort
+// Block b counts the experts of its chunk of the ids.
+__global__ void __launch_bounds__(kSortThreads) dg_moe_count_kernel(const int* __restrict__ ids, int n, int G,
+                                                                    int chunk, u32* __restrict__ hist) {
+    __shared__ u32 h[kMaxExperts];
+    for (int g = threadIdx.x; g < G; g += kSortThreads) h[g] = 0u;
+    __syncthreads();
+    const int first = (int)blockIdx.x * chunk;
+    const int last = n - first < chunk ? n : first + chunk;
+    for (int i = first + (int)threadIdx.x; i < last; i += kSortThreads) {
+        const u32 e = (u32)ids[i];
+        if (e < (u32)G) atomicAdd(&h[e], 1u);
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < G; g += kSortThreads) hist[(u64)blockIdx.x * G + g] = h[g];
+}
+
+// Block b places its chunk.  Rank of an id = ids of the same expert in earlier
+// blocks (summed here from every block's counts) + in earlier waves of the
+// block (an LDS table [wave][expert]) + in earlier lanes (lanes with the same
+// expert found by one ballot per bit of the id).  hist == nullptr: the only
+// block, which counts its own ids.  masked_rows > 0: masked layout, expert g's
+// rows start at g * masked_rows; 0: contiguous layout, segments of whole
+// 128-row blocks, and every block writes its share of m_indices.
+__global__ void __launch_bounds__(kSortThreads)
+dg_moe_place_kernel(const int* __restrict__ ids, int n, int G, int bits, int chunk, const u32* __restrict__ hist,
+                    int masked_rows, int rows, int* __restrict__ pos, int* __restrict__ m_indices,
+                    int* __restrict__ group_rows) {
+    __shared__ u32 total[kMaxExperts];      // rows of each expert
+    __shared__ u32 before[kMaxExperts];     // ... in earlier blocks; then the next rank
+    __shared__ u32 base[kMaxExperts];       // first row of the expert's segment
+    __shared__ u16 wcnt[kSortWaves * kMaxExperts];
+    __shared__ u16 step_total[kMaxExperts];
+    __shared__ u32 wave_sum[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int b = blockIdx.x, blocks = gridDim.x;
+
+    for (int g = tid; g < G; g += kSortThreads) total[g] = before[g] = 0u;
+    __syncthreads();
+    const int first = b * chunk;
+    const int last = n - first < chunk ? n : first + chunk;
+    if (hist) {
+        // thread (part, g): the counts of every parts-th block (g fastest: coalesced)
+        int wide = 64;
+        while (wide < G) wide *= 2;
+        const int parts = kSortThreads / wide, g = tid & (wide - 1);
+        if (g < G) {
+            u32 all = 0, mine = 0;
+            for (int o = tid / wide; o < blocks; o += parts) {
+                const u32 c = hist[(u64)o * G + g];
+                all += c;
+                if (o < b) mine += c;
+            }
+            if (all) atomicAdd(&total[g], all);
+            if (mine) atomicAdd(&before[g], mine);
+        }
+    } else {
+        for (int i = first + tid; i < last; i += kSortThreads) {
+            const u32 e = (u32)ids[i];
+            if (e < (u32)G) atomicAdd(&total[e], 1u);
+        }
+    }
+    __syncthreads();
+
+    // first rows: exclusive sum of the segments (one expert a thread: G <= 1024)
+    {
+        const u32 cnt = tid < G ? total[tid] : 0u;
+        u32 seg = 0;
+        if (tid < G) seg = masked_rows > 0 ? (u32)masked_rows : (cnt + kAlign - 1) / kAlign * kAlign;
+        u32 x = seg;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const u32 y = __shfl_up(x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 63) wave_sum[wave] = x;
+        __syncthreads();
+        u32 off = 0;
+        for (int w = 0; w < wave; ++w) off += wave_sum[w];
+        const u32 start = off + x - seg;
+        if (tid < G) {
+            base[tid] = start;
+            if (b == 0) {
+                if (masked_rows > 0) {
+                    group_rows[tid] = (int)(cnt < (u32)masked_rows ? cnt : (u32)masked_rows);
+                } else {
+                    const u32 room = start < (u32)rows ? (u32)rows - start : 0u;
+                    group_rows[tid] = (int)(seg < room ? seg : room);
+                }
+            }
+        }
+    }
+
+    for (int i0 = first; i0 < last; i0 += kSortThreads) {
+        for (int w = tid; w < kSortWaves * G / 2; w += kSortThreads) ((u32*)wcnt)[w] = 0u;   // 16 G counters
+        __syncthreads();
+        const int i = i0 + tid;
+        const u32 e = i < last ? (u32)ids[i] : 0xffffffffu;
+        const bool ok = e < (u32)G;
+        u64 peers = __ballot(ok);
+        for (int bit = 0; bit < bits; ++bit) {
+            const bool one = (e >> bit) & 1u;
+            const u64 m = __ballot(one);
+            peers &= one ? m : ~m;
+        }
+        const u32 rank = __popcll(peers & ((1ull << lane) - 1ull));
+        if (ok && rank == 0) wcnt[wave * G + e] = (u16)__popcll(peers);
+        __syncthreads();
+        for (int g = tid; g < G; g += kSortThreads) {
+            u32 run = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) {
+                const u32 c = wcnt[w * G + g];
+                wcnt[w * G + g] = (u16)run;
+                run += c;
+            }
+            step_total[g] = (u16)run;
+        }
+        __syncthreads();
+        if (i < last) {
+            int row = -1;
+            if (ok) {
+                const u32 r = before[e] + wcnt[wave * G + e] + rank;
+                const u32 at = base[e] + r;
+                if (masked_rows > 0 ? r < (u32)masked_rows : at < (u32)rows) row = (int)at;
+            }
+            pos[i] = row;
+        }
+        __syncthreads();
+        for (int g = tid; g < G; g += kSortThreads) before[g] += step_total[g];
+        // (the next step's first barrier orders these sums before their next reads)
+    }
+
+    if (masked_rows > 0) return;
+    // this block's share of m_indices: the expert whose segment holds the row is
+    // the last one that starts at or before it (empty segments start where the
+    // next one does, and the last of equals is the one that holds rows)
+    __syncthreads();
+    const int share = (rows + blocks - 1) / blocks;
+    const int r0 = b * share < rows ? b * share : rows;
+    const int r1 = rows - r0 < share ? rows : r0 + share;
+    for (int r = r0 + tid; r < r1; r += kSortThreads) {
+        int lo = 0, hi = G - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (base[mid] <= (u32)r) lo = mid;
+            else hi = mid - 1;
+        }
+        const u32 in = (u32)r - base[lo], cnt = total[lo];
+        m_indices[r] = in < cnt ? lo : in < (cnt + kAlign - 1) / kAlign * kAlign ? kPadding : kUnused;
+    }
+}
+
+// ---------------------------------------------------------------- padding rows
+// Wave's share of the padding rows of 128-row block `blk`: `fill(row)` for each
+// row whose index is -1.  Rows past the last segment (-2) are left alone.
+template <typename F>
+__device__ __forceinline__ void for_padding_rows(const int* __restrict__ m_indices, int blk, int rows, F&& fill) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r0 = blk * kAlign + half * 64;
+        const int r = r0 + lane;
+        u64 pad = __ballot(r < rows && m_indices[r] == kPadding);
+        while (pad) {
+            const int at = __builtin_ctzll(pad);
+            pad &= pad - 1;
+            fill(r0 + at);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dispatch
+// One wave a (token, piece of 1024 elements); pieces of a token are
+// neighbours.  Waves past them clear the padding rows, one a (128-row block, piece).
+constexpr int kPiece = 1024;
+
+// BF16.  VEC: rows are 16-byte aligned (H % 8 == 0), a lane moves two groups of
+// 8 elements; otherwise 16 single elements, 64 apart.
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+dg_moe_dispatch_bf16_kernel(const u16* __restrict__ X, const int* __restrict__ pos, const int* __restrict__ m_indices,
+                            u16* __restrict__ out, int T, int k, int rows, int H, int pieces) {
+    const int lane = threadIdx.x & 63;
+    const int unit = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = unit / pieces, c0 = unit % pieces * kPiece;
+    if (t < T) {
+        const u16* src = X + (u64)t * H;
+        if constexpr (VEC) {
+            const int ca = c0 + lane * 8, cb = ca + 512;
+            u32x4 a = {0u, 0u, 0u, 0u}, c = a;
+            if (ca < H) a = *(const u32x4*)(src + ca);
+            if (cb < H) c = *(const u32x4*)(src + cb);
+            for (int j = 0; j < k; ++j) {
+                const int r = pos[(u64)t * k + j];
+                if ((u32)r >= (u32)rows) continue;
+                u16* dst = out + (u64)r * H;
+                if (ca < H) *(u32x4*)(dst + ca) = a;
+                if (cb < H) *(u32x4*)(dst + cb) = c;
+            }
+        } else {
+            u16 v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = c0 + lane + 64 * i < H ? src[c0 + lane + 64 * i] : (u16)0;
+            for (int j = 0; j < k; ++j) {
+                const int r = pos[(u64)t * k + j];
+                if ((u32)r >= (u32)rows) continue;
+                u16* dst = out + (u64)r * H;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c0 + lane + 64 * i < H) dst[c0 + lane + 64 * i] = v[i];
+            }
+        }
+        return;
+    }
+    const int blk = t - T;
+    if (!m_indices || blk >= (rows + kAlign - 1) / kAlign) return;
+    for_padding_rows(m_indices, blk, rows, [&](int r) {
+        u16* dst = out + (u64)r * H;
+        if constexpr (VEC) {
+            const int ca = c0 + lane * 8, cb = ca + 512;
+            if (ca < H) *(u32x4*)(dst + ca) = u32x4{0u, 0u, 0u, 0u};
+            if (cb < H) *(u32x4*)(dst + cb) = u32x4{0u, 0u, 0u, 0u};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c0 + lane + 64 * i < H) dst[c0 + lane + 64 * i] = 0;
+        }
+    });
+}
+
+// E4M3 with one scale per 1x128 block, each token quantised once for its k
+// rows.  A lane holds 16 consecutive elements, eight lanes a block, so a row
+// takes 16-byte stores of 1 KB a wave.  The quotient x / s is the correctly
+// rounded FP32 one (not x times a rounded 1 / s), so the codes are those of the
+// definition.  The largest magnitude is taken over the bit patterns: as unsigned
+// integers the magnitudes order with infinities and NaN on top, so a block that
+// holds one gets a scale that says so.
+// UE8M0: scales are powers of two, four K blocks to a word (sf int32 [H/512][rows]).
+template <bool UE8M0>
+__global__ void __launch_bounds__(256)
+dg_moe_dispatch_fp8_kernel(const u16* __restrict__ X, const int* __restrict__ pos, const int* __restrict__ m_indices,
+                           u8* __restrict__ out, u32* __restrict__ sf, int T, int k, int rows, int group_rows, int H,
+                           int pieces) {
+    const int lane = threadIdx.x & 63;
+    const int unit = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = unit / pieces, c0 = unit % pieces * kPiece;
+    const int c = c0 + lane * 16;
+    const int kb = c >> 7;                              // this lane's 128-wide block
+    const int sf_rows = UE8M0 ? (H + 511) / 512 : H / 128;   // scale entries along K
+    // lanes that write a scale entry, and its index along K
+    const bool scale_lane = (UE8M0 ? (lane & 31) : (lane & 7)) == 0 && c < H;
+    const int sk = UE8M0 ? c >> 9 : kb;
+    // row r's entry sk: sf [group][sk][row in the group]
+    auto sf_at = [&](int r) {
+        const int g = r / group_rows;
+        return ((u64)g * sf_rows + sk) * group_rows + (r - g * group_rows);
+    };
+    if (t < T) {
+        float x[16];
+        u32 top = 0;
+        if (c < H) {
+            const u16* src = X + (u64)t * H + c;
+            const u32x4 a = *(const u32x4*)src, b = *(const u32x4*)(src + 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(a[i]);
+                x[2 * i + 1] = bf16_hi(a[i]);
+                x[8 + 2 * i] = bf16_lo(b[i]);
+                x[9 + 2 * i] = bf16_hi(b[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const u32 m = __builtin_bit_cast(u32, x[i]) & 0x7fffffffu;
+            top = m > top ? m : top;
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) {
+            const u32 y = __shfl_xor(top, d);
+            top = y > top ? y : top;
+        }
+        const float amax = __builtin_bit_cast(float, top);
+        float s = amax / 448.f;
+        if (s < 0x1p-126f) s = 0x1p-126f;               // a subnormal scale would lose bits of the quotient
+        if (top == 0u) s = 1.f;
+        u32 entry;
+        if constexpr (UE8M0) {
+            // the next power of two: exponent field, one more when any mantissa bit is set
+            const u32 sb = __builtin_bit_cast(u32, s);
+            u32 e = (sb >> 23) + ((sb & 0x7fffffu) ? 1u : 0u);
+            if (e > 255u) e = 255u;
+            s = __builtin_bit_cast(float, e == 255u ? 0x7fc00000u : e << 23);
+            // four neighbouring blocks' bytes (8 lanes apart) meet in the lowest lane of 32;
+            // blocks past H count as scale 1
+            if (c >= H) e = 127u;
+            entry = e | (__shfl_down(e, 8) << 8) | (__shfl_down(e, 16) << 16) | (__shfl_down(e, 24) << 24);
+        } else {
+            entry = __builtin_bit_cast(u32, s);
+        }
+        u32x4 q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float y = x[4 * i + j] / s;
+                // clamp without losing a NaN
+                y = y > 448.f ? 448.f : y;
+                y = y < -448.f ? -448.f : y;
+                v[j] = y;
+            }
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+            q[i] = (u32)w;
+        }
+        for (int j = 0; j < k; ++j) {
+            const int r = pos[(u64)t * k + j];
+            if ((u32)r >= (u32)rows) continue;
+            if (c < H) *(u32x4*)(out + (u64)r * H + c) = q;
+            if (scale_lane) sf[sf_at(r)] = entry;
+        }
+        return;
+    }
+    const int blk = t - T;
+    if (!m_indices || blk >= (rows + kAlign - 1) / kAlign) return;
+    for_padding_rows(m_indices, blk, rows, [&](int r) {
+        if (c < H) *(u32x4*)(out + (u64)r * H + c) = u32x4{0u, 0u, 0u, 0u};
+        if (scale_lane) sf[sf_at(r)] = UE8M0 ? 0x7f7f7f7fu : 0x3f800000u;
+    });
+}
+
+// ---------------------------------------------------------------- combine
+// One wave a (token, piece of 512 elements): 8 consecutive elements a lane, the
+// token's rows loaded four at a time and added in j order in FP32.  A dropped
+// assignment (pos outside the rows) is not read at all.
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+dg_moe_combine_kernel(const u16* __restrict__ in, const int* __restrict__ pos, const float* __restrict__ weights,
+                      const u16* __restrict__ residual, u16* __restrict__ Y, int T, int k, int rows, int N, int pieces) {
+    const int lane = threadIdx.x & 63;
+    const int unit = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = unit / pieces;
+    if (t >= T) return;
+    const int c0 = unit % pieces * 512;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    // element i of this lane: 8 neighbours, or 64 apart where rows are not aligned
+    auto col = [&](int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 64 * i; };
+    const bool in_range = col(0) < N;
+    auto load = [&](const u16* p, u32 (&w)[8]) {
+        if constexpr (VEC) {
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (in_range) v = *(const u32x4*)(p + col(0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[2 * i] = v[i] << 16;
+                w[2 * i + 1] = v[i] & 0xffff0000u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = col(i) < N ? (u32)p[col(i)] << 16 : 0u;
+        }
+    };
+    for (int j0 = 0; j0 < k; j0 += 4) {
+        u32 w[4][8];
+        float wt[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const int j = j0 + jj;
+            const int r = j < k ? pos[(u64)t * k + j] : -1;
+            wt[jj] = 0.f;
+            if ((u32)r < (u32)rows) {
+                wt[jj] = weights ? weights[(u64)t * k + j] : 1.f;
+                load(in + (u64)r * N, w[jj]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[jj][i] = 0u;
+            }
+        }
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(wt[jj], __builtin_bit_cast(float, w[jj][i]), acc[i]);
+    }
+    if (residual) {
+        u32 w[8];
+        load(residual + (u64)t * N, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += __builtin_bit_cast(float, w[i]);
+    }
+    u16* dst = Y + (u64)t * N;
+    if constexpr (VEC) {
+        if (in_range)
+            *(u32x4*)(dst + col(0)) = u32x4{to_bf16x2(acc[0], acc[1]), to_bf16x2(acc[2], acc[3]),
+                                            to_bf16x2(acc[4], acc[5]), to_bf16x2(acc[6], acc[7])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col(i) < N) dst[col(i)] = to_bf16(acc[i]);
+    }
+}
+
+// One workgroup a token: its four waves take every fourth 512-element piece,
+// read dY once and each of the token's rows once, write w dY and keep the dot
+// products of up to four rows in registers (a token with more goes round again
+// and finds dY in the cache).  The four waves' partial products are added in
+// wave order.  Workgroups past the tokens clear the padding rows.
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+dg_moe_combine_backward_kernel(const u16* __restrict__ dY, const u16* __restrict__ in, const int* __restrict__ pos,
+                               const float* __restrict__ weights, const int* __restrict__ m_indices,
+                               u16* __restrict__ d_in, float* __restrict__ d_weights, int T, int k, int rows, int N) {
+    __shared__ float part[4][4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x;
+    auto col = [&](int c0, int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 64 * i; };
+    auto load = [&](const u16* p, int c0, float (&v)[8]) {
+        if constexpr (VEC) {
+            u32x4 w = {0u, 0u, 0u, 0u};
+            if (col(c0, 0) < N) w = *(const u32x4*)(p + col(c0, 0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_lo(w[i]);
+                v[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = col(c0, i) < N ? __builtin_bit_cast(float, (u32)p[col(c0, i)] << 16) : 0.f;
+        }
+    };
+    auto store = [&](u16* p, int c0, const float (&v)[8]) {
+        if constexpr (VEC) {
+            if (col(c0, 0) < N)
+                *(u32x4*)(p + col(c0, 0)) = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                                                  to_bf16x2(v[6], v[7])};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col(c0, i) < N) p[col(c0, i)] = to_bf16(v[i]);
+        }
+    };
+    if (t >= T) {
+        const int blk = t - T;
+        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for_padding_rows(m_indices, blk, rows, [&](int r) {
+            for (int c0 = wave * 512; c0 < N; c0 += 2048) store(d_in + (u64)r * N, c0, zero);
+        });
+        return;
+    }
+    for (int j0 = 0; j0 < k; j0 += 4) {
+        int r[4];
+        float w[4], dot[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const int at = j0 + jj < k ? pos[(u64)t * k + j0 + jj] : -1;
+            r[jj] = (u32)at < (u32)rows ? at : -1;
+            w[jj] = r[jj] < 0 ? 0.f : weights ? weights[(u64)t * k + j0 + jj] : 1.f;
+            dot[jj] = 0.f;
+        }
+        for (int c0 = wave * 512; c0 < N; c0 += 2048) {
+            float g[8];
+            load(dY + (u64)t * N, c0, g);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                if (r[jj] < 0) continue;
+                float v[8];
+                if (d_weights) {
+                    load(in + (u64)r[jj] * N, c0, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[jj] = __builtin_fmaf(g[i], v[i], dot[jj]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = w[jj] * g[i];
+                store(d_in + (u64)r[jj] * N, c0, v);
+            }
+        }
+        if (!d_weights) continue;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+            for (int d = 32; d > 0; d /= 2) dot[jj] += __shfl_xor(dot[jj], d);
+            if (lane == 0) part[wave][jj] = dot[jj];
+        }
+        __syncthreads();
+        if (threadIdx.x < 4 && j0 + (int)threadIdx.x < k) {
+            const int jj = threadIdx.x;
+            d_weights[(u64)t * k + j0 + jj] = part[0][jj] + part[1][jj] + part[2][jj] + part[3][jj];
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+dg_status launched(const char* what) {
+    hipError_t e = hipGetLastError();
+    return e == hipSuccess ? DG_OK : set_error(DG_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+dg_status check_sort(const void* ids, const void* pos, const void* groups, int T, int topk, int G) {
+    // an array of no elements may be NULL (so it is for torch's empty tensors)
+    if ((T != 0 && (!ids || !pos)) || !groups) return set_error(DG_ERR_INVALID_ARG, "moe_sort: NULL pointer");
+    if (T < 0 || topk <= 0 || G <= 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: sizes must be positive (T may be 0)");
+    if (G > kMaxExperts) return set_error(DG_ERR_UNSUPPORTED, "moe_sort: at most 1024 experts");
+    if ((int64_t)T * topk > (1 << 30)) return set_error(DG_ERR_UNSUPPORTED, "moe_sort: more than 2^30 assignments");
+    if (!aligned(ids, 4) || !aligned(pos, 4) || !aligned(groups, 4))
+        return set_error(DG_ERR_ALIGNMENT, "moe_sort: arrays must be 4-byte aligned");
+    return DG_OK;
+}
+
+dg_status sort(const int32_t* ids, int32_t* pos, int32_t* m_indices, int32_t* group_rows, int T, int topk, int G,
+               int masked_rows, int rows, void* stream_ptr) {
+    const hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+    const int n = T * topk;
+    int bits = 0;
+    while ((1 << bits) < G) ++bits;
+    // One block up to two steps of 1024 ids (one launch); otherwise blocks of whole
+    // steps, counted by a launch of their own.
+    int chunk = 2 * kSortThreads, blocks = 1;
+    u32* hist = nullptr;
+    if (n > chunk) {
+        const int steps = (n + kSortThreads - 1) / kSortThreads;
+        chunk = (steps + kSortBlocks - 1) / kSortBlocks * kSortThreads;
+        blocks = (n + chunk - 1) / chunk;
+        float* ws = nullptr;
+        dg_status s = stream_scratch(stream_ptr, (size_t)blocks * G * sizeof(u32), &ws);
+        if (s != DG_OK) return s;
+        hist = reinterpret_cast<u32*>(ws);
+        hipLaunchKernelGGL(dg_moe_count_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n, G, chunk, hist);
+        s = launched("moe_sort (count)");
+        if (s != DG_OK) return s;
+    }
+    hipLaunchKernelGGL(dg_moe_place_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n, G, bits, chunk, hist,
+                       masked_rows, rows, pos, m_indices, group_rows);
+    return launched("moe_sort (place)");
+}
+
+// the arguments dispatch, combine and combine backward share
+dg_status check_rows(const char* what, const void* x, const void* pos, const void* rows_ptr, int T, int topk, int rows,
+                     int width) {
+    // arrays of no elements may be NULL
+    if ((T != 0 && (!x || !pos)) || (rows != 0 && !rows_ptr))
+        return set_error(DG_ERR_INVALID_ARG, std::string(what) + ": NULL pointer");
+    if (T < 0 || topk <= 0 || rows < 0 || width <= 0)
+        return set_error(DG_ERR_INVALID_ARG, std::string(what) + ": sizes must be positive (T and rows may be 0)");
+    if (!aligned(x, 16) || !aligned(rows_ptr, 16))
+        return set_error(DG_ERR_ALIGNMENT, std::string(what) + ": token and row arrays must be 16-byte aligned");
+    if (!aligned(pos, 4)) return set_error(DG_ERR_ALIGNMENT, std::string(what) + ": pos must be 4-byte aligned");
+    return DG_OK;
+}
+
+// workgroups of four one-wave units (the kernels count units in 32 bits); 0: too many
+unsigned grid_of(int64_t units) { return units <= INT_MAX - 3 ? (unsigned)((units + 3) / 4) : 0u; }
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+int64_t dg_moe_sorted_rows(int T, int topk, int num_experts) {
+    if (T < 0 || topk <= 0 || num_experts <= 0) return -1;
+    const int64_t n = (int64_t)T * topk;
+    const int64_t used = n < num_experts ? n : num_experts;
+    return (n + used * (kAlign - 1) + kAlign - 1) / kAlign * kAlign;
+}
+
+dg_status dg_moe_sort_contiguous(const int32_t* expert_ids, int32_t* pos, int32_t* m_indices, int32_t* ks, int T,
+                                 int topk, int num_experts, int rows, void* stream) {
+    dg_status s = check_sort(expert_ids, pos, ks, T, topk, num_experts);
+    if (s != DG_OK) return s;
+    if (rows != 0 && !m_indices) return set_error(DG_ERR_INVALID_ARG, "moe_sort: NULL pointer");
+    if (!aligned(m_indices, 4)) return set_error(DG_ERR_ALIGNMENT, "moe_sort: arrays must be 4-byte aligned");
+    if (rows < 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: rows must not be negative");
+    if (rows % kAlign) return set_error(DG_ERR_ALIGNMENT, "moe_sort: rows must be a multiple of the M alignment (128)");
+    return sort(expert_ids, pos, m_indices, ks, T, topk, num_experts, 0, rows, stream);
+}
+
+dg_status dg_moe_sort_masked(const int32_t* expert_ids, int32_t* pos, int32_t* masked_m, int T, int topk,
+                             int num_experts, int M_max, void* stream) {
+    dg_status s = check_sort(expert_ids, pos, masked_m, T, topk, num_experts);
+    if (s != DG_OK) return s;
+    if (M_max <= 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: M_max must be positive");
+    if ((int64_t)M_max * num_experts > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_sort: more than 2^31 rows");
+    return sort(expert_ids, pos, nullptr, masked_m, T, topk, num_experts, M_max, M_max * num_experts, stream);
+}
+
+dg_status dg_moe_dispatch_bf16(const void* X, const int32_t* pos, const int32_t* m_indices, void* rows_out, int T,
+                               int topk, int rows, int H, void* stream) {
+    dg_status s = check_rows("moe_dispatch_bf16", X, pos, rows_out, T, topk, rows, H);
+    if (s != DG_OK) return s;
+    if (m_indices && !aligned(m_indices, 4))
+        return set_error(DG_ERR_ALIGNMENT, "moe_dispatch_bf16: m_indices must be 4-byte aligned");
+    const int pieces = (H + kPiece - 1) / kPiece;
+    const int64_t units = ((int64_t)T + (m_indices ? (rows + kAlign - 1) / kAlign : 0)) * pieces;
+    if (units == 0) return DG_OK;
+    const unsigned grid = grid_of(units);
+    if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_bf16: too many tokens for one launch");
+    hipLaunchKernelGGL(H % 8 == 0 ? dg_moe_dispatch_bf16_kernel<true> : dg_moe_dispatch_bf16_kernel<false>, dim3(grid),
+                       dim3(256), 0, static_cast<hipStream_t>(stream), static_cast<const u16*>(X), pos, m_indices,
+                       static_cast<u16*>(rows_out), T, topk, rows, H, pieces);
+    return launched("moe_dispatch_bf16");
+}
+
+dg_status dg_moe_dispatch_fp8(const void* X, const int32_t* pos, const int32_t* m_indices, void* rows_out, void* sf,
+                              int T, int topk, int rows, int group_rows, int H, int ue8m0, void* stream) {
+    dg_status s = check_rows("moe_dispatch_fp8", X, pos, rows_out, T, topk, rows, H);
+    if (s != DG_OK) return s;
+    if (!sf && rows != 0) return set_error(DG_ERR_INVALID_ARG, "moe_dispatch_fp8: NULL pointer");
+    if (!aligned(sf, 4) || (m_indices && !aligned(m_indices, 4)))
+        return set_error(DG_ERR_ALIGNMENT, "moe_dispatch_fp8: scales and m_indices must be 4-byte aligned");
+    if (H % 128) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: H must be a multiple of 128 (the scale block)");
+    if (rows > 0 && (group_rows <= 0 || rows % group_rows))
+        return set_error(DG_ERR_INVALID_ARG, "moe_dispatch_fp8: rows must be a multiple of group_rows");
+    const int pieces = (H + kPiece - 1) / kPiece;
+    const int64_t units = ((int64_t)T + (m_indices ? (rows + kAlign - 1) / kAlign : 0)) * pieces;
+    if (units == 0 || rows == 0) return DG_OK;
+    const unsigned grid = grid_of(units);
+    if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: too many tokens for one launch");
+    hipLaunchKernelGGL(ue8m0 ? dg_moe_dispatch_fp8_kernel<true> : dg_moe_dispatch_fp8_kernel<false>, dim3(grid),
+                       dim3(256), 0, static_cast<hipStream_t>(stream), static_cast<const u16*>(X), pos, m_indices,
+                       static_cast<u8*>(rows_out), static_cast<u32*>(sf), T, topk, rows, group_rows, H, pieces);
+    return launched("moe_dispatch_fp8");
+}
+
+dg_status dg_moe_combine(const void* rows_in, const int32_t* pos, const float* weights, const void* residual, void* Y,
+                         int T, int topk, int rows, int N, void* stream) {
+    dg_status s = check_rows("moe_combine", Y, pos, rows_in, T, topk, rows, N);
+    if (s != DG_OK) return s;
+    if ((residual && !aligned(residual, 16)) || (weights && !aligned(weights, 4)))
+        return set_error(DG_ERR_ALIGNMENT, "moe_combine: residual must be 16-byte, weights 4-byte aligned");
+    const int pieces = (N + 511) / 512;
+    if (T == 0) return DG_OK;
+    const unsigned grid = grid_of((int64_t)T * pieces);
+    if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_combine: too many tokens for one launch");
+    hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_kernel<true> : dg_moe_combine_kernel<false>, dim3(grid), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), static_cast<const u16*>(rows_in), pos, weights,
+                       static_cast<const u16*>(residual), static_cast<u16*>(Y), T, topk, rows, N, pieces);
+    return launched("moe_combine");
+}
+
+dg_status dg_moe_combine_backward(const void* dY, const void* rows_in, const int32_t* pos, const float* weights,
+                                  const int32_t* m_indices, void* d_rows, float* d_weights, int T, int topk, int rows,
+                                  int N, void* stream) {
+    dg_status s = check_rows("moe_combine_backward", dY, pos, d_rows, T, topk, rows, N);
+    if (s != DG_OK) return s;
+    if (d_weights && !rows_in && rows != 0)
+        return set_error(DG_ERR_INVALID_ARG, "moe_combine_backward: the weights' gradient needs the rows");
+    if ((rows_in && !aligned(rows_in, 16)) || (weights && !aligned(weights, 4)) || (d_weights && !aligned(d_weights, 4)) ||
+        (m_indices && !aligned(m_indices, 4)))
+        return set_error(DG_ERR_ALIGNMENT, "moe_combine_backward: rows must be 16-byte, the other arrays 4-byte aligned");
+    const int64_t blocks = (int64_t)T + (m_indices ? (rows + kAlign - 1) / kAlign : 0);
+    if (blocks == 0) return DG_OK;
+    if (blocks > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_combine_backward: too many tokens for one launch");
+    hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_backward_kernel<true> : dg_moe_combine_backward_kernel<false>,
+                       dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+                       static_cast<const u16*>(dY), static_cast<const u16*>(rows_in), pos, weights, m_indices,
+                       static_cast<u16*>(d_rows), d_weights, T, topk, rows, N);
+    return launched("moe_combine_backward");
+}
+
+}  // extern "C"

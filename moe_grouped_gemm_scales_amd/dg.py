@@ -96,6 +96,16 @@ def _load():
     lib.dg_get_wait_giveups.restype = i32
     lib.dg_reset_wait_giveups.argtypes = []
     lib.dg_reset_wait_giveups.restype = i32
+    lib.dg_moe_sorted_rows.argtypes = [i32] * 3
+    lib.dg_moe_sorted_rows.restype = ctypes.c_int64
+    for name, args in (("dg_moe_sort_contiguous", [vp] * 4 + [i32] * 4 + [vp]),
+                       ("dg_moe_sort_masked", [vp] * 3 + [i32] * 4 + [vp]),
+                       ("dg_moe_dispatch_bf16", [vp] * 4 + [i32] * 4 + [vp]),
+                       ("dg_moe_dispatch_fp8", [vp] * 5 + [i32] * 6 + [vp]),
+                       ("dg_moe_combine", [vp] * 5 + [i32] * 4 + [vp]),
+                       ("dg_moe_combine_backward", [vp] * 7 + [i32] * 4 + [vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i32
     return lib
 
 
@@ -679,3 +689,123 @@ def dg_m_grouped_fp4_fp4_gemm_nt_masked(A, sfa, B, sfb, masked_m, C, D, stream=N
 fp4_fp4_gemm_nt = dg_fp4_fp4_gemm_nt
 m_grouped_fp4_fp4_gemm_nt_contiguous = dg_m_grouped_fp4_fp4_gemm_nt_contiguous
 m_grouped_fp4_fp4_gemm_nt_masked = dg_m_grouped_fp4_fp4_gemm_nt_masked
+
+
+# ---------------------------------------------------------------- tokens to experts and back
+def _typed(t: torch.Tensor, name: str, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _dev(t, name)
+
+
+def moe_sorted_rows(T: int, topk: int, num_experts: int) -> int:
+    """Rows of the contiguous layout that hold T tokens' topk assignments whatever experts they choose."""
+    n = int(lib.dg_moe_sorted_rows(T, topk, num_experts))
+    if n < 0:
+        raise ValueError("T must not be negative, topk and num_experts must be positive")
+    return n
+
+
+def _ids(expert_ids, pos):
+    if expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be int32 [T, topk]")
+    _typed(expert_ids, "expert_ids", torch.int32, expert_ids.shape)
+    _typed(pos, "pos", torch.int32, expert_ids.shape)
+    return expert_ids.shape
+
+
+def dg_moe_sort_contiguous(expert_ids, num_experts, pos, m_indices, ks, stream=None):
+    """Sort the assignments expert_ids [T,topk] by expert into the contiguous layout.
+
+    pos [T,topk]: each assignment's row (-1: dropped); m_indices [rows] as the contiguous products take
+    it (-1 padding, -2 past the last segment); ks [num_experts]: segment rows, multiples of 128.
+    """
+    T, k = _ids(expert_ids, pos)
+    _typed(m_indices, "m_indices", torch.int32, (m_indices.numel(),))
+    _typed(ks, "ks", torch.int32, (num_experts,))
+    _check(lib.dg_moe_sort_contiguous(_ptr(expert_ids), _ptr(pos), _ptr(m_indices), _ptr(ks), T, k, num_experts,
+                                      m_indices.numel(), _stream(stream)))
+    return pos
+
+
+def dg_moe_sort_masked(expert_ids, num_experts, M_max, pos, masked_m, stream=None):
+    """Sort the assignments by expert into the masked layout: expert g's rows start at g * M_max."""
+    T, k = _ids(expert_ids, pos)
+    _typed(masked_m, "masked_m", torch.int32, (num_experts,))
+    _check(lib.dg_moe_sort_masked(_ptr(expert_ids), _ptr(pos), _ptr(masked_m), T, k, num_experts, M_max,
+                                  _stream(stream)))
+    return pos
+
+
+def _token_rows(X, name, pos, rows, m_indices):
+    """Shapes of a token tensor X [T,width], pos [T,topk] and rows [R,width] or [G,M_max,width]."""
+    if X.dim() != 2 or pos.dim() != 2 or rows.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [T, width], pos [T, topk], rows [R, width] or [G, M_max, width]")
+    T, width = X.shape
+    _typed(X, name, torch.bfloat16, (T, width))
+    _typed(pos, "pos", torch.int32, (T, pos.shape[1]))
+    if rows.shape[-1] != width:
+        raise ValueError(f"rows must be {width} wide like {name}, got {tuple(rows.shape)}")
+    n = rows.numel() // width
+    if m_indices is not None:
+        _typed(m_indices, "m_indices", torch.int32, (n,))
+    return T, pos.shape[1], n, width
+
+
+def dg_moe_dispatch_bf16(X, pos, m_indices, rows, stream=None):
+    """rows[pos[t,j]] = X[t]; contiguous layout (m_indices given): padding rows are cleared."""
+    T, k, n, H = _token_rows(X, "X", pos, rows, m_indices)
+    _typed(rows, "rows", torch.bfloat16, rows.shape)
+    _check(lib.dg_moe_dispatch_bf16(_ptr(X), _ptr(pos), _ptr(m_indices), _ptr(rows), T, k, n, H, _stream(stream)))
+    return rows
+
+
+def dg_moe_dispatch_fp8(X, pos, m_indices, rows, sf, stream=None):
+    """rows[pos[t,j]] = E4M3(X[t] / s), one scale per 1x128 block.
+
+    sf: float32 [H/128, R] (rows [R,H]) or [G, H/128, M_max] (rows [G,M_max,H]); int32 words of packed UE8M0
+    scales in the same place ([ceil(H/512), R], [G, ceil(H/512), M_max]) select power-of-two scales.
+    """
+    T, k, n, H = _token_rows(X, "X", pos, rows, m_indices)
+    _fp8(rows, "rows")
+    ue8m0 = sf.dtype == torch.int32
+    kb = _cdiv(H, 512) if ue8m0 else H // 128
+    _typed(sf, "sf", torch.int32 if ue8m0 else torch.float32, (*rows.shape[:-2], kb, rows.shape[-2]))
+    _check(lib.dg_moe_dispatch_fp8(_ptr(X), _ptr(pos), _ptr(m_indices), _ptr(rows), _ptr(sf), T, k, n,
+                                   rows.shape[-2], H, int(ue8m0), _stream(stream)))
+    return rows
+
+
+def dg_moe_combine(rows, pos, weights, residual, Y, stream=None):
+    """Y[t] = residual[t] + sum_j weights[t,j] * rows[pos[t,j]] (weights, residual may be None: 1, none)."""
+    T, k, n, N = _token_rows(Y, "Y", pos, rows, None)
+    _typed(rows, "rows", torch.bfloat16, rows.shape)
+    if weights is not None:
+        _typed(weights, "weights", torch.float32, (T, k))
+    if residual is not None:
+        _typed(residual, "residual", torch.bfloat16, (T, N))
+    _check(lib.dg_moe_combine(_ptr(rows), _ptr(pos), _ptr(weights), _ptr(residual), _ptr(Y), T, k, n, N,
+                              _stream(stream)))
+    return Y
+
+
+def dg_moe_combine_backward(dY, rows, pos, weights, m_indices, d_rows, d_weights, stream=None):
+    """d_rows[pos[t,j]] = weights[t,j] * dY[t]; d_weights[t,j] = <dY[t], rows[pos[t,j]]>.
+
+    d_weights None: not computed (rows may be None).  Padding rows of the contiguous layout are cleared.
+    """
+    T, k, n, N = _token_rows(dY, "dY", pos, d_rows, m_indices)
+    _typed(d_rows, "d_rows", torch.bfloat16, d_rows.shape)
+    if rows is not None:
+        _typed(rows, "rows", torch.bfloat16, d_rows.shape)
+    elif d_weights is not None:
+        raise ValueError("d_weights needs rows")
+    if weights is not None:
+        _typed(weights, "weights", torch.float32, (T, k))
+    if d_weights is not None:
+        _typed(d_weights, "d_weights", torch.float32, (T, k))
+    _check(lib.dg_moe_combine_backward(_ptr(dY), _ptr(rows), _ptr(pos), _ptr(weights), _ptr(m_indices), _ptr(d_rows),
+                                       _ptr(d_weights), T, k, n, N, _stream(stream)))
+    return d_rows
