@@ -320,6 +320,89 @@ dg_status dg_m_grouped_fp4_fp4_gemm_nt_masked(const void *A, const int32_t *sfa,
                                               int num_groups, void *stream);
 
 /*
+ * The BF16 and FP8 (FP32-scale) forms with a fused epilogue:
+ *
+ *     Z = A . B^T + bias,   D = activation(Z) + residual
+ *
+ * in FP32 from the accumulator on, each output rounded once to BF16.  Every
+ * part is optional:
+ *   bias      one value per column, [N] (grouped forms [G][N]: each expert its
+ *             own), FP32 or BF16 (bias_type)
+ *   activation  relu; silu z / (1 + e^-z); gelu z Phi(z) (erf form); gelu_tanh
+ *             z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *   residual  BF16, laid out like D (it may be D itself)
+ *   Z         BF16, laid out like D: the pre-activation, kept for the backward pass
+ * bias, residual and Z must be 16-byte aligned.  Rows that a grouped form does
+ * not compute are untouched in D and Z alike.  Everything else (layouts, groups,
+ * masks, checks, streams) is as for the form without `_epilogue`.
+ */
+typedef enum { DG_TYPE_F32 = 0, DG_TYPE_BF16 = 1 } dg_type;
+typedef enum { DG_ACT_NONE = 0, DG_ACT_RELU = 1, DG_ACT_SILU = 2, DG_ACT_GELU = 3, DG_ACT_GELU_TANH = 4 } dg_activation;
+typedef struct {
+    const void *bias;       /* or NULL */
+    int bias_type;          /* dg_type */
+    int activation;         /* dg_activation */
+    const void *residual;   /* or NULL */
+    void *Z;                /* or NULL */
+} dg_epilogue;
+dg_status dg_bf16_gemm_nt_epilogue(const void *A, const void *B, const dg_epilogue *epilogue, void *D, int M, int N,
+                                   int K, void *stream);
+dg_status dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(const void *A, const void *B, const int32_t *m_indices,
+                                                        const dg_epilogue *epilogue, void *D, int M, int N, int K,
+                                                        int num_groups, void *stream);
+dg_status dg_m_grouped_bf16_gemm_nt_masked_epilogue(const void *A, const void *B, const int32_t *masked_m,
+                                                    const dg_epilogue *epilogue, void *D, int M_max, int N, int K,
+                                                    int num_groups, void *stream);
+dg_status dg_fp8_gemm_nt_epilogue(const void *A, const float *sfa, const void *B, const float *sfb,
+                                  const dg_epilogue *epilogue, void *D, int M, int N, int K, void *stream);
+dg_status dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(const void *A, const float *sfa, const void *B, const float *sfb,
+                                                       const int32_t *m_indices, const dg_epilogue *epilogue, void *D,
+                                                       int M, int N, int K, int num_groups, void *stream);
+dg_status dg_m_grouped_fp8_gemm_nt_masked_epilogue(const void *A, const float *sfa, const void *B, const float *sfb,
+                                                   const int32_t *masked_m, const dg_epilogue *epilogue, void *D,
+                                                   int M_max, int N, int K, int num_groups, void *stream);
+
+/*
+ * Backward pass of the fused epilogue.  With dD the gradient of D [M][N] and Z
+ * as the forward call stored it:
+ *   dZ = dD * activation'(Z)             BF16 [M][N] (the one rounding; may be dD itself, or NULL)
+ *   dbias[n] = sum over rows of dZ       FP32 [N] (grouped [G][N]; 0 for an expert without rows), or
+ *                                        NULL; summed before dZ is rounded, in an order that does
+ *                                        not change from run to run
+ * Z may be NULL without an activation.  The residual's gradient is dD itself.
+ * Contiguous: m_indices as for the forward call; dZ of padding rows (-1) is
+ * cleared, as the weight gradient over whole segments needs, other rows that
+ * name no expert are untouched.  Then, with A and B as in the forward call,
+ *   dA = dZ . B        dg_bf16_gemm_nn            dg_m_grouped_bf16_gemm_nn_contiguous
+ *   dB = dZ^T . A      dg_bf16_gemm_tn            dg_k_grouped_bf16_gemm_tn_contiguous
+ * The partial sums of dbias use the stream's workspace.
+ */
+dg_status dg_epilogue_backward(const void *dD, const void *Z, int activation, void *dZ, float *dbias, int M, int N,
+                               void *stream);
+dg_status dg_m_grouped_epilogue_backward_contiguous(const void *dD, const void *Z, int activation,
+                                                    const int32_t *m_indices, void *dZ, float *dbias, int M, int N,
+                                                    int num_groups, void *stream);
+
+/*
+ * BF16 products of the other storage layouts, D = C + (logical) A . B^T as for
+ * the FP8 calls of the same letters, C float or NULL, D BF16:
+ *   nn  A [M][K], B [K][N] (grouped [G][K][N]); K a multiple of 64
+ *   tn  A [K][M], B [K][N]; any K, 0 included (D = C, or zeros)
+ *   k_grouped tn  A [K][M], B [K][N], ks int32 [G] (device): consecutive K
+ *       segments of the groups, multiples of 128, as for the FP8 form; C, D
+ *       [G][M][N], an empty group gets C or zeros; K a multiple of 128
+ * Operands stored K-outermost are first rewritten K-contiguous into the
+ * stream's workspace: G * N * K * 2 bytes for nn, (M + N) * ceil(K/512) * 1024
+ * for tn.
+ */
+dg_status dg_bf16_gemm_nn(const void *A, const void *B, const float *C, void *D, int M, int N, int K, void *stream);
+dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void *A, const void *B, const int32_t *m_indices, const float *C,
+                                               void *D, int M, int N, int K, int num_groups, void *stream);
+dg_status dg_bf16_gemm_tn(const void *A, const void *B, const float *C, void *D, int M, int N, int K, void *stream);
+dg_status dg_k_grouped_bf16_gemm_tn_contiguous(const void *A, const void *B, const int32_t *ks, const float *C, void *D,
+                                               int M, int N, int K, int num_groups, void *stream);
+
+/*
  * Tokens to experts and back: the steps between a router's choice of topk
  * experts a token and the grouped products above, and from their rows back to
  * the tokens.  BF16 token states X, Y [T][width]; a router's expert_ids int32
@@ -428,14 +511,20 @@ dg_status dg_init(void);
 #define DG_BF16 16           /* BF16 x BF16 without scales (K in elements) */
 #define DG_SCALE_FP4_FP4 32  /* FP4 x FP4 */
 #define DG_SCALE_UE8M0_I16 64   /* UE8M0 pairs in 16-bit words, MN-major */
+/* ... and for the parts of a fused epilogue (DG_EPI_ACT takes a dg_activation) */
+#define DG_EPI_BIAS_F32 0x100
+#define DG_EPI_BIAS_BF16 0x200
+#define DG_EPI_RESIDUAL 0x400
+#define DG_EPI_Z 0x800
+#define DG_EPI_ACT(a) ((a) << 12)
 
 /*
  * Compile (or load from the cache) the kernel(s) that a later call with these
  * arguments would use, without launching anything.  kind: 0 dense,
  * 1 contiguous, 2 masked, 3 K-grouped (K = the K rows; the FP32 scale form
- * only) (| DG_SCALE_UE8M0 for packed UE8M0 scales, | DG_SCALE_UE8M0_I16 for
+ * or BF16) (| DG_SCALE_UE8M0 for packed UE8M0 scales, | DG_SCALE_UE8M0_I16 for
  * UE8M0 pairs in 16-bit words, | DG_SCALE_FP8_FP4 for FP8 x FP4, | DG_BF16,
- * | DG_SCALE_FP4_FP4); has_c:
+ * | DG_SCALE_FP4_FP4, | DG_EPI_* for a fused epilogue); has_c:
  * 0/1; rows = M (dense/contiguous) or M_max.
  * Needs no GPU: the code object is built for gfx950 and stored in the cache
  * directory (DG_CACHE_DIR, else <library dir>/jit_cache).

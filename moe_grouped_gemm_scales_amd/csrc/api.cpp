@@ -44,6 +44,13 @@ struct LaunchParams {
 static_assert(sizeof(LaunchParams) == 96 && offsetof(LaunchParams, M) == 72 && offsetof(LaunchParams, status) == 88,
               "the kernel reads this layout");
 
+// With a fused epilogue the argument goes on with its tensors.
+struct LaunchParamsEpilogue {
+    LaunchParams lp;
+    EpilogueArgs ep;
+};
+static_assert(sizeof(LaunchParamsEpilogue) == 120 && offsetof(LaunchParamsEpilogue, ep) == 96, "the kernel reads this layout");
+
 struct Workspace {
     float* partials = nullptr;
     size_t partial_bytes = 0;
@@ -70,7 +77,7 @@ struct Plan {
     hipFunction_t transpose = nullptr;   // K-grouped: the K-contiguous rewrite of the operands
 };
 
-using PlanKey = std::tuple<int, int, int, int, int, int, int, int, std::string>;
+using PlanKey = std::tuple<int, int, int, int, int, int, int, int, int, std::string>;
 
 struct DeviceState {
     int num_cus = 0;
@@ -90,7 +97,7 @@ std::atomic<int> g_num_cus_limit{0};   // 0: use the device's count
 // nodes that are never erased, and workspaces a call outgrows are retired, not
 // freed, so the pointers stay valid.
 struct WarmCall {
-    int kind = -1, rows = 0, n = 0, k = 0, g = 0, has_c = 0, sf = 0, dev = -1, limit = 0;
+    int kind = -1, rows = 0, n = 0, k = 0, g = 0, has_c = 0, sf = 0, ep = 0, dev = -1, limit = 0;
     uint64_t env = 0;
     hipStream_t stream = nullptr;
     const Plan* plan = nullptr;
@@ -112,11 +119,13 @@ uint64_t fnv1a_str(const char* s, uint64_t h) {
 // its arrival counters at zero).
 dg_status launch_segments(const Plan& plan, const Problem& p, const void* A, const void* sfa, const void* B,
                           const void* sfb, const int32_t* grp, const float* C, void* D, hipStream_t stream,
-                          float* partials, uint32_t* counters, unsigned int* status) {
+                          float* partials, uint32_t* counters, unsigned int* status, const EpilogueArgs& ep) {
     for (const Segment& seg : plan.segs) {
         const KernelConfig& cfg = seg.cfg;
         if (seg.items <= 0) continue;
-        LaunchParams lp{};
+        LaunchParamsEpilogue all{};          // a kernel without epilogue reads the first 96 bytes
+        LaunchParams& lp = all.lp;
+        all.ep = ep;
         lp.A = A; lp.sfa = sfa; lp.B = B; lp.sfb = sfb; lp.C = C; lp.D = D; lp.grp = grp;
         lp.M = p.rows;
         lp.num_tiles = (int)seg.items;
@@ -126,7 +135,7 @@ dg_status launch_segments(const Plan& plan, const Problem& p, const void* A, con
             lp.ws = partials;
             lp.counters = counters;
         }
-        void* args[] = {&lp};
+        void* args[] = {&all};
         hipError_t e = hipModuleLaunchKernel(seg.fn, seg.grid, 1, 1, cfg.threads(), 1, 1, 0, stream, args, nullptr);
         if (e != hipSuccess) return hip_fail(e, "hipModuleLaunchKernel");
     }
@@ -239,7 +248,8 @@ dg_status check_common(const void* A, const void* sfa, const void* B, const void
 // load), split-K partials and counters go to the library's static scratch array
 // instead of the stream's workspace, and nothing is allocated.
 dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B, const void* sfb,
-                 const int32_t* grp, const float* C, void* D, void* stream_ptr, bool noalloc = false) {
+                 const int32_t* grp, const float* C, void* D, void* stream_ptr, bool noalloc = false,
+                 const EpilogueArgs& ep = {}) {
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     const bool rewrite = p.kind == kKGrouped || p.a_k_outer || p.b_k_outer;
     // ---- warm call: the previous call of this thread had the same key
@@ -250,9 +260,9 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     const int limit = g_num_cus_limit.load(std::memory_order_relaxed);
     WarmCall& w = t_warm;
     if (!noalloc && !rewrite && w.plan && w.kind == p.kind && w.rows == p.rows && w.n == p.n && w.k == p.k &&
-        w.g == p.g && w.has_c == p.has_c && w.sf == p.sf && w.dev == dev_now && w.stream == stream &&
+        w.g == p.g && w.has_c == p.has_c && w.sf == p.sf && w.ep == p.ep.code() && w.dev == dev_now && w.stream == stream &&
         w.env == env && w.limit == limit)
-        return launch_segments(*w.plan, p, A, sfa, B, sfb, grp, C, D, stream, w.partials, w.counters, w.status);
+        return launch_segments(*w.plan, p, A, sfa, B, sfb, grp, C, D, stream, w.partials, w.counters, w.status, ep);
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState* st = nullptr;
     int dev = 0;
@@ -260,7 +270,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     if (s != DG_OK) return s;
     const int cus = effective_cus(*st);
     const char* forced = std::getenv("DG_FORCE_CONFIG");
-    PlanKey key{p.kind, p.rows, p.n, p.k, p.g, p.has_c, p.sf, cus,
+    PlanKey key{p.kind, p.rows, p.n, p.k, p.g, p.has_c, p.sf, p.ep.code(), cus,
                 std::string(forced ? forced : "") + "|" + jit_extra_option()};
     auto it = st->plans.find(key);
     if (noalloc) {
@@ -329,7 +339,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
         }
         it = st->plans.emplace(key, plan).first;
     }
-    if (rewrite && !it->second.transpose) {
+    if (rewrite && p.sf != 3 && !it->second.transpose) {
         void* fptr = nullptr;
         s = get_function(it->second.segs.front().cfg, &fptr, "dg_transpose_k_major");
         if (s != DG_OK) return s;
@@ -338,6 +348,11 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     // rewrite of a K-outermost operand X [groups][rows_k][cols] as [groups][cols][pitch]
     // (one workgroup per 64 x 64 byte block, K blocks fastest; grid.z: groups)
     auto rewrite_k_major = [&](const void* x, void* xt, int rows_k, int cols, int groups) -> dg_status {
+        if (p.sf == 3) {       // BF16: K in elements; K-grouped K is padded with zeros to whole K blocks
+            const bool kg = p.kind == kKGrouped;
+            return transpose_bf16(x, xt, groups, kg ? p.k_rows : rows_k / 2, cols, kg ? p.kt : rows_k / 2, p.k / 2,
+                                  stream_ptr);
+        }
         const uint64_t blocks = (uint64_t)(rows_k / 64) * (uint64_t)((cols + 63) / 64);
         if (blocks >= (1ull << 31) || groups > 65535)
             return set_error(DG_ERR_UNSUPPORTED, "operand too large for the K-contiguous rewrite");
@@ -402,11 +417,11 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
         for (const Segment& seg : it->second.segs)
             std::fprintf(stderr, "[dg] launch %s grid=%d block=%d items=%lld lds=%d\n", seg.cfg.key().c_str(),
                          seg.grid, seg.cfg.threads(), (long long)seg.items, seg.cfg.lds_bytes());
-    s = launch_segments(it->second, p, A, sfa, B, sfb, grp, C, D, stream, partials, counters, st->status);
+    s = launch_segments(it->second, p, A, sfa, B, sfb, grp, C, D, stream, partials, counters, st->status, ep);
     if (s != DG_OK) return s;
     if (!rewrite && !print) {
         WarmCall& r = t_warm;
-        r.kind = p.kind; r.rows = p.rows; r.n = p.n; r.k = p.k; r.g = p.g; r.has_c = p.has_c; r.sf = p.sf;
+        r.kind = p.kind; r.rows = p.rows; r.n = p.n; r.k = p.k; r.g = p.g; r.has_c = p.has_c; r.sf = p.sf; r.ep = p.ep.code();
         r.dev = dev; r.limit = limit; r.env = env; r.stream = stream; r.plan = &it->second;
         r.partials = partials; r.counters = counters; r.status = st->status;
     }
@@ -447,19 +462,21 @@ namespace {
 // The three forms, for each scale format (sf: 0 FP32, 1 packed UE8M0, 2 FP8 x
 // FP4 with E2M1 B; the scale pointers are only passed through to the kernel).
 dg_status dense(const void* A, const void* sfa, const void* B, const void* sfb, const float* C, void* D, int M,
-                int N, int K, int sf, void* stream, int a_k_outer = 0, int b_k_outer = 0) {
+                int N, int K, int sf, void* stream, int a_k_outer = 0, int b_k_outer = 0, const Epilogue& ep = {},
+                const EpilogueArgs& args = {}) {
     dg_status s = check_common(A, sfa, B, sfb, C, D, M, N, K, sf == 5 ? 2 : 4);
     if (s != DG_OK) return s;
     if (M == 0) return DG_OK;
     Problem p{kDense, M, N, K, 1, C ? 1 : 0, sf};
     p.a_k_outer = a_k_outer;
     p.b_k_outer = b_k_outer;
-    return launch(p, A, sfa, B, sfb, nullptr, C, D, stream);
+    p.ep = ep;
+    return launch(p, A, sfa, B, sfb, nullptr, C, D, stream, false, args);
 }
 
 dg_status contiguous(const void* A, const void* sfa, const void* B, const void* sfb, const int32_t* m_indices,
                      const float* C, void* D, int M, int N, int K, int num_groups, int sf, void* stream,
-                     int b_k_outer = 0) {
+                     int b_k_outer = 0, const Epilogue& ep = {}, const EpilogueArgs& args = {}) {
     dg_status s = check_common(A, sfa, B, sfb, C, D, M, N, K, sf == 5 ? 2 : 4);
     if (s != DG_OK) return s;
     if (!m_indices) return set_error(DG_ERR_INVALID_ARG, "m_indices must be non-NULL");
@@ -470,11 +487,13 @@ dg_status contiguous(const void* A, const void* sfa, const void* B, const void* 
     if (M == 0) return DG_OK;
     Problem p{kContiguous, M, N, K, num_groups, C ? 1 : 0, sf};
     p.b_k_outer = b_k_outer;
-    return launch(p, A, sfa, B, sfb, m_indices, C, D, stream);
+    p.ep = ep;
+    return launch(p, A, sfa, B, sfb, m_indices, C, D, stream, false, args);
 }
 
 dg_status masked(const void* A, const void* sfa, const void* B, const void* sfb, const int32_t* masked_m,
-                 const float* C, void* D, int M_max, int N, int K, int num_groups, int sf, void* stream) {
+                 const float* C, void* D, int M_max, int N, int K, int num_groups, int sf, void* stream,
+                 const Epilogue& ep = {}, const EpilogueArgs& args = {}) {
     dg_status s = check_common(A, sfa, B, sfb, C, D, M_max, N, K, sf == 5 ? 2 : 4);
     if (s != DG_OK) return s;
     if (!masked_m) return set_error(DG_ERR_INVALID_ARG, "masked_m must be non-NULL");
@@ -482,12 +501,31 @@ dg_status masked(const void* A, const void* sfa, const void* B, const void* sfb,
     if (!aligned(masked_m, 4)) return set_error(DG_ERR_ALIGNMENT, "masked_m must be 4-byte aligned");
     if (M_max == 0) return DG_OK;
     Problem p{kMasked, M_max, N, K, num_groups, C ? 1 : 0, sf};
-    return launch(p, A, sfa, B, sfb, masked_m, C, D, stream);
+    p.ep = ep;
+    return launch(p, A, sfa, B, sfb, masked_m, C, D, stream, false, args);
+}
+
+// Checks a caller's epilogue and splits it into the kernel's switches and its tensors.
+dg_status read_epilogue(const dg_epilogue* e, Epilogue* ep, EpilogueArgs* args) {
+    if (!e) return set_error(DG_ERR_INVALID_ARG, "epilogue must be non-NULL");
+    if (e->bias && e->bias_type != DG_TYPE_F32 && e->bias_type != DG_TYPE_BF16)
+        return set_error(DG_ERR_INVALID_ARG, "epilogue: bias_type must be DG_TYPE_F32 or DG_TYPE_BF16");
+    if (e->activation < DG_ACT_NONE || e->activation > DG_ACT_GELU_TANH)
+        return set_error(DG_ERR_INVALID_ARG, "epilogue: unknown activation");
+    if (!aligned(e->bias, 16) || !aligned(e->residual, 16) || !aligned(e->Z, 16))
+        return set_error(DG_ERR_ALIGNMENT, "epilogue: bias, residual and Z must be 16-byte aligned");
+    ep->bias = e->bias ? 1 + e->bias_type : 0;
+    ep->act = e->activation;
+    ep->res = e->residual ? 1 : 0;
+    ep->zout = e->Z ? 1 : 0;
+    *args = EpilogueArgs{e->bias, e->residual, e->Z};
+    return DG_OK;
 }
 
 // BF16 x BF16, the three M forms: no scales; the kernels count K in bytes
 dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, const float* C, void* D, int rows,
-                    int N, int K, int num_groups, void* stream) {
+                    int N, int K, int num_groups, void* stream, int b_k_outer = 0, const Epilogue& ep = {},
+                    const EpilogueArgs& args = {}) {
     if (!A || !B || !D) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
     if (rows < 0 || N <= 0 || K <= 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M may be 0)");
     if (K % 64 != 0) return set_error(DG_ERR_UNSUPPORTED, "BF16: K must be a multiple of 64 (one 128-byte block)");
@@ -503,7 +541,25 @@ dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, 
         return set_error(DG_ERR_ALIGNMENT, "contiguous M must be a multiple of the M alignment (128)");
     if (rows == 0) return DG_OK;
     Problem p{kind, rows, N, 2 * K, kind == kDense ? 1 : num_groups, C ? 1 : 0, 3};
-    return launch(p, A, nullptr, B, nullptr, grp, C, D, stream);
+    p.b_k_outer = b_k_outer;
+    p.ep = ep;
+    return launch(p, A, nullptr, B, nullptr, grp, C, D, stream, false, args);
+}
+
+// BF16 TN (A [K][M], B [K][N]): K-grouped, or one group of any K (ks NULL)
+dg_status bf16_gemm_tn(const void* A, const void* B, const int32_t* ks, const float* C, void* D, int M, int N, int K,
+                       int num_groups, void* stream) {
+    if ((K != 0 && (!A || !B)) || !D) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
+    if (M < 0 || N <= 0 || K < 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M and K may be 0)");
+    if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || (C && !aligned(C, 16)))
+        return set_error(DG_ERR_ALIGNMENT, "A, B, C and D must be 16-byte aligned");
+    const int64_t pitch = ((int64_t)2 * K + 1023) / 1024 * 1024;
+    if ((uint64_t)pitch * 256u >= (1ull << 32)) return set_error(DG_ERR_UNSUPPORTED, "sizes exceed 32-bit buffer offsets");
+    if (M == 0) return DG_OK;
+    Problem p{kKGrouped, M, N, (int)std::max<int64_t>(pitch, 1024), num_groups, C ? 1 : 0, 3};
+    p.k_rows = K;
+    p.kt = (K + 63) / 64 * 64;
+    return launch(p, A, nullptr, B, nullptr, ks, C, D, stream);
 }
 
 dg_status k_grouped(const void* A, const float* sfa, const void* B, const float* sfb, const int32_t* ks,
@@ -587,18 +643,31 @@ int scale_format(int* kind) {
     return sf;
 }
 
+// Epilogue encoded in `kind` by the DG_EPI_* flags
+Epilogue epilogue_flags(int* kind) {
+    Epilogue ep;
+    ep.bias = (*kind & DG_EPI_BIAS_BF16) ? 2 : (*kind & DG_EPI_BIAS_F32) ? 1 : 0;
+    ep.res = (*kind & DG_EPI_RESIDUAL) ? 1 : 0;
+    ep.zout = (*kind & DG_EPI_Z) ? 1 : 0;
+    ep.act = (*kind >> 12) & 7;
+    *kind &= ~(DG_EPI_BIAS_F32 | DG_EPI_BIAS_BF16 | DG_EPI_RESIDUAL | DG_EPI_Z | DG_EPI_ACT(7));
+    return ep;
+}
+
 // the kernels' K: BF16 rows are counted in bytes; K-grouped operands use the padded pitch
 int kernel_k(int kind, int sf, int K) {
-    if (sf == 3) return 2 * K;
+    if (sf == 3) return kind == kKGrouped ? k_grouped_pitch(2 * K) : 2 * K;
     return kind == kKGrouped ? k_grouped_pitch(K) : K;
 }
 
 dg_status dg_precompile(int kind, int rows, int N, int K, int num_groups, int has_c, int num_cus) {
+    const Epilogue ep = epilogue_flags(&kind);
     const int sf = scale_format(&kind);
-    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0)
+    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH)
         return set_error(DG_ERR_INVALID_ARG, "dg_precompile: bad arguments");
-    if (K % (sf == 3 ? 64 : 128)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
+    if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
     Problem p{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
+    p.ep = ep;
     for (const KernelConfig& cfg : select_plan(p, num_cus > 0 ? num_cus : 256)) {
         std::vector<char> code;
         dg_status s = compile_code(cfg, &code);
@@ -609,10 +678,12 @@ dg_status dg_precompile(int kind, int rows, int N, int K, int num_groups, int ha
 
 dg_status dg_describe_config(int kind, int rows, int N, int K, int num_groups, int has_c, int num_cus, char* buf,
                              int len) {
+    const Epilogue ep = epilogue_flags(&kind);
     const int sf = scale_format(&kind);
-    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || !buf || len <= 0)
+    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH || !buf ||
+        len <= 0)
         return set_error(DG_ERR_INVALID_ARG, "dg_describe_config: bad arguments");
-    if (K % (sf == 3 ? 64 : 128)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
+    if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
     int cus = num_cus;
     if (cus <= 0) {
         std::lock_guard<std::mutex> lock(g_mu);
@@ -623,6 +694,7 @@ dg_status dg_describe_config(int kind, int rows, int N, int K, int num_groups, i
         cus = effective_cus(*st);
     }
     Problem p{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
+    p.ep = ep;
     std::string key;
     for (const KernelConfig& c : select_plan(p, cus)) key += (key.empty() ? "" : "+") + c.key();
     std::snprintf(buf, (size_t)len, "%s", key.c_str());
@@ -764,6 +836,82 @@ dg_status dg_m_grouped_fp4_fp4_gemm_nt_masked(const void* A, const int32_t* sfa,
                                               const int32_t* sfb, const int32_t* masked_m, const float* C, void* D,
                                               int M_max, int N, int K, int num_groups, void* stream) {
     return masked(A, sfa, B, sfb, masked_m, C, D, M_max, N, K, num_groups, 4, stream);
+}
+
+// ---- fused epilogue
+dg_status dg_bf16_gemm_nt_epilogue(const void* A, const void* B, const dg_epilogue* epilogue, void* D, int M, int N,
+                                   int K, void* stream) {
+    Epilogue ep;
+    EpilogueArgs args;
+    dg_status s = read_epilogue(epilogue, &ep, &args);
+    return s != DG_OK ? s : bf16_gemm(kDense, A, B, nullptr, nullptr, D, M, N, K, 1, stream, 0, ep, args);
+}
+
+dg_status dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(const void* A, const void* B, const int32_t* m_indices,
+                                                        const dg_epilogue* epilogue, void* D, int M, int N, int K,
+                                                        int num_groups, void* stream) {
+    Epilogue ep;
+    EpilogueArgs args;
+    dg_status s = read_epilogue(epilogue, &ep, &args);
+    return s != DG_OK ? s : bf16_gemm(kContiguous, A, B, m_indices, nullptr, D, M, N, K, num_groups, stream, 0, ep, args);
+}
+
+dg_status dg_m_grouped_bf16_gemm_nt_masked_epilogue(const void* A, const void* B, const int32_t* masked_m,
+                                                    const dg_epilogue* epilogue, void* D, int M_max, int N, int K,
+                                                    int num_groups, void* stream) {
+    Epilogue ep;
+    EpilogueArgs args;
+    dg_status s = read_epilogue(epilogue, &ep, &args);
+    return s != DG_OK ? s : bf16_gemm(kMasked, A, B, masked_m, nullptr, D, M_max, N, K, num_groups, stream, 0, ep, args);
+}
+
+dg_status dg_fp8_gemm_nt_epilogue(const void* A, const float* sfa, const void* B, const float* sfb,
+                                  const dg_epilogue* epilogue, void* D, int M, int N, int K, void* stream) {
+    Epilogue ep;
+    EpilogueArgs args;
+    dg_status s = read_epilogue(epilogue, &ep, &args);
+    return s != DG_OK ? s : dense(A, sfa, B, sfb, nullptr, D, M, N, K, 0, stream, 0, 0, ep, args);
+}
+
+dg_status dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(const void* A, const float* sfa, const void* B, const float* sfb,
+                                                       const int32_t* m_indices, const dg_epilogue* epilogue, void* D,
+                                                       int M, int N, int K, int num_groups, void* stream) {
+    Epilogue ep;
+    EpilogueArgs args;
+    dg_status s = read_epilogue(epilogue, &ep, &args);
+    return s != DG_OK ? s : contiguous(A, sfa, B, sfb, m_indices, nullptr, D, M, N, K, num_groups, 0, stream, 0, ep, args);
+}
+
+dg_status dg_m_grouped_fp8_gemm_nt_masked_epilogue(const void* A, const float* sfa, const void* B, const float* sfb,
+                                                   const int32_t* masked_m, const dg_epilogue* epilogue, void* D,
+                                                   int M_max, int N, int K, int num_groups, void* stream) {
+    Epilogue ep;
+    EpilogueArgs args;
+    dg_status s = read_epilogue(epilogue, &ep, &args);
+    return s != DG_OK ? s : masked(A, sfa, B, sfb, masked_m, nullptr, D, M_max, N, K, num_groups, 0, stream, ep, args);
+}
+
+// ---- BF16 products of the backward pass
+dg_status dg_bf16_gemm_nn(const void* A, const void* B, const float* C, void* D, int M, int N, int K, void* stream) {
+    return bf16_gemm(kDense, A, B, nullptr, C, D, M, N, K, 1, stream, 1);
+}
+
+dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void* A, const void* B, const int32_t* m_indices, const float* C,
+                                               void* D, int M, int N, int K, int num_groups, void* stream) {
+    return bf16_gemm(kContiguous, A, B, m_indices, C, D, M, N, K, num_groups, stream, 1);
+}
+
+dg_status dg_bf16_gemm_tn(const void* A, const void* B, const float* C, void* D, int M, int N, int K, void* stream) {
+    return bf16_gemm_tn(A, B, nullptr, C, D, M, N, K, 1, stream);
+}
+
+dg_status dg_k_grouped_bf16_gemm_tn_contiguous(const void* A, const void* B, const int32_t* ks, const float* C, void* D,
+                                               int M, int N, int K, int num_groups, void* stream) {
+    if (!ks) return set_error(DG_ERR_INVALID_ARG, "ks must be non-NULL");
+    if (num_groups <= 0) return set_error(DG_ERR_INVALID_ARG, "num_groups must be positive");
+    if (!aligned(ks, 4)) return set_error(DG_ERR_ALIGNMENT, "ks must be 4-byte aligned");
+    if (K % 128 != 0) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (whole segments)");
+    return bf16_gemm_tn(A, B, ks, C, D, M, N, K, num_groups, stream);
 }
 
 }  // extern "C"

@@ -12,6 +12,23 @@ namespace dg {
 
 enum Kind : int { kDense = 0, kContiguous = 1, kMasked = 2, kKGrouped = 3 };
 
+// What the fused epilogue D = act(A . B^T + bias) + residual consists of (the
+// kernel's DG_BIAS, DG_ACT, DG_RES, DG_ZOUT); all zero: the plain D = C + A . B^T.
+struct Epilogue {
+    int bias = 0;              // 0 none, 1 FP32, 2 BF16
+    int act = 0;               // dg_activation
+    int res = 0;               // residual added
+    int zout = 0;              // pre-activation stored
+    bool any() const { return bias || act || res || zout; }
+    int code() const { return ((bias * 8 + act) * 2 + res) * 2 + zout; }
+};
+// ... and its tensors
+struct EpilogueArgs {
+    const void* bias = nullptr;
+    const void* res = nullptr;
+    void* z = nullptr;
+};
+
 // One compiled specialisation of the kernel.  Everything here becomes a -D
 // macro of the hipRTC compile; N and K are compile-time constants (the
 // DeepGEMM launch article, section 4.2, bakes the matrix sizes into each JIT
@@ -42,6 +59,7 @@ struct KernelConfig {
                                // launch two column ranges with different tile widths
     int bstream = 0;           // each B block is read by at most two row blocks of the launch
                                // (dense or masked, few rows): B loads carry the non-temporal hint
+    Epilogue ep;               // fused epilogue of the *_epilogue entry points (none: plain D)
 
     int n_begin() const { return nb; }
     int n_end() const { return ne > 0 ? ne : n; }
@@ -84,7 +102,9 @@ struct Problem {
     int has_c;
     int sf = 0;    // scale format: as KernelConfig::sf
     int kt = 0;    // K-grouped: K rows of the operands (n, k above: N and the padded pitch)
+    int k_rows = 0;   // BF16 K-grouped: K before it is rounded up to whole K blocks (kt)
     int a_k_outer = 0, b_k_outer = 0;   // A stored [K][rows] (T), B stored [(G)][K][N] (N)
+    Epilogue ep;
 };
 
 // Tile heuristics (heuristics.cpp): the launches of one call, in order (one,
@@ -105,6 +125,11 @@ dg_status get_function(const KernelConfig& c, void** function /* hipFunction_t *
 // K-grouped operands are rewritten K-contiguous with this row pitch (the
 // compile-time K of the kernels; a new pitch means a new compile)
 inline int k_grouped_pitch(int k) { return (k + 1023) / 1024 * 1024; }
+
+// BF16 X [groups][rows_k][cols] rewritten K-contiguous as Xt [groups][cols][pitch]
+// (elements); columns [rows_k, k_end) of Xt are zeros (linear.hip)
+dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int cols, int k_end, int64_t pitch,
+                         void* stream);
 std::string cache_dir();
 
 // Device address of the library's status words on the current device

@@ -130,7 +130,7 @@ bool valid(const KernelConfig& c, const Problem& p) {
                            (c.bn / c.wn / 16) % 2 || c.bn / c.wn / 16 < 4))
         return false;
     if (c.sf && ((c.variant != 0 && c.variant != 4 && c.variant != 6) || c.kstep != 1)) return false;   // UE8M0, FP4: variant 0, one K block a stage
-    if (p.kind == kKGrouped && (c.sf || (c.variant != 0 && c.variant != 6) || c.kstep != 1)) return false;   // K-grouped: the same
+    if (p.kind == kKGrouped && ((c.sf && c.sf != 3) || (c.variant != 0 && c.variant != 6) || c.kstep != 1)) return false;   // K-grouped: the same
     if (c.variant < 0 || c.variant > 6) return false;
     int tm = c.bm / c.wm / 16, tn = c.bn / c.wn / 16;
     if (c.lds_bytes() > kLdsBytes) return false;
@@ -343,6 +343,7 @@ std::vector<KernelConfig> select_plan(const Problem& p, int num_cus) {
     base.n = p.n;
     base.k = p.k;
     base.g = (p.kind == kDense) ? 1 : p.g;
+    base.ep = p.ep;
 
     std::vector<KernelConfig> forced = parse_forced(base);
     if (valid_plan(forced, p)) return with_b_streams(forced, p);

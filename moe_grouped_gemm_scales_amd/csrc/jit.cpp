@@ -69,6 +69,12 @@ std::vector<std::string> compile_options(const KernelConfig& c) {
     if (c.variant == 6) def("DG_SPLIT", 1);
     def("DG_SF", c.sf);
     if (c.bstream) def("DG_BSTREAM", 1);
+    if (c.ep.any()) {
+        def("DG_BIAS", c.ep.bias);
+        def("DG_ACT", c.ep.act);
+        def("DG_RES", c.ep.res);
+        def("DG_ZOUT", c.ep.zout);
+    }
     if (c.ne > 0) {
         def("DG_NB", c.nb);
         def("DG_NE", c.ne);
@@ -193,6 +199,7 @@ std::string KernelConfig::key() const {
     if (sf == 3) s << "_bf16";
     if (sf == 4) s << "_f4f4";
     if (sf == 5) s << "_e8m0x2";
+    if (ep.any()) s << "_ep" << ep.bias << ep.act << ep.res << ep.zout;
     if (ne > 0) s << "_cols" << nb << "-" << ne;
     return s.str();
 }

@@ -26,6 +26,7 @@
 //     in order.  A and B here are the operands already made K-contiguous
 //     ([M][K], [N][K] with K the padded row pitch) by dg_transpose_k_major
 //     below; B has one FP32 scale per column and K block, sfb[K/128][N].
+//     BF16 operands have no scales, and grp == nullptr means one group of all kt rows.
 //
 // Layout of the work (MI355X-specific, not from the pages):
 //   * MFMA orientation is swapped: the MFMA "row" operand is a 16-row slice of
@@ -104,6 +105,24 @@ typedef u16 v4u16 __attribute__((ext_vector_type(4)));
 #ifndef DG_BSTREAM
 #define DG_BSTREAM 0
 #endif
+// Epilogue of the *_epilogue entry points: D = act(A . B^T + bias) + residual.
+// DG_BIAS: 0 none, 1 FP32, 2 BF16, one per column ([N], grouped forms [G][N]);
+// DG_ACT: 0 none, 1 ReLU, 2 SiLU, 3 GELU (erf), 4 GELU (tanh form);
+// DG_RES: a BF16 residual laid out like D is added after the activation;
+// DG_ZOUT: the pre-activation A . B^T + bias is stored in BF16 too, laid out like D.
+#ifndef DG_BIAS
+#define DG_BIAS 0
+#endif
+#ifndef DG_ACT
+#define DG_ACT 0
+#endif
+#ifndef DG_RES
+#define DG_RES 0
+#endif
+#ifndef DG_ZOUT
+#define DG_ZOUT 0
+#endif
+#define DG_EPI (DG_BIAS || DG_ACT || DG_RES || DG_ZOUT)
 
 namespace dg {
 
@@ -142,7 +161,8 @@ constexpr int KB_A = FP4A ? K / 2 : K;        // ... of A
 // FP4 B has a scale per row, never one per wave
 constexpr bool KG = kKind == 3;                // K-grouped: per-column B scales, per-group K ranges
 constexpr bool SB_UNIFORM = (KBLK % WAVE_N) == 0 && (DG_NB % WAVE_N) == 0 && !FP4B && !KG && !BF16;
-static_assert(!BF16 || (DG_KSTEP == 1 && kKind != 3), "BF16: one K block a stage, M-grouped or dense");
+static_assert(!BF16 || DG_KSTEP == 1, "BF16: one K block a stage");
+constexpr int KROWS = BF16 ? KBLK / 2 : KBLK;  // K indices of a 128-byte block (K-grouped counts)
 static_assert(!KG || (!SF_E8 && DG_SPLITK == 1 && DG_KSTEP == 1), "K-grouped: FP32 scales, no split-K, one K block a stage");
 
 static_assert(K % KBLK == 0, "K must be a multiple of 128");
@@ -177,6 +197,11 @@ struct Params {
     int num_tiles;         // total work items for this launch
     int kt;                // K-grouped: K rows of the operands (the groups' segments are cut there)
     u32* status;           // library status words: [0] counts bounded waits that gave up
+#if DG_EPI
+    const u8* bias;
+    const u16* res;
+    u16* z;
+#endif
 };
 
 // The kernel's one argument: the pointers and sizes of Params, passed by value in
@@ -198,8 +223,16 @@ struct KernArgs {
     int num_tiles;
     int kt;
     DG_GLOBAL u32* status;
+#if DG_EPI
+    const DG_GLOBAL u8* bias;
+    const DG_GLOBAL u16* res;
+    DG_GLOBAL u16* z;
+#define DG_EPI_ARGS , (const u8*)ka.bias, (const u16*)ka.res, (u16*)ka.z
+#else
+#define DG_EPI_ARGS
+#endif
 };
-static_assert(sizeof(KernArgs) == 96 && __builtin_offsetof(KernArgs, M) == 72 &&
+static_assert(sizeof(KernArgs) == (DG_EPI ? 120 : 96) && __builtin_offsetof(KernArgs, M) == 72 &&
               __builtin_offsetof(KernArgs, status) == 88, "the host fills this layout");
 
 // Promotion scale of one MFMA result: one FP32 per (row, 128-row block of B),
@@ -411,10 +444,13 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         const int g = t / per_g;
         const int local = t % per_g;
         int off = 0;
-        for (int h = 0; h < g; ++h) off += p.grp[h] > 0 ? p.grp[h] : 0;
-        int len = p.grp[g] > 0 ? p.grp[g] : 0;
-        const int kbt = p.kt / KBLK;
-        int kb0 = off / KBLK, kb1 = (off + len) / KBLK;
+        int len = p.kt;
+        if (!BF16 || p.grp) {
+            for (int h = 0; h < g; ++h) off += p.grp[h] > 0 ? p.grp[h] : 0;
+            len = p.grp[g] > 0 ? p.grp[g] : 0;
+        }
+        const int kbt = p.kt / KROWS;
+        int kb0 = off / KROWS, kb1 = (off + len) / KROWS;
         kb0 = kb0 < kbt ? kb0 : kbt;
         kb1 = kb1 < kbt ? kb1 : kbt;
         // grouped order inside the group: 8 row blocks per column sweep
@@ -471,6 +507,166 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
 // and 8-column alignment of every row, tile and column range.
 template <int TN_>
 constexpr bool PAIRED_STORES = TN_ % 2 == 0 && N % 8 == 0 && N_BEGIN % 8 == 0 && N_END % 8 == 0 && BN % 8 == 0;
+
+#if DG_EPI
+// ------------------------------------------------------------ fused epilogue
+// The activation in FP32; its result is rounded once, to BF16, with the residual
+// added, so the hardware's exp2 and reciprocal (1 ulp) are exact enough.  A NaN
+// stays a NaN.
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (DG_ACT == 1) return z < 0.f ? 0.f : z;
+    // z / (1 + e^-z)
+    if constexpr (DG_ACT == 2)
+        return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+    // z Phi(z), Phi from Abramowitz and Stegun 7.1.26 (|error of erf| < 1.5e-7): the
+    // polynomial gives erfc(|x|), x = z / sqrt 2, so Phi keeps its small values for z < 0
+    if constexpr (DG_ACT == 3) {
+        const float x = __builtin_fabsf(z) * 0.70710678f;
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.f));
+        float y = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+        y = __builtin_fmaf(t, y, 1.421413741f);
+        y = __builtin_fmaf(t, y, -0.284496736f);
+        y = __builtin_fmaf(t, y, 0.254829592f) * t;
+        const float half_erfc = 0.5f * y * __builtin_amdgcn_exp2f(-1.44269504f * x * x);
+        return z * (z < 0.f ? half_erfc : 1.f - half_erfc);
+    }
+    // z (1 + tanh u) / 2 = z / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3)
+    if constexpr (DG_ACT == 4) {
+        const float u2 = 1.59576912f * z * __builtin_fmaf(0.044715f * z, z, 1.f);
+        return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * u2));
+    }
+    return z;
+}
+__device__ __forceinline__ v4f activate4(v4f z) {
+    return v4f{activate(z.x), activate(z.y), activate(z.z), activate(z.w)};
+}
+typedef u32 v2u32 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v4f bf16x4(v2u32 w) {
+    return v4f{__builtin_bit_cast(float, w.x << 16), __builtin_bit_cast(float, w.x & 0xffff0000u),
+               __builtin_bit_cast(float, w.y << 16), __builtin_bit_cast(float, w.y & 0xffff0000u)};
+}
+constexpr bool VEC4 = N % 4 == 0 && N_END % 4 == 0;      // a lane's four columns are one aligned piece
+
+// Four columns n .. n + 3 of a lane at element offset off, as BF16.
+__device__ __forceinline__ void store4(u16* base, u64 off, int n, v4f v) {
+    if constexpr (VEC4) {
+        if (n < N_END) *(v4u16*)(base + off) = v4u16{f32_to_bf16(v.x), f32_to_bf16(v.y), f32_to_bf16(v.z), f32_to_bf16(v.w)};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N_END) base[off + e] = f32_to_bf16(v[e]);
+    }
+}
+// Two sub-tiles' columns (n and n + 16) of a lane as one 16-byte store: lanes 16
+// apart swap four values (see the plain epilogue).  Every lane of the row calls it.
+__device__ __forceinline__ void store_pair(u16* base, u64 row_off, int n, bool odd, v4f v0, v4f v1) {
+    const u32 lo0 = bf16_pair(v0.x, v0.y), hi0 = bf16_pair(v0.z, v0.w);
+    const u32 lo1 = bf16_pair(v1.x, v1.y), hi1 = bf16_pair(v1.z, v1.w);
+    const u32 r_lo = (u32)__builtin_amdgcn_ds_swizzle((int)(odd ? lo0 : lo1), 0x401F);
+    const u32 r_hi = (u32)__builtin_amdgcn_ds_swizzle((int)(odd ? hi0 : hi1), 0x401F);
+    const int n_out = odd ? n + 12 : n;
+    if (n_out < N_END)
+        *(v4i*)(base + row_off + n_out) = odd ? v4i{(int)r_lo, (int)r_hi, (int)lo1, (int)hi1}
+                                              : v4i{(int)lo0, (int)hi0, (int)r_lo, (int)r_hi};
+}
+
+// D = act(acc + bias) + residual of the rows that may be stored, and Z = acc +
+// bias where it is kept.  Everything stays in FP32 up to the one rounding of each
+// output.  The bias of the lane's columns is read once for all its rows, and a
+// row's residual one row ahead, so that its latency runs under the row before.
+// D may be the residual: a wave reads a row's residual before it stores that row.
+template <int TM_, int TN_, bool GRP_LDS>
+__device__ __forceinline__ void fused_epilogue(const Params& p, const Tile& tl, v4f (&acc)[TM_][TN_], int row0, int col0,
+                                               u32 grp_lds, u64 row_base) {
+    v4f bias[DG_BIAS ? TN_ : 1];
+    if constexpr (DG_BIAS != 0) {
+        const u64 g0 = kKind == 0 ? 0 : (u64)tl.g * N;
+#pragma unroll
+        for (int b = 0; b < TN_; ++b) {
+            const int n = tl.n0 + col0 + b * 16;
+            v4f v = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (VEC4) {
+                if (n < N_END) {
+                    if constexpr (DG_BIAS == 1) v = *(const v4f*)((const float*)p.bias + g0 + n);
+                    else v = bf16x4(*(const v2u32*)((const u16*)p.bias + g0 + n));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N_END)
+                        v[e] = DG_BIAS == 1 ? ((const float*)p.bias)[g0 + n + e]
+                                            : __builtin_bit_cast(float, (u32)((const u16*)p.bias)[g0 + n + e] << 16);
+            }
+            bias[b] = v;
+        }
+    }
+    auto stored = [&](int a) {
+        const int r = row0 + a * 16;
+        bool ok = r < tl.row_limit;
+        if constexpr (kKind == 1) {
+            const int gr = GRP_LDS ? *(__attribute__((address_space(3))) const int*)(grp_lds + a * 64)
+                                   : p.grp[tl.m0 + (ok ? r : 0)];
+            ok = ok && gr == tl.g;
+        }
+        return ok;
+    };
+    // the residual of row a's columns, as the BF16 pairs that are in memory
+    v2u32 res[2][DG_RES && VEC4 ? TN_ : 1];
+    auto read_residual = [&](int a, v2u32 (&to)[DG_RES && VEC4 ? TN_ : 1]) {
+        if constexpr (DG_RES != 0 && VEC4) {
+            if (!stored(a)) return;
+            const u64 off = row_base + (u64)(row0 + a * 16) * N + tl.n0 + col0;
+#pragma unroll
+            for (int b = 0; b < TN_; ++b)
+                if (tl.n0 + col0 + b * 16 < N_END) to[b] = *(const v2u32*)(p.res + off + b * 16);
+        }
+    };
+#pragma unroll
+    for (int b = 0; b < (DG_RES && VEC4 ? TN_ : 1); ++b) res[0][b] = res[1][b] = v2u32{0u, 0u};
+    read_residual(0, res[0]);
+    const bool odd = ((col0 >> 2) & 1) != 0;
+#pragma unroll
+    for (int a = 0; a < TM_; ++a) {
+        if (a + 1 < TM_) read_residual(a + 1, res[(a + 1) & 1]);
+        if (!stored(a)) continue;
+        const u64 row_off = row_base + (u64)(row0 + a * 16) * N;
+        auto finish = [&](int b, v4f z) {
+            v4f v = activate4(z);
+            if constexpr (DG_RES != 0 && VEC4) {
+                v += bf16x4(res[a & 1][b]);
+            } else if constexpr (DG_RES != 0) {
+                const int n = tl.n0 + col0 + b * 16;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N_END) v[e] += __builtin_bit_cast(float, (u32)p.res[row_off + n + e] << 16);
+            }
+            return v;
+        };
+        if constexpr (PAIRED_STORES<TN_>) {
+#pragma unroll
+            for (int b = 0; b < TN_; b += 2) {
+                const int n = tl.n0 + col0 + b * 16;
+                v4f z0 = acc[a][b], z1 = acc[a][b + 1];
+                if constexpr (DG_BIAS != 0) {
+                    z0 += bias[b];
+                    z1 += bias[b + 1];
+                }
+                if constexpr (DG_ZOUT != 0) store_pair(p.z, row_off, n, odd, z0, z1);
+                store_pair(p.D, row_off, n, odd, finish(b, z0), finish(b + 1, z1));
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < TN_; ++b) {
+                const int n = tl.n0 + col0 + b * 16;
+                v4f z = acc[a][b];
+                if constexpr (DG_BIAS != 0) z += bias[b];
+                if constexpr (DG_ZOUT != 0) store4(p.z, row_off + n, n, z);
+                store4(p.D, row_off + n, n, finish(b, z));
+            }
+        }
+    }
+}
+#endif
 
 // GRP_LDS (contiguous form): the expert of the lane's row row0 + 16 a is the
 // int at LDS address grp_lds + 64 a, instead of being read from global memory.
@@ -593,6 +789,10 @@ __device__ __forceinline__ void finish_tile(const Params& p, const Tile& tl, v4f
     u64 row_base;      // element offset of row 0 of this tile in C/D
     if constexpr (kKind == 2 || kKind == 3) row_base = ((u64)tl.g * p.M + tl.m0) * N;
     else row_base = (u64)tl.m0 * N;
+#if DG_EPI
+    fused_epilogue<TM_, TN_, GRP_LDS>(p, tl, acc, row0, col0, grp_lds, row_base);
+    return;
+#endif
 #pragma unroll
     for (int a = 0; a < TM_; ++a) {
         const int r = row0 + a * 16;            // row inside the tile
@@ -825,7 +1025,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
     u32* __restrict__ counters = (u32*)ka.counters;
     const int M = ka.M, num_tiles = ka.num_tiles, kt = ka.kt;
     u32* __restrict__ status = (u32*)ka.status;
-    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status};
+    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status DG_EPI_ARGS};
     // Every argument in one round trip of scalar loads: otherwise the loop bound
     // is fetched first and the pointers only after it arrives (~0.5 us each).
     asm volatile("" :: "s"(A), "s"(sfa), "s"(B), "s"(sfb), "s"(C), "s"(D), "s"(grp), "s"(ws), "s"(counters), "s"(M),
@@ -1574,7 +1774,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
     u32* __restrict__ counters = (u32*)ka.counters;
     const int M = ka.M, num_tiles = ka.num_tiles, kt = ka.kt;
     u32* __restrict__ status = (u32*)ka.status;
-    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status};
+    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status DG_EPI_ARGS};
     // Every argument in one round trip of scalar loads: otherwise the loop bound
     // is fetched first and the pointers only after it arrives (~0.5 us each).
     asm volatile("" :: "s"(A), "s"(sfa), "s"(B), "s"(sfb), "s"(C), "s"(D), "s"(grp), "s"(ws), "s"(counters), "s"(M),
@@ -1901,7 +2101,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
     u32* __restrict__ counters = (u32*)ka.counters;
     const int M = ka.M, num_tiles = ka.num_tiles, kt = ka.kt;
     u32* __restrict__ status = (u32*)ka.status;
-    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status};
+    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status DG_EPI_ARGS};
     // Every argument in one round trip of scalar loads: otherwise the loop bound
     // is fetched first and the pointers only after it arrives (~0.5 us each).
     asm volatile("" :: "s"(A), "s"(sfa), "s"(B), "s"(sfb), "s"(C), "s"(D), "s"(grp), "s"(ws), "s"(counters), "s"(M),
@@ -2176,7 +2376,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
     u32* __restrict__ counters = (u32*)ka.counters;
     const int M = ka.M, num_tiles = ka.num_tiles, kt = ka.kt;
     u32* __restrict__ status = (u32*)ka.status;
-    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status};
+    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status DG_EPI_ARGS};
     asm volatile("" :: "s"(A), "s"(sfa), "s"(B), "s"(sfb), "s"(C), "s"(D), "s"(grp), "s"(M), "s"(num_tiles),
                  "s"(gridDim.x));
     __shared__ __attribute__((aligned(1024))) u8 smem[LDS_BYTES];

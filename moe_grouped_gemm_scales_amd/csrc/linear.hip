@@ -1,0 +1,289 @@
+// Backward side of the products with a fused epilogue (hipcc, gfx950): the
+// activation's gradient with the bias gradient in the same pass, and the
+// K-contiguous rewrite of BF16 operands for the NN and TN products.  The
+// operations are specified in include/dg.h.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+typedef unsigned short u16;
+typedef unsigned int u32;
+typedef unsigned long long u64;
+typedef u32 u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPadding = -1;           // m_indices of a padding row inside a segment
+
+__device__ __forceinline__ float bf16_lo(u32 w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+__device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
+__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
+
+// ---------------------------------------------------------------- K-contiguous rewrite
+// X [rows_k][cols] -> Xt [cols][pitch], columns [rows_k, k_end) of Xt zero.  One
+// workgroup a 64 x 64 block through LDS: 16-byte loads along cols, 16-byte
+// stores along K.  A row of the LDS block is 33 words, so the gather of a
+// column (four lanes 16 rows apart, 16 columns a wave) touches 32 distinct
+// banks.  K blocks fastest, as in the FP8 rewrite.
+__global__ void __launch_bounds__(256)
+dg_transpose_bf16_kernel(const u16* __restrict__ X, u16* __restrict__ Xt, int rows_k, int cols, int k_blocks,
+                         long long pitch) {
+    __shared__ __attribute__((aligned(4))) u16 tile[64][66];
+    const int tid = threadIdx.x;
+    const int k0 = (int)(blockIdx.x % (u32)k_blocks) * 64, c0 = (int)(blockIdx.x / (u32)k_blocks) * 64;
+    X += (u64)blockIdx.z * (u64)rows_k * (u64)cols;
+    Xt += (u64)blockIdx.z * (u64)cols * (u64)pitch;
+    const int r = tid >> 2, piece = (tid & 3) * 16;
+    {
+        const int k = k0 + r, c = c0 + piece;
+        u32 w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        if (k < rows_k) {
+            const u16* src = X + (u64)k * (u64)cols + c;
+            if ((cols & 7) == 0) {                          // every 8-element group is whole and aligned
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (c + 8 * h < cols) {
+                        const u32x4 x = *(const u32x4*)(src + 8 * h);
+                        w[4 * h] = x.x; w[4 * h + 1] = x.y; w[4 * h + 2] = x.z; w[4 * h + 3] = x.w;
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < cols) w[i >> 1] |= (u32)src[i] << (16 * (i & 1));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *(u32*)&tile[r][piece + 2 * j] = w[j];
+    }
+    __syncthreads();
+    const int c = c0 + r;
+    if (c < cols) {
+        u32 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = (u32)tile[piece + 2 * j][r] | ((u32)tile[piece + 2 * j + 1][r] << 16);
+        u16* dst = Xt + (u64)c * (u64)pitch + k0 + piece;
+        *(u32x4*)dst = u32x4{w[0], w[1], w[2], w[3]};
+        *(u32x4*)(dst + 8) = u32x4{w[4], w[5], w[6], w[7]};
+    }
+}
+
+// ---------------------------------------------------------------- activation and bias gradient
+// d act / d z in FP32 (the device library's exp and erf: the bias gradient stays
+// FP32, so these are not rounded to BF16).  Past |z| = 16 the slopes are 0 or 1 to
+// the last bit (SiLU: past 200 its tail is below FP32); z is cut there, so that
+// no infinity meets a zero.  A NaN stays a NaN.
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+    if constexpr (ACT == DG_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
+    if constexpr (ACT == DG_ACT_SILU) {
+        z = z > 200.f ? 200.f : z < -200.f ? -200.f : z;
+        const float s = 1.f / (1.f + expf(-z));
+        return s * (1.f + z * (1.f - s));
+    }
+    if constexpr (ACT == DG_ACT_GELU) {
+        z = z > 16.f ? 16.f : z < -16.f ? -16.f : z;
+        return 0.5f * (1.f + erff(0.70710678f * z)) + 0.39894228f * z * expf(-0.5f * z * z);
+    }
+    if constexpr (ACT == DG_ACT_GELU_TANH) {
+        z = z > 16.f ? 16.f : z < -16.f ? -16.f : z;
+        const float s = 1.f / (1.f + expf(-1.59576912f * z * (1.f + 0.044715f * z * z)));
+        return s + z * s * (1.f - s) * 1.59576912f * (1.f + 0.134145f * z * z);
+    }
+    return 1.f;
+}
+
+// dZ = dD slope(Z), and the column sums of dZ (FP32, before its rounding) of the
+// workgroup's rows.  A workgroup takes 512 columns of `chunk` rows: 8 columns a
+// lane, its four waves every fourth row, whose sums meet in LDS and are added in
+// wave order.  Contiguous form: the rows of a chunk (a divisor of 128) belong to
+// the expert of its first row; padding rows (-1) get dZ = 0, rows past the last
+// segment are untouched.  partial [chunks][N], or nullptr: no bias gradient.
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(256)
+dg_epilogue_backward_kernel(const u16* __restrict__ dD, const u16* __restrict__ Z, const int* __restrict__ m_indices,
+                            u16* __restrict__ dZ, float* __restrict__ partial, int rows, int N, int G, int chunk) {
+    __shared__ float sums[4][512];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c0 = (int)blockIdx.y * 512;
+    const int r0 = (int)blockIdx.x * chunk;
+    const int r1 = rows - r0 < chunk ? rows : r0 + chunk;
+    auto col = [&](int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 64 * i; };
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    auto load = [&](const u16* p, float (&v)[8]) {
+        if constexpr (VEC) {
+            u32x4 w = {0u, 0u, 0u, 0u};
+            if (col(0) < N) w = *(const u32x4*)(p + col(0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_lo(w[i]);
+                v[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = col(i) < N ? __builtin_bit_cast(float, (u32)p[col(i)] << 16) : 0.f;
+        }
+    };
+    const int owner = m_indices ? m_indices[r0] : 0;
+#pragma unroll 4
+    for (int r = r0 + wave; r < r1; r += 4) {
+        const int g = m_indices ? m_indices[r] : 0;
+        float v[8];
+        if ((u32)g < (u32)G) {
+            load(dD + (u64)r * N, v);
+            if constexpr (ACT != DG_ACT_NONE) {
+                float z[8];
+                load(Z + (u64)r * N, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= slope<ACT>(z[i]);
+            }
+            if (g == owner) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += v[i];
+            }
+        } else if (g == kPadding) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        } else {
+            continue;
+        }
+        if (!dZ) continue;
+        u16* dst = dZ + (u64)r * N;
+        if constexpr (VEC) {
+            if (col(0) < N)
+                *(u32x4*)(dst + col(0)) = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                                                to_bf16x2(v[6], v[7])};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col(i) < N) dst[col(i)] = to_bf16(v[i]);
+        }
+    }
+    if (!partial) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[wave][col(i) - c0] = acc[i];
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = (int)threadIdx.x + 256 * h;
+        if (c0 + c < N) partial[(u64)blockIdx.x * N + c0 + c] = sums[0][c] + sums[1][c] + sums[2][c] + sums[3][c];
+    }
+}
+
+// dbias[g][n]: the partial sums of the chunks that belong to expert g, in chunk
+// order within each of four quarters, then the quarters in order: the same sum
+// on every run.
+__global__ void __launch_bounds__(256)
+dg_bias_sum_kernel(const float* __restrict__ partial, const int* __restrict__ m_indices, float* __restrict__ dbias,
+                   int chunks, int chunk, int N) {
+    __shared__ float sums[4][64];
+    const int lane = threadIdx.x & 63, quarter = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = (int)blockIdx.x * 64 + lane, g = blockIdx.y;
+    const int each = (chunks + 3) / 4;
+    const int first = quarter * each, last = chunks - first < each ? chunks : first + each;
+    float s = 0.f;
+#pragma unroll 8
+    for (int c = first; c < last; ++c) {
+        if (m_indices && m_indices[(u64)c * chunk] != g) continue;
+        s += n < N ? partial[(u64)c * N + n] : 0.f;
+    }
+    sums[quarter][lane] = s;
+    __syncthreads();
+    if (quarter == 0 && n < N) dbias[(u64)g * N + n] = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+dg_status launched(const char* what) {
+    hipError_t e = hipGetLastError();
+    return e == hipSuccess ? DG_OK : set_error(DG_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+template <int ACT>
+void launch_backward(dim3 grid, hipStream_t stream, const u16* dD, const u16* Z, const int* m_indices, u16* dZ,
+                     float* partial, int rows, int N, int G, int chunk) {
+    hipLaunchKernelGGL(N % 8 == 0 ? (dg_epilogue_backward_kernel<ACT, true>) : (dg_epilogue_backward_kernel<ACT, false>),
+                       grid, dim3(256), 0, stream, dD, Z, m_indices, dZ, partial, rows, N, G, chunk);
+}
+
+dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_t* m_indices, void* dZ, float* dbias,
+                            int rows, int N, int G, void* stream_ptr) {
+    if (rows != 0 && (!dD || (act != DG_ACT_NONE && !Z)))
+        return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: dD and (with an activation) Z must be non-NULL");
+    if (act < DG_ACT_NONE || act > DG_ACT_GELU_TANH)
+        return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: unknown activation");
+    if (rows < 0 || N <= 0 || G <= 0)
+        return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: sizes must be positive (M may be 0)");
+    if (!aligned(dD, 16) || !aligned(Z, 16) || !aligned(dZ, 16) || !aligned(dbias, 4) || !aligned(m_indices, 4))
+        return set_error(DG_ERR_ALIGNMENT, "epilogue_backward: dD, Z and dZ must be 16-byte, the rest 4-byte aligned");
+    if (G > 65535 || N > 65535 * 512)
+        return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many groups or columns for one launch");
+    const hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+    constexpr int chunk = 32;
+    const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
+    float* partial = nullptr;
+    if (dbias && chunks > 0) {
+        dg_status s = stream_scratch(stream_ptr, (size_t)chunks * (size_t)N * sizeof(float), &partial);
+        if (s != DG_OK) return s;
+    }
+    if (chunks > 0 && (dZ || dbias)) {
+        const dim3 grid(chunks, (N + 511) / 512);
+        const u16 *d = static_cast<const u16*>(dD), *z = static_cast<const u16*>(Z);
+        u16* out = static_cast<u16*>(dZ);
+        auto* f = act == DG_ACT_RELU ? launch_backward<DG_ACT_RELU> : act == DG_ACT_SILU ? launch_backward<DG_ACT_SILU>
+                : act == DG_ACT_GELU ? launch_backward<DG_ACT_GELU>
+                : act == DG_ACT_GELU_TANH ? launch_backward<DG_ACT_GELU_TANH> : launch_backward<DG_ACT_NONE>;
+        f(grid, stream, d, z, m_indices, out, partial, rows, N, G, chunk);
+        dg_status s = launched("epilogue_backward");
+        if (s != DG_OK) return s;
+    }
+    if (dbias) {
+        hipLaunchKernelGGL(dg_bias_sum_kernel, dim3((N + 63) / 64, G), dim3(256), 0, stream, partial, m_indices, dbias,
+                           chunks, chunk, N);
+        return launched("epilogue_backward (bias)");
+    }
+    return DG_OK;
+}
+
+}  // namespace
+
+dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int cols, int k_end, int64_t pitch,
+                         void* stream) {
+    const int k_blocks = k_end / 64;
+    const uint64_t blocks = (uint64_t)k_blocks * (uint64_t)((cols + 63) / 64);
+    if (blocks >= (1ull << 31) || groups > 65535)
+        return set_error(DG_ERR_UNSUPPORTED, "operand too large for the K-contiguous rewrite");
+    if (blocks == 0) return DG_OK;
+    hipLaunchKernelGGL(dg_transpose_bf16_kernel, dim3((unsigned)blocks, 1, (unsigned)groups), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), static_cast<const u16*>(x), static_cast<u16*>(xt), rows_k, cols,
+                       k_blocks, (long long)pitch);
+    return launched("K-contiguous rewrite");
+}
+
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dg_status dg_epilogue_backward(const void* dD, const void* Z, int activation, void* dZ, float* dbias, int M, int N,
+                               void* stream) {
+    return epilogue_backward(dD, Z, activation, nullptr, dZ, dbias, M, N, 1, stream);
+}
+
+dg_status dg_m_grouped_epilogue_backward_contiguous(const void* dD, const void* Z, int activation,
+                                                    const int32_t* m_indices, void* dZ, float* dbias, int M, int N,
+                                                    int num_groups, void* stream) {
+    if (!m_indices && M != 0) return set_error(DG_ERR_INVALID_ARG, "m_indices must be non-NULL");
+    if (M > 0 && M % dg_get_mk_alignment_for_contiguous_layout() != 0)
+        return set_error(DG_ERR_ALIGNMENT, "contiguous M must be a multiple of the M alignment (128)");
+    return epilogue_backward(dD, Z, activation, m_indices, dZ, dbias, M, N, num_groups, stream);
+}
+
+}  // extern "C"

@@ -102,6 +102,18 @@ def _load():
                        ("dg_moe_sort_masked", [vp] * 3 + [i32] * 4 + [vp]),
                        ("dg_moe_dispatch_bf16", [vp] * 4 + [i32] * 4 + [vp]),
                        ("dg_moe_dispatch_fp8", [vp] * 5 + [i32] * 6 + [vp]),
+                       ("dg_bf16_gemm_nt_epilogue", [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_m_grouped_bf16_gemm_nt_contiguous_epilogue", [vp] * 5 + [i32] * 4 + [vp]),
+                       ("dg_m_grouped_bf16_gemm_nt_masked_epilogue", [vp] * 5 + [i32] * 4 + [vp]),
+                       ("dg_fp8_gemm_nt_epilogue", [vp] * 6 + [i32] * 3 + [vp]),
+                       ("dg_m_grouped_fp8_gemm_nt_contiguous_epilogue", [vp] * 7 + [i32] * 4 + [vp]),
+                       ("dg_m_grouped_fp8_gemm_nt_masked_epilogue", [vp] * 7 + [i32] * 4 + [vp]),
+                       ("dg_epilogue_backward", [vp, vp, i32, vp, vp, i32, i32, vp]),
+                       ("dg_m_grouped_epilogue_backward_contiguous", [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp]),
+                       ("dg_bf16_gemm_nn", [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_bf16_gemm_tn", [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_m_grouped_bf16_gemm_nn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
+                       ("dg_k_grouped_bf16_gemm_tn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_moe_combine", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_moe_combine_backward", [vp] * 7 + [i32] * 4 + [vp])):
         getattr(lib, name).argtypes = args
@@ -809,3 +821,214 @@ def dg_moe_combine_backward(dY, rows, pos, weights, m_indices, d_rows, d_weights
     _check(lib.dg_moe_combine_backward(_ptr(dY), _ptr(rows), _ptr(pos), _ptr(weights), _ptr(m_indices), _ptr(d_rows),
                                        _ptr(d_weights), T, k, n, N, _stream(stream)))
     return d_rows
+
+
+# ---------------------------------------------------------------- products with a fused epilogue
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # dg_activation
+
+
+# OR into `kind` of precompile / describe_config, with activation << 12
+EPI_BIAS_F32, EPI_BIAS_BF16, EPI_RESIDUAL, EPI_Z = 0x100, 0x200, 0x400, 0x800
+
+
+class _Epilogue(ctypes.Structure):      # dg_epilogue
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int), ("activation", ctypes.c_int),
+                ("residual", ctypes.c_void_p), ("Z", ctypes.c_void_p)]
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _epilogue(D, lead, bias, activation, residual, Z):
+    """The dg_epilogue of D [*, N] with bias [*lead, N]."""
+    e = _Epilogue(activation=_activation(activation))
+    if bias is not None:
+        if bias.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"bias must be float32 or bfloat16, got {bias.dtype}")
+        _typed(bias, "bias", bias.dtype, (*lead, D.shape[-1]))
+        e.bias, e.bias_type = bias.data_ptr(), int(bias.dtype == torch.bfloat16)
+    if residual is not None:
+        _typed(residual, "residual", torch.bfloat16, D.shape)
+        e.residual = residual.data_ptr()
+    if Z is not None:
+        _typed(Z, "Z", torch.bfloat16, D.shape)
+        e.Z = Z.data_ptr()
+    return ctypes.byref(e)
+
+
+def dg_bf16_gemm_nt_epilogue(A, B, D, bias=None, activation="none", residual=None, Z=None, stream=None):
+    """D = activation(A @ B.T + bias) + residual in BF16; Z (optional) receives A @ B.T + bias.
+
+    A [M,K], B [N,K], D, residual and Z [M,N] bfloat16, bias [N] float32 or bfloat16."""
+    M, K = A.shape
+    N = B.shape[0]
+    _bf(A, "A", (M, K)); _bf(B, "B", (N, K))
+    _out(D, (M, N))
+    e = _epilogue(D, (), bias, activation, residual, Z)
+    _check(lib.dg_bf16_gemm_nt_epilogue(_ptr(A), _ptr(B), e, _ptr(D), M, N, K, _stream(stream)))
+    return D
+
+
+def dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(A, B, m_indices, D, bias=None, activation="none", residual=None,
+                                                  Z=None, stream=None):
+    """Contiguous M-grouped form: B [G,N,K], bias [G,N], m_indices int32 [M]."""
+    M, K = A.shape
+    G, N = B.shape[0], B.shape[1]
+    _bf(A, "A", (M, K)); _bf(B, "B", (G, N, K))
+    _typed(m_indices, "m_indices", torch.int32, (M,))
+    _out(D, (M, N))
+    e = _epilogue(D, (G,), bias, activation, residual, Z)
+    _check(lib.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(_ptr(A), _ptr(B), _ptr(m_indices), e, _ptr(D), M, N, K, G,
+                                                             _stream(stream)))
+    return D
+
+
+def dg_m_grouped_bf16_gemm_nt_masked_epilogue(A, B, masked_m, D, bias=None, activation="none", residual=None, Z=None,
+                                              stream=None):
+    """Masked M-grouped form: A [G,M_max,K], B [G,N,K], bias [G,N], masked_m int32 [G]."""
+    G, M_max, K = A.shape
+    N = B.shape[1]
+    _bf(A, "A", (G, M_max, K)); _bf(B, "B", (G, N, K))
+    _typed(masked_m, "masked_m", torch.int32, (G,))
+    _out(D, (G, M_max, N))
+    e = _epilogue(D, (G,), bias, activation, residual, Z)
+    _check(lib.dg_m_grouped_bf16_gemm_nt_masked_epilogue(_ptr(A), _ptr(B), _ptr(masked_m), e, _ptr(D), M_max, N, K, G,
+                                                         _stream(stream)))
+    return D
+
+
+def dg_fp8_gemm_nt_epilogue(A, sfa, B, sfb, D, bias=None, activation="none", residual=None, Z=None, stream=None):
+    """As dg_bf16_gemm_nt_epilogue with E4M3 operands and FP32 scales (layouts of dg_fp8_gemm_nt)."""
+    _fp8(A, "A"); _fp8(B, "B")
+    M, K = A.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError("A and B must share K")
+    _f32(sfa, "sfa", (_cdiv(K, 128), M)); _f32(sfb, "sfb", (_cdiv(N, 128), _cdiv(K, 128)))
+    _out(D, (M, N))
+    e = _epilogue(D, (), bias, activation, residual, Z)
+    _check(lib.dg_fp8_gemm_nt_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), e, _ptr(D), M, N, K, _stream(stream)))
+    return D
+
+
+def dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(A, sfa, B, sfb, m_indices, D, bias=None, activation="none",
+                                                 residual=None, Z=None, stream=None):
+    """Contiguous M-grouped FP8 form (layouts of dg_m_grouped_fp8_gemm_nt_contiguous), bias [G,N]."""
+    _fp8(A, "A"); _fp8(B, "B")
+    M, K = A.shape
+    G, N = B.shape[0], B.shape[1]
+    if B.shape[2] != K:
+        raise ValueError("A and B must share K")
+    _f32(sfa, "sfa", (_cdiv(K, 128), M)); _f32(sfb, "sfb", (G, _cdiv(N, 128), _cdiv(K, 128)))
+    _typed(m_indices, "m_indices", torch.int32, (M,))
+    _out(D, (M, N))
+    e = _epilogue(D, (G,), bias, activation, residual, Z)
+    _check(lib.dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(m_indices), e,
+                                                            _ptr(D), M, N, K, G, _stream(stream)))
+    return D
+
+
+def dg_m_grouped_fp8_gemm_nt_masked_epilogue(A, sfa, B, sfb, masked_m, D, bias=None, activation="none", residual=None,
+                                             Z=None, stream=None):
+    """Masked M-grouped FP8 form (layouts of dg_m_grouped_fp8_gemm_nt_masked), bias [G,N]."""
+    _fp8(A, "A"); _fp8(B, "B")
+    G, M_max, K = A.shape
+    N = B.shape[1]
+    if B.shape[0] != G or B.shape[2] != K:
+        raise ValueError("B must be [G, N, K]")
+    _f32(sfa, "sfa", (G, _cdiv(K, 128), M_max)); _f32(sfb, "sfb", (G, _cdiv(N, 128), _cdiv(K, 128)))
+    _typed(masked_m, "masked_m", torch.int32, (G,))
+    _out(D, (G, M_max, N))
+    e = _epilogue(D, (G,), bias, activation, residual, Z)
+    _check(lib.dg_m_grouped_fp8_gemm_nt_masked_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(masked_m), e,
+                                                        _ptr(D), M_max, N, K, G, _stream(stream)))
+    return D
+
+
+def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=None):
+    """dZ = dD * activation'(Z) and dbias = its column sums (either may be None).
+
+    dD, Z, dZ bfloat16 [M,N] (Z None without an activation), dbias float32 [N]; with m_indices int32 [M]
+    (contiguous layout) dbias is [G,N], and dZ of padding rows is cleared."""
+    if dD.dim() != 2:
+        raise ValueError("dD must be [M, N]")
+    M, N = dD.shape
+    act = _activation(activation)
+    _bf(dD, "dD", (M, N))
+    if act:
+        if Z is None:
+            raise ValueError("Z is needed with an activation")
+        _bf(Z, "Z", (M, N))
+    if dZ is not None:
+        _bf(dZ, "dZ", (M, N))
+    z = _ptr(Z) if act else None
+    if m_indices is None:
+        if dbias is not None:
+            _typed(dbias, "dbias", torch.float32, (N,))
+        _check(lib.dg_epilogue_backward(_ptr(dD), z, act, _ptr(dZ), _ptr(dbias), M, N, _stream(stream)))
+    else:
+        _typed(m_indices, "m_indices", torch.int32, (M,))
+        G = 65535                       # without a bias any row that names an expert is one
+        if dbias is not None:
+            G = dbias.shape[0]
+            _typed(dbias, "dbias", torch.float32, (G, N))
+        _check(lib.dg_m_grouped_epilogue_backward_contiguous(_ptr(dD), z, act, _ptr(m_indices), _ptr(dZ), _ptr(dbias), M,
+                                                             N, G, _stream(stream)))
+    return dZ
+
+
+# ---------------------------------------------------------------- BF16 products of the backward pass
+def dg_bf16_gemm_nn(A, B, C, D, stream=None):
+    """D = C + A @ B with A [M,K], B [K,N] bfloat16, C None or float32 [M,N]."""
+    M, K = A.shape
+    N = B.shape[1]
+    _bf(A, "A", (M, K)); _bf(B, "B", (K, N))
+    if C is not None:
+        _f32(C, "C", (M, N))
+    _out(D, (M, N))
+    _check(lib.dg_bf16_gemm_nn(_ptr(A), _ptr(B), _ptr(C), _ptr(D), M, N, K, _stream(stream)))
+    return D
+
+
+def dg_m_grouped_bf16_gemm_nn_contiguous(A, B, m_indices, C, D, stream=None):
+    """Contiguous M-grouped: row m of D is C[m] + A[m] @ B[m_indices[m]], B [G,K,N]."""
+    M, K = A.shape
+    G, N = B.shape[0], B.shape[2]
+    _bf(A, "A", (M, K)); _bf(B, "B", (G, K, N))
+    _typed(m_indices, "m_indices", torch.int32, (M,))
+    if C is not None:
+        _f32(C, "C", (M, N))
+    _out(D, (M, N))
+    _check(lib.dg_m_grouped_bf16_gemm_nn_contiguous(_ptr(A), _ptr(B), _ptr(m_indices), _ptr(C), _ptr(D), M, N, K, G,
+                                                    _stream(stream)))
+    return D
+
+
+def dg_bf16_gemm_tn(A, B, C, D, stream=None):
+    """D = C + A.T @ B with A [K,M], B [K,N] bfloat16 (any K), C None or float32 [M,N]."""
+    K, M = A.shape
+    N = B.shape[1]
+    _bf(A, "A", (K, M)); _bf(B, "B", (K, N))
+    if C is not None:
+        _f32(C, "C", (M, N))
+    _out(D, (M, N))
+    _check(lib.dg_bf16_gemm_tn(_ptr(A), _ptr(B), _ptr(C), _ptr(D), M, N, K, _stream(stream)))
+    return D
+
+
+def dg_k_grouped_bf16_gemm_tn_contiguous(A, B, ks, C, D, stream=None):
+    """D[g] = C[g] + A_seg.T @ B_seg over the K segments ks int32 [G]; A [K,M], B [K,N], C, D [G,M,N]."""
+    K, M = A.shape
+    N = B.shape[1]
+    G = ks.numel()
+    _bf(A, "A", (K, M)); _bf(B, "B", (K, N))
+    _typed(ks, "ks", torch.int32, (G,))
+    if C is not None:
+        _f32(C, "C", (G, M, N))
+    _out(D, (G, M, N))
+    _check(lib.dg_k_grouped_bf16_gemm_tn_contiguous(_ptr(A), _ptr(B), _ptr(ks), _ptr(C), _ptr(D), M, N, K, G,
+                                                    _stream(stream)))
+    return D

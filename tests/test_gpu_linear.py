@@ -1,0 +1,405 @@
+"""Products with a fused epilogue, their backward pass and the BF16 NN / TN products on the GPU, against
+plain CPU forms in 64 bits.
+
+Tolerances.  The forms without epilogue are held to |D - ref| <= 2^-7 |ref| + 1e-3 rms(ref) (tests/check.py):
+one BF16 rounding (2^-8 covers it) and 1e-3 rms for FP32 accumulation.  Here the accumulation's share passes
+through the activation, whose slope is at most 1.13, so D is held to 2^-8 |ref| + 1.13e-3 rms(Z), Z to the plain
+bound.  Backward: dZ rounds once, its slope is computed in FP32 (the device's exp and erf, a few 2^-23 of terms up
+to 1 + |z|): 2^-8 |ref| + 2^-20 |dD| (1 + |z|); the bias gradient adds at most `rows` FP32 terms."""
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_scales_amd as dg
+from tests import check, gen
+from tests import linear_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.init()
+
+
+def _bf(shape, seed, scale=1.0):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * scale).to(torch.bfloat16)
+
+
+def _run(p, bias, act, residual, keep_z, d=None):
+    """(D, Z, their sentinel) on the CPU, flat rows."""
+    shape = (*p.A.shape[:-1], p.B.shape[-2])
+    sent = gen.sentinel_like(shape, 99)
+    D = sent.cuda() if d is None else d
+    Z = sent.cuda() if keep_z else None
+    c = lambda t: None if t is None else t.cuda()
+    kind = "bf16" if p.bf16 else "fp8"
+    operands = [c(p.A), c(p.B)] if p.bf16 else [c(p.A), c(p.sfa), c(p.B), c(p.sfb)]
+    kw = dict(bias=c(bias), activation=act, residual=D if residual is D else c(residual), Z=Z)
+    if p.kind == "dense":
+        getattr(dg, f"dg_{kind}_gemm_nt_epilogue")(*operands, D, **kw)
+    else:
+        grp = p.m_indices if p.kind == "contiguous" else p.masked_m
+        getattr(dg, f"dg_m_grouped_{kind}_gemm_nt_{p.kind}_epilogue")(*operands, c(grp), D, **kw)
+    torch.cuda.synchronize()
+    N = shape[-1]
+    return D.cpu().reshape(-1, N), None if Z is None else Z.cpu().reshape(-1, N), sent.reshape(-1, N)
+
+
+def _check(p, with_bias, act, with_res, keep_z, seed, bias_dtype=torch.float32, what=""):
+    N = p.B.shape[-2]
+    lead = () if p.kind == "dense" else (p.B.shape[0],)
+    bias = torch.randn((*lead, N), generator=torch.Generator().manual_seed(seed)).to(bias_dtype) if with_bias else None
+    shape = (*p.A.shape[:-1], N)
+    res = _bf(shape, seed + 1) if with_res else None
+    D, Z, sent = _run(p, bias, act, res, keep_z)
+    z, d, comp = ref.forward(p, None if bias is None else bias.double().numpy().reshape(-1, N), act,
+                             None if res is None else res.double().numpy().reshape(-1, N))
+    rms = float(np.sqrt(np.mean(z[comp] ** 2))) if comp.any() else 0.0
+    got = check.bf16_to_f64(D)[comp]
+    assert np.isfinite(got).all(), what
+    assert np.all(np.abs(got - d[comp]) <= 2.0 ** -8 * np.abs(d[comp]) + 1.13e-3 * rms), what
+    idx = torch.from_numpy(~comp)
+    assert torch.equal(D[idx].view(torch.int16), sent[idx].view(torch.int16)), f"{what}: an uncomputed row was written"
+    if keep_z:
+        check.assert_close(check.bf16_to_f64(Z)[comp], z[comp], what + " Z")
+        assert torch.equal(Z[idx].view(torch.int16), sent[idx].view(torch.int16))
+
+
+SIZES = [(1, 16, 64), (1, 7168, 256), (5, 129, 192), (64, 2112, 1024), (100, 302, 512), (257, 515, 640), (300, 1004, 2048),
+         (517, 2112, 1536)]
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_bf16_dense(M, N, K, act):
+    p = gen.make_bf16("dense", seed=M + N + K, M=M, N=N, K=K)
+    _check(p, True, act, True, True, M + N, what=f"bf16 {M}x{N}x{K} {act}")
+
+
+@pytest.mark.parametrize("with_bias,act,with_res,keep_z", [(True, "none", False, False), (False, "gelu", False, False),
+                                                           (False, "none", True, False), (False, "silu", False, True),
+                                                           (False, "none", False, False)])
+@pytest.mark.parametrize("M,N,K", [(33, 200, 256), (70, 131, 128), (400, 1024, 512)])
+def test_each_part_alone(M, N, K, with_bias, act, with_res, keep_z):
+    p = gen.make_bf16("dense", seed=3, M=M, N=N, K=K)
+    _check(p, with_bias, act, with_res, keep_z, 5, what="parts")
+    p = gen.make_dense(M, N, K, seed=4) if K % 128 == 0 else p
+    _check(p, with_bias, act, with_res, keep_z, 6, what="parts fp8")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (64, 2112, 1024), (100, 302, 512), (257, 515, 640)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_fp8_dense(M, N, K, act):
+    _check(gen.make_dense(M, N, K, seed=M + N), True, act, True, True, 8, bias_dtype=torch.bfloat16, what="fp8")
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("N", [256, 333, 1024])
+def test_grouped(bf16, N):
+    """Each expert's own bias; padding rows, empty experts and masked rows untouched, their NaN kept out."""
+    for rows in ([128, 0, 256, 100], [1, 1, 1], [300, 0, 0]):
+        if bf16:
+            p = gen.make_bf16("contiguous", seed=13, N=N, K=640, group_rows=rows, pad_rows=128)
+            p.A[p.m_indices < 0] = float("nan")
+        else:
+            p = gen.make_contiguous(rows, N, 640, seed=13, pad_rows=128)
+            p.A.view(torch.uint8)[p.m_indices < 0] = 0x7f
+        _check(p, True, "gelu", True, True, 14, what=f"contiguous {rows}")
+    for counts in ([200, 0, 77], [0, 0, 0], [1, 200, 128]):
+        if bf16:
+            p = gen.make_bf16("masked", seed=14, N=N, K=640, G=3, M_max=200, masked_m=counts)
+        else:
+            p = gen.make_masked(3, 200, N, 640, seed=14, masked_m=counts)
+        _check(p, True, "silu", True, True, 15, what=f"masked {counts}")
+
+
+@pytest.mark.parametrize("forced", ["128,128,4,2,2,1,1,0", "256,256,4,2,2,1,1,0", "64,96,2,2,4,2,1,0", "32,64,1,2,3,4,1,0",
+                                    "256,224,2,2,2,1,1,0", "256,256,4,2,2,1,1,4", "256,256,4,2,2,1,1,6",
+                                    "128,128,2,2,3,1,1,6"])
+def test_bf16_tile_structures(monkeypatch, forced):
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    for N in (520, 516, 519):
+        _check(gen.make_bf16("dense", seed=15, M=300, N=N, K=1024), True, "gelu", True, True, 16, what=f"{forced} {N}")
+
+
+@pytest.mark.parametrize("forced", ["128,128,4,2,2,1,2,0", "64,64,1,4,4,2,1,1", "64,64,1,4,4,2,1,2", "64,96,1,6,3,1,1,3",
+                                    "128,256,1,8,4,1,1,5", "256,256,4,2,2,1,1,6"])
+def test_fp8_tile_structures(monkeypatch, forced):
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    _check(gen.make_dense(200, 520, 1024, seed=17), True, "gelu", True, True, 18, what=forced)
+
+
+@pytest.mark.parametrize("M,N,K", [(96, 400, 256), (40, 131, 512), (1, 64, 4096)])
+def test_whole_numbers_bitwise(M, N, K):
+    """Every value exact in FP32 and the result in BF16's nearest-even: relu, bias and residual bit for bit."""
+    g = torch.Generator().manual_seed(12)
+    A = torch.randint(-9, 10, (M, K), generator=g).to(torch.bfloat16)
+    B = torch.randint(-9, 10, (N, K), generator=g).to(torch.bfloat16)
+    bias = torch.randint(-50, 51, (N,), generator=g).float()
+    res = torch.randint(-100, 101, (M, N), generator=g).to(torch.bfloat16)
+    p = gen.Problem("dense", A, None, B, None, bf16=True)
+    D, Z, _ = _run(p, bias, "relu", res, True)
+    z = A.double() @ B.double().T + bias.double()
+    assert torch.equal(Z, z.float().to(torch.bfloat16))
+    assert torch.equal(D, (z.clamp(min=0) + res.double()).float().to(torch.bfloat16))
+
+
+def test_residual_may_be_the_output():
+    p = gen.make_bf16("dense", seed=20, M=300, N=520, K=512)
+    res = _bf((300, 520), 21)
+    apart, _, _ = _run(p, None, "silu", res, False)
+    d = res.cuda()
+    same, _, _ = _run(p, None, "silu", d, False, d=d)
+    assert torch.equal(apart, same)
+
+
+def test_activation_far_out():
+    """Large pre-activations of both signs: the limits, no NaN; a NaN row stays in its row."""
+    vals = torch.tensor([0.0, 1e-30, 30.0, -30.0, 100.0, -100.0, 1e4, -1e4, 1e30, -1e30, 3e38, -3e38])
+    A = torch.zeros(len(vals) + 1, 64)
+    A[:len(vals), 0] = vals
+    A[-1] = float("nan")
+    B = torch.zeros(32, 64)
+    B[:, 0] = 1
+    p = gen.Problem("dense", A.to(torch.bfloat16), None, B.to(torch.bfloat16), None, bf16=True)
+    v = p.A[:-1, 0].double().numpy()
+    for act in ref.ACTS:
+        D, Z, _ = _run(p, None, act, None, True)
+        assert torch.isnan(D[-1].float()).all() and torch.isnan(Z[-1].float()).all(), act
+        with np.errstate(all="ignore"):
+            want = np.where(np.abs(v) > 50, np.maximum(v, 0) if act != "none" else v, ref.act(v, act))
+        got = check.bf16_to_f64(D)[:-1, 0]
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 1e-6), (act, got, want)
+
+
+# ------------------------------------------------------------------ backward
+def _backward(dd, z, act, m=None, G=1, bias=True, inplace=False):
+    M, N = dd.shape
+    d = dd.cuda()
+    dz = d if inplace else torch.full((M, N), float("inf"), dtype=torch.bfloat16, device="cuda")
+    db = torch.full((N,) if m is None else (G, N), float("nan"), device="cuda") if bias else None
+    dg.dg_epilogue_backward(d, None if z is None else z.cuda(), act, dz, db, None if m is None else m.cuda())
+    torch.cuda.synchronize()
+    return dz.cpu(), None if db is None else db.cpu()
+
+
+@pytest.mark.parametrize("act", ref.ACTS)
+@pytest.mark.parametrize("M,N", [(0, 40), (1, 1), (1, 512), (31, 130), (33, 1000), (200, 515), (517, 2112), (1025, 64)])
+def test_epilogue_backward(M, N, act):
+    dd, z = _bf((M, N), M + N), _bf((M, N), M + N + 1, 2.0)
+    dz, db = _backward(dd, z if act != "none" else None, act)
+    d, zz = dd.double().numpy(), z.double().numpy()
+    want = d * ref.slope(zz, act)
+    slack = 2.0 ** -20 * np.abs(d) * (1 + np.abs(zz))
+    assert np.all(np.abs(dz.double().numpy() - want) <= 2.0 ** -8 * np.abs(want) + slack)
+    assert np.all(np.abs(db.double().numpy() - want.sum(0)) <= slack.sum(0) + (M + 8) * 2.0 ** -24 * np.abs(want).sum(0))
+    again, db2 = _backward(dd, z, act, inplace=True)
+    assert torch.equal(again, dz) and torch.equal(db2, db)
+
+
+@pytest.mark.parametrize("act", ref.ACTS[1:])
+def test_slope_against_differences(act):
+    """dZ for dD = 1 is the derivative of the forward activation, by central differences in 64 bits."""
+    z = torch.linspace(-8, 8, 4096).to(torch.bfloat16)
+    if act == "relu":
+        z = z[z.abs() > 0.01]
+    z = z[None, :]
+    _, db = _backward(torch.ones_like(z), z, act)
+    v, h = z[0].double().numpy(), 1e-5
+    want = (ref.act(v + h, act) - ref.act(v - h, act)) / (2 * h)
+    # the difference quotient is off by h^2/6 of the third derivative and 2^-52 |z| / h of rounding: under 1e-9
+    assert np.all(np.abs(db.double().numpy() - want) <= 2.0 ** -20 * (1 + np.abs(v)) + 1e-9)
+
+
+def test_epilogue_backward_far_out():
+    """No infinity meets a zero: slopes of huge pre-activations are 0 or 1, of NaN NaN."""
+    inf = float("inf")
+    z = torch.tensor([[inf, -inf, 1e30, -1e30, 300.0, -300.0, float("nan"), 0.0]]).to(torch.bfloat16)
+    for act in ref.ACTS[1:]:
+        dz, _ = _backward(torch.ones_like(z), z, act)
+        got = dz[0].float().tolist()
+        assert [got[i] for i in (0, 2, 4)] == [1.0] * 3 and all(abs(got[i]) == 0 for i in (1, 3, 5)), (act, got)
+        assert got[6] != got[6]
+
+
+@pytest.mark.parametrize("N", [64, 515, 1024])
+@pytest.mark.parametrize("rows", [[128, 0, 200, 100], [1, 1, 1], [0, 0, 5], [640, 3, 0]])
+def test_grouped_epilogue_backward(N, rows):
+    """Each expert's own bias gradient, zeros in padding rows, rows past the segments untouched."""
+    m = []
+    for g, c in enumerate(rows):
+        m += [g] * c + [-1] * (-c % 128)
+    m += [-2] * 128
+    m = torch.tensor(m, dtype=torch.int32)
+    M, G = len(m), len(rows)
+    dd, z = _bf((M, N), 1), _bf((M, N), 2)
+    dd[m < 0] = float("nan")
+    z[m < 0] = float("nan")
+    dz, db = _backward(dd, z, "gelu", m, G)
+    keep = (m >= 0).numpy()
+    d, zz = dd.double().numpy(), z.double().numpy()
+    want = d[keep] * ref.slope(zz[keep], "gelu")
+    slack = 2.0 ** -20 * np.abs(d[keep]) * (1 + np.abs(zz[keep]))
+    assert np.all(np.abs(dz.double().numpy()[keep] - want) <= 2.0 ** -8 * np.abs(want) + slack)
+    assert (dz[m == -1] == 0).all() and torch.isinf(dz[m == -2].float()).all()
+    owner = m.numpy()[keep]
+    for g in range(G):
+        w, s = want[owner == g], slack[owner == g]
+        err = np.abs(db[g].double().numpy() - w.sum(0))
+        assert np.all(err <= s.sum(0) + (len(w) + 8) * 2.0 ** -24 * np.abs(w).sum(0)), g
+    # without a bias gradient dZ is the same
+    again, _ = _backward(dd, z, "gelu", m, G, bias=False)
+    assert torch.equal(again.view(torch.int16), dz.view(torch.int16))
+
+
+# ------------------------------------------------------------------ NN / TN
+def _close(D, want, what):
+    check.assert_close(check.bf16_to_f64(D), want, what)
+
+
+@pytest.mark.parametrize("with_c", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 64), (5, 129, 192), (64, 2112, 1024), (257, 515, 640), (517, 1536, 2112), (300, 7, 64)])
+def test_bf16_nn(M, N, K, with_c):
+    A, B = _bf((M, K), 1), _bf((K, N), 2)
+    C = torch.randn((M, N), generator=torch.Generator().manual_seed(3)) if with_c else None
+    D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_bf16_gemm_nn(A.cuda(), B.cuda(), None if C is None else C.cuda(), D)
+    _close(D, A.double().numpy() @ B.double().numpy() + (0 if C is None else C.double().numpy()), f"nn {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("with_c", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (16, 24, 63), (129, 5, 65), (2112, 64, 517), (515, 257, 640), (64, 520, 1),
+                                   (1536, 2112, 200)])
+def test_bf16_tn(M, N, K, with_c):
+    """Any K: the reduction over the tokens of a batch."""
+    A, B = _bf((K, M), 1), _bf((K, N), 2)
+    C = torch.randn((M, N), generator=torch.Generator().manual_seed(3)) if with_c else None
+    D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    # a NaN left in the workspace by an earlier call must not come in through the padding of K
+    nan = torch.full((max(K, 1) + 100, M), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_bf16_gemm_tn(nan, torch.zeros((nan.shape[0], N), dtype=torch.bfloat16, device="cuda"), None, torch.empty_like(D))
+    dg.dg_bf16_gemm_tn(A.cuda(), B.cuda(), None if C is None else C.cuda(), D)
+    _close(D, A.double().numpy().T @ B.double().numpy() + (0 if C is None else C.double().numpy()), f"tn {M}x{N}x{K}")
+
+
+def test_bf16_tn_without_tokens():
+    D = torch.full((40, 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    e = lambda n: torch.empty((0, n), dtype=torch.bfloat16, device="cuda")
+    dg.dg_bf16_gemm_tn(e(40), e(24), None, D)
+    assert (D == 0).all()
+    C = torch.randn((40, 24), device="cuda")
+    dg.dg_bf16_gemm_tn(e(40), e(24), C, D)
+    assert torch.equal(D, C.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("N", [64, 515])
+def test_bf16_nn_contiguous(N):
+    rows, K = [128, 0, 200, 100], 320
+    m = []
+    for g, c in enumerate(rows):
+        m += [g] * c + [-1] * (-c % 128)
+    m = torch.tensor(m + [-2] * 128, dtype=torch.int32)
+    A, B = _bf((len(m), K), 1), _bf((4, K, N), 2)
+    A[m < 0] = float("nan")
+    D = torch.full((len(m), N), float("inf"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_m_grouped_bf16_gemm_nn_contiguous(A.cuda(), B.cuda(), m.cuda(), None, D)
+    D = D.cpu()
+    keep = m >= 0
+    want = np.stack([A[r].double().numpy() @ B[int(m[r])].double().numpy() for r in range(len(m)) if m[r] >= 0])
+    _close(D[keep], want, "nn contiguous")
+    assert torch.isinf(D[~keep].float()).all()
+
+
+@pytest.mark.parametrize("with_c", [False, True])
+@pytest.mark.parametrize("ks,M,N", [([128], 40, 72), ([128, 0, 256], 257, 515), ([0, 0], 16, 16), ([384, 128, 0, 640], 512, 1024),
+                                    ([128] * 9, 33, 520)])
+def test_bf16_k_grouped(ks, M, N, with_c):
+    K, G = sum(ks) + 256, len(ks)               # rows past the segments: never read into a result
+    A, B = _bf((K, M), 1), _bf((K, N), 2)
+    A[sum(ks):] = float("nan")
+    C = torch.randn((G, M, N), generator=torch.Generator().manual_seed(3)) if with_c else None
+    D = torch.full((G, M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_k_grouped_bf16_gemm_tn_contiguous(A.cuda(), B.cuda(), torch.tensor(ks, dtype=torch.int32).cuda(),
+                                            None if C is None else C.cuda(), D)
+    at, want = 0, np.zeros((G, M, N)) if C is None else C.double().numpy().copy()
+    for g, k in enumerate(ks):
+        want[g] += A[at:at + k].double().numpy().T @ B[at:at + k].double().numpy()
+        at += k
+    _close(D, want, f"k-grouped {ks}")
+
+
+def test_gradients_of_a_layer_against_differences():
+    """dA, dB, dbias and the residual's gradient of <W, D> against differences of the forward kernels.
+
+    Whole numbers small enough that Z and D are exact in BF16 and no relu argument changes sign, so one
+    step of 1 in any input changes <W, D> by exactly its gradient."""
+    g = torch.Generator().manual_seed(5)
+    M, N, K = 6, 64, 64
+    A = torch.randint(-1, 2, (M, K), generator=g).float()
+    B = torch.randint(-1, 2, (N, K), generator=g).float()
+    bias = torch.where(torch.rand(N, generator=g) < 0.5, 80.0, -80.0)     # |A . B| <= 64, moved by at most 2
+    res = torch.randint(-8, 9, (M, N), generator=g).float()
+    W = torch.randint(-1, 2, (M, N), generator=g).float()
+    h = lambda t: t.to(torch.bfloat16).cuda()
+
+    def forward(a, b, bias, r):
+        D, Z = (torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        dg.dg_bf16_gemm_nt_epilogue(h(a), h(b), D, bias=bias.cuda(), activation="relu", residual=h(r), Z=Z)
+        return float((D.double().cpu() * W.double()).sum()), Z
+
+    at, Z = forward(A, B, bias, res)
+    dz = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    db = torch.empty(N, device="cuda")
+    dg.dg_epilogue_backward(h(W), Z, "relu", dz, db)
+    dA = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    dB = torch.empty((N, K), dtype=torch.bfloat16, device="cuda")
+    dg.dg_bf16_gemm_nn(dz, h(B), None, dA)
+    dg.dg_bf16_gemm_tn(dz, h(A), None, dB)
+    step = lambda t, i: t.clone().index_put_(tuple(torch.tensor(j) for j in i), torch.tensor(1.0), accumulate=True)
+    for i in [(0, 0), (3, 17), (5, 63)]:
+        assert forward(step(A, i), B, bias, res)[0] - at == float(dA[i]), ("A", i)
+        assert forward(A, step(B, i), bias, res)[0] - at == float(dB[i]), ("B", i)
+        assert forward(A, B, bias, step(res, i))[0] - at == float(W[i]), ("residual", i)
+    for n in (0, 9, 63):
+        assert forward(A, B, step(bias, (n,)), res)[0] - at == float(db[n]), ("bias", n)
+
+
+def test_layer_replays_from_a_graph():
+    """Forward and backward of a layer captured once on a side stream; every replay matches eager calls on
+    the same contents, with eager work between the replays."""
+    M, N, K = 200, 320, 256
+    x, w = _bf((M, K), 1).cuda(), _bf((N, K), 2, 0.1).cuda()
+    bias, res, dd = torch.randn(N, device="cuda"), _bf((M, N), 3).cuda(), _bf((M, N), 4).cuda()
+
+    def buffers():
+        n = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+        return [n(M, N), n(M, N), n(M, N), torch.zeros(N, device="cuda"), n(M, K), n(N, K)]
+
+    def calls(b):
+        dg.dg_bf16_gemm_nt_epilogue(x, w, b[0], bias=bias, activation="gelu", residual=res, Z=b[1])
+        dg.dg_epilogue_backward(dd, b[1], "gelu", b[2], b[3])
+        dg.dg_bf16_gemm_nn(b[2], w, None, b[4])
+        dg.dg_bf16_gemm_tn(b[2], x, None, b[5])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    captured = buffers()
+    with torch.cuda.stream(side):
+        calls(captured)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        calls(captured)
+    for seed in range(4):
+        x.copy_(_bf((M, K), 10 + seed))
+        torch.cuda.synchronize()
+        eager = buffers()
+        calls(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(captured, eager)):
+            assert torch.equal(a, b), (seed, i)
