@@ -98,76 +98,95 @@ __device__ __forceinline__ float slope(float z) {
 }
 
 // dZ = dD slope(Z), and the column sums of dZ (FP32, before its rounding) of the
-// workgroup's rows.  A workgroup takes 512 columns of `chunk` rows: 8 columns a
-// lane, its four waves every fourth row, whose sums meet in LDS and are added in
-// wave order.  Contiguous form: the rows of a chunk (a divisor of 128) belong to
-// the expert of its first row; padding rows (-1) get dZ = 0, rows past the last
-// segment are untouched.  partial [chunks][N], or nullptr: no bias gradient.
+// workgroup's rows.  A workgroup takes 512 columns of kChunk rows: 8 columns a
+// lane, its four waves every fourth row.  A wave's loads are all issued before
+// its first use of one (kChunk / 4 rows of dD and Z in flight), the waves' sums
+// meet in LDS and are added in wave order.  Contiguous form: the rows of a chunk
+// (kChunk divides 128) belong to the expert of its first row; padding rows (-1)
+// get dZ = 0, rows past the last segment are untouched.  partial [chunks][N], or
+// nullptr: no bias gradient.
+constexpr int kChunk = 16;
+constexpr int kWaveRows = kChunk / 4;
+struct BackwardArgs {
+    const u16* dD;
+    const u16* Z;
+    const int* m_indices;
+    u16* dZ;
+    float* partial;
+    int rows, N, G;
+};
 template <int ACT, bool VEC>
-__global__ void __launch_bounds__(256)
-dg_epilogue_backward_kernel(const u16* __restrict__ dD, const u16* __restrict__ Z, const int* __restrict__ m_indices,
-                            u16* __restrict__ dZ, float* __restrict__ partial, int rows, int N, int G, int chunk) {
+__global__ void __launch_bounds__(256) dg_epilogue_backward_kernel(const BackwardArgs a) {
+    const u16* __restrict__ dD = a.dD;
+    const u16* __restrict__ Z = a.Z;
+    const int* __restrict__ m_indices = a.m_indices;
+    u16* __restrict__ dZ = a.dZ;
+    float* __restrict__ partial = a.partial;
+    const int rows = a.rows, N = a.N, G = a.G;
     __shared__ float sums[4][512];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = (int)blockIdx.y * 512;
-    const int r0 = (int)blockIdx.x * chunk;
-    const int r1 = rows - r0 < chunk ? rows : r0 + chunk;
+    const int r0 = (int)blockIdx.x * kChunk;
     auto col = [&](int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 64 * i; };
+    // row i of this wave, its expert (a padding row's or none: below 0), and whether it is read
+    int expert[kWaveRows];
+#pragma unroll
+    for (int i = 0; i < kWaveRows; ++i) {
+        const int r = r0 + wave + 4 * i;
+        expert[i] = r >= rows ? kPadding - 1 : m_indices ? m_indices[r] : 0;
+    }
+    const int owner = m_indices ? m_indices[r0] : 0;
+    u32x4 d[kWaveRows], z[kWaveRows];      // eight BF16 each
+    auto load = [&](const u16* p) {
+        u32x4 w = {0u, 0u, 0u, 0u};
+        if constexpr (VEC) {
+            if (col(0) < N) w = *(const u32x4*)(p + col(0));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col(i) < N) w[i >> 1] |= (u32)p[col(i)] << (16 * (i & 1));
+        }
+        return w;
+    };
+#pragma unroll
+    for (int i = 0; i < kWaveRows; ++i) {
+        d[i] = z[i] = u32x4{0u, 0u, 0u, 0u};
+        if ((u32)expert[i] < (u32)G) {
+            const u64 at = (u64)(r0 + wave + 4 * i) * N;
+            d[i] = load(dD + at);
+            if constexpr (ACT != DG_ACT_NONE) z[i] = load(Z + at);
+        }
+    }
     float acc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    auto load = [&](const u16* p, float (&v)[8]) {
-        if constexpr (VEC) {
-            u32x4 w = {0u, 0u, 0u, 0u};
-            if (col(0) < N) w = *(const u32x4*)(p + col(0));
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = bf16_lo(w[i]);
-                v[2 * i + 1] = bf16_hi(w[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = col(i) < N ? __builtin_bit_cast(float, (u32)p[col(i)] << 16) : 0.f;
-        }
-    };
-    const int owner = m_indices ? m_indices[r0] : 0;
-#pragma unroll 4
-    for (int r = r0 + wave; r < r1; r += 4) {
-        const int g = m_indices ? m_indices[r] : 0;
+    for (int i = 0; i < kWaveRows; ++i) {
+        const bool real = (u32)expert[i] < (u32)G;
+        if (!real && expert[i] != kPadding) continue;
         float v[8];
-        if ((u32)g < (u32)G) {
-            load(dD + (u64)r * N, v);
-            if constexpr (ACT != DG_ACT_NONE) {
-                float z[8];
-                load(Z + (u64)r * N, z);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= slope<ACT>(z[i]);
-            }
-            if (g == owner) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += v[i];
-            }
-        } else if (g == kPadding) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        } else {
-            continue;
+        for (int e = 0; e < 8; ++e) {
+            v[e] = e & 1 ? bf16_hi(d[i][e >> 1]) : bf16_lo(d[i][e >> 1]);
+            if constexpr (ACT != DG_ACT_NONE)
+                if (real) v[e] *= slope<ACT>(e & 1 ? bf16_hi(z[i][e >> 1]) : bf16_lo(z[i][e >> 1]));
+            if (real && expert[i] == owner) acc[e] += v[e];
         }
         if (!dZ) continue;
-        u16* dst = dZ + (u64)r * N;
+        u16* dst = dZ + (u64)(r0 + wave + 4 * i) * N;
         if constexpr (VEC) {
             if (col(0) < N)
                 *(u32x4*)(dst + col(0)) = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
                                                 to_bf16x2(v[6], v[7])};
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col(i) < N) dst[col(i)] = to_bf16(v[i]);
+            for (int e = 0; e < 8; ++e)
+                if (col(e) < N) dst[col(e)] = to_bf16(v[e]);
         }
     }
     if (!partial) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[wave][col(i) - c0] = acc[i];
+    for (int e = 0; e < 8; ++e) sums[wave][col(e) - c0] = acc[e];
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -176,26 +195,43 @@ dg_epilogue_backward_kernel(const u16* __restrict__ dD, const u16* __restrict__ 
     }
 }
 
-// dbias[g][n]: the partial sums of the chunks that belong to expert g, in chunk
-// order within each of four quarters, then the quarters in order: the same sum
-// on every run.
-__global__ void __launch_bounds__(256)
-dg_bias_sum_kernel(const float* __restrict__ partial, const int* __restrict__ m_indices, float* __restrict__ dbias,
-                   int chunks, int chunk, int N) {
-    __shared__ float sums[4][64];
-    const int lane = threadIdx.x & 63, quarter = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// dbias[g][n]: the partial sums of the chunks that belong to expert g.  Sixteen
+// waves share 64 columns, each a sixteenth of the chunks in order, eight loads in
+// flight; then the sixteenths in order: the same sum on every run.
+constexpr int kSumWaves = 16;
+struct BiasSumArgs {
+    const float* partial;
+    const int* m_indices;
+    float* dbias;
+    int chunks, N;
+};
+__global__ void __launch_bounds__(64 * kSumWaves) dg_bias_sum_kernel(const BiasSumArgs a) {
+    const float* __restrict__ partial = a.partial;
+    const int* __restrict__ m_indices = a.m_indices;
+    __shared__ float sums[kSumWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = (int)blockIdx.x * 64 + lane, g = blockIdx.y;
-    const int each = (chunks + 3) / 4;
-    const int first = quarter * each, last = chunks - first < each ? chunks : first + each;
+    const int each = (a.chunks + kSumWaves - 1) / kSumWaves;
+    const int first = wave * each, last = a.chunks - first < each ? a.chunks : first + each;
     float s = 0.f;
-#pragma unroll 8
-    for (int c = first; c < last; ++c) {
-        if (m_indices && m_indices[(u64)c * chunk] != g) continue;
-        s += n < N ? partial[(u64)c * N + n] : 0.f;
+    for (int c = first; c < last; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool mine = c + i < last && (!m_indices || m_indices[(u64)(c + i) * kChunk] == g);
+            v[i] = mine && n < a.N ? partial[(u64)(c + i) * a.N + n] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[i];
     }
-    sums[quarter][lane] = s;
+    sums[wave][lane] = s;
     __syncthreads();
-    if (quarter == 0 && n < N) dbias[(u64)g * N + n] = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
+    if (wave == 0 && n < a.N) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSumWaves; ++w) t += sums[w][lane];
+        a.dbias[(u64)g * a.N + n] = t;
+    }
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -206,10 +242,9 @@ dg_status launched(const char* what) {
 }
 
 template <int ACT>
-void launch_backward(dim3 grid, hipStream_t stream, const u16* dD, const u16* Z, const int* m_indices, u16* dZ,
-                     float* partial, int rows, int N, int G, int chunk) {
-    hipLaunchKernelGGL(N % 8 == 0 ? (dg_epilogue_backward_kernel<ACT, true>) : (dg_epilogue_backward_kernel<ACT, false>),
-                       grid, dim3(256), 0, stream, dD, Z, m_indices, dZ, partial, rows, N, G, chunk);
+void launch_backward(dim3 grid, hipStream_t stream, const BackwardArgs& a) {
+    hipLaunchKernelGGL(a.N % 8 == 0 ? (dg_epilogue_backward_kernel<ACT, true>) : (dg_epilogue_backward_kernel<ACT, false>),
+                       grid, dim3(256), 0, stream, a);
 }
 
 dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_t* m_indices, void* dZ, float* dbias,
@@ -225,8 +260,7 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
     if (G > 65535 || N > 65535 * 512)
         return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many groups or columns for one launch");
     const hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
-    constexpr int chunk = 32;
-    const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
+    const int chunks = (int)(((int64_t)rows + kChunk - 1) / kChunk);
     float* partial = nullptr;
     if (dbias && chunks > 0) {
         dg_status s = stream_scratch(stream_ptr, (size_t)chunks * (size_t)N * sizeof(float), &partial);
@@ -234,18 +268,17 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
     }
     if (chunks > 0 && (dZ || dbias)) {
         const dim3 grid(chunks, (N + 511) / 512);
-        const u16 *d = static_cast<const u16*>(dD), *z = static_cast<const u16*>(Z);
-        u16* out = static_cast<u16*>(dZ);
         auto* f = act == DG_ACT_RELU ? launch_backward<DG_ACT_RELU> : act == DG_ACT_SILU ? launch_backward<DG_ACT_SILU>
                 : act == DG_ACT_GELU ? launch_backward<DG_ACT_GELU>
                 : act == DG_ACT_GELU_TANH ? launch_backward<DG_ACT_GELU_TANH> : launch_backward<DG_ACT_NONE>;
-        f(grid, stream, d, z, m_indices, out, partial, rows, N, G, chunk);
+        f(grid, stream, BackwardArgs{static_cast<const u16*>(dD), static_cast<const u16*>(Z), m_indices,
+                                     static_cast<u16*>(dZ), partial, rows, N, G});
         dg_status s = launched("epilogue_backward");
         if (s != DG_OK) return s;
     }
     if (dbias) {
-        hipLaunchKernelGGL(dg_bias_sum_kernel, dim3((N + 63) / 64, G), dim3(256), 0, stream, partial, m_indices, dbias,
-                           chunks, chunk, N);
+        hipLaunchKernelGGL(dg_bias_sum_kernel, dim3((N + 63) / 64, G), dim3(64 * kSumWaves), 0, stream,
+                           BiasSumArgs{partial, m_indices, dbias, chunks, N});
         return launched("epilogue_backward (bias)");
     }
     return DG_OK;

@@ -704,12 +704,44 @@ m_grouped_fp4_fp4_gemm_nt_masked = dg_m_grouped_fp4_fp4_gemm_nt_masked
 
 
 # ---------------------------------------------------------------- tokens to experts and back
-def _typed(t: torch.Tensor, name: str, dtype, shape):
+# The calls of a decode step are a few microseconds of GPU work each, so the checks of these functions are
+# kept to one short pass a tensor: _arg() returns the address, and only a tensor that fails goes on to
+# _refuse(), which says why.
+def _refuse(t, name: str, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     _dev(t, name)
+    raise ValueError(f"{name} is not on the other tensors' device")
+
+
+def _arg(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dtype, shape, dev: int):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
+
+
+def _on(t, name: str) -> int:
+    """The device of a call's first tensor, which has to be the current one."""
+    d = t.get_device()
+    if d < 0 or d != _cur_device():
+        if name != "expert_ids" and t.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"{name} must be bfloat16 (FP8 forms: E4M3), got {t.dtype}")
+        _dev(t, name)
+    return d
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return _cur_raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+_BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def moe_sorted_rows(T: int, topk: int, num_experts: int) -> int:
@@ -720,11 +752,11 @@ def moe_sorted_rows(T: int, topk: int, num_experts: int) -> int:
     return n
 
 
-def _ids(expert_ids, pos):
+def _ids(expert_ids):
+    if expert_ids.dtype is not _I32:
+        raise TypeError(f"expert_ids must be int32, got {expert_ids.dtype}")
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be int32 [T, topk]")
-    _typed(expert_ids, "expert_ids", torch.int32, expert_ids.shape)
-    _typed(pos, "pos", torch.int32, expert_ids.shape)
     return expert_ids.shape
 
 
@@ -734,43 +766,51 @@ def dg_moe_sort_contiguous(expert_ids, num_experts, pos, m_indices, ks, stream=N
     pos [T,topk]: each assignment's row (-1: dropped); m_indices [rows] as the contiguous products take
     it (-1 padding, -2 past the last segment); ks [num_experts]: segment rows, multiples of 128.
     """
-    T, k = _ids(expert_ids, pos)
-    _typed(m_indices, "m_indices", torch.int32, (m_indices.numel(),))
-    _typed(ks, "ks", torch.int32, (num_experts,))
-    _check(lib.dg_moe_sort_contiguous(_ptr(expert_ids), _ptr(pos), _ptr(m_indices), _ptr(ks), T, k, num_experts,
-                                      m_indices.numel(), _stream(stream)))
+    shape = _ids(expert_ids)
+    dev = _on(expert_ids, "expert_ids")
+    rows = m_indices.numel()
+    status = lib.dg_moe_sort_contiguous(
+        _arg(expert_ids, "expert_ids", _I32, shape, dev), _arg(pos, "pos", _I32, shape, dev),
+        _arg(m_indices, "m_indices", _I32, (rows,), dev), _arg(ks, "ks", _I32, (num_experts,), dev), shape[0], shape[1],
+        num_experts, rows, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return pos
 
 
 def dg_moe_sort_masked(expert_ids, num_experts, M_max, pos, masked_m, stream=None):
     """Sort the assignments by expert into the masked layout: expert g's rows start at g * M_max."""
-    T, k = _ids(expert_ids, pos)
-    _typed(masked_m, "masked_m", torch.int32, (num_experts,))
-    _check(lib.dg_moe_sort_masked(_ptr(expert_ids), _ptr(pos), _ptr(masked_m), T, k, num_experts, M_max,
-                                  _stream(stream)))
+    shape = _ids(expert_ids)
+    dev = _on(expert_ids, "expert_ids")
+    status = lib.dg_moe_sort_masked(
+        _arg(expert_ids, "expert_ids", _I32, shape, dev), _arg(pos, "pos", _I32, shape, dev),
+        _arg(masked_m, "masked_m", _I32, (num_experts,), dev), shape[0], shape[1], num_experts, M_max,
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return pos
 
 
-def _token_rows(X, name, pos, rows, m_indices):
-    """Shapes of a token tensor X [T,width], pos [T,topk] and rows [R,width] or [G,M_max,width]."""
-    if X.dim() != 2 or pos.dim() != 2 or rows.dim() not in (2, 3):
-        raise ValueError(f"{name} must be [T, width], pos [T, topk], rows [R, width] or [G, M_max, width]")
+def _token_rows(X, name, pos, rows, rows_name="rows"):
+    """(T, topk, rows, width, shape of the rows) of X [T,width], pos [T,topk] and rows [R,width] or [G,M_max,width]."""
+    shape = rows.shape
+    if X.dim() != 2 or pos.dim() != 2 or len(shape) not in (2, 3):
+        raise ValueError(f"{name} must be [T, width], pos [T, topk], {rows_name} [R, width] or [G, M_max, width]")
     T, width = X.shape
-    _typed(X, name, torch.bfloat16, (T, width))
-    _typed(pos, "pos", torch.int32, (T, pos.shape[1]))
-    if rows.shape[-1] != width:
-        raise ValueError(f"rows must be {width} wide like {name}, got {tuple(rows.shape)}")
-    n = rows.numel() // width
-    if m_indices is not None:
-        _typed(m_indices, "m_indices", torch.int32, (n,))
-    return T, pos.shape[1], n, width
+    if shape[-1] != width:
+        raise ValueError(f"{rows_name} must be {width} wide like {name}, got {tuple(shape)}")
+    return T, pos.shape[1], shape[0] if len(shape) == 2 else shape[0] * shape[1], width, shape
 
 
 def dg_moe_dispatch_bf16(X, pos, m_indices, rows, stream=None):
     """rows[pos[t,j]] = X[t]; contiguous layout (m_indices given): padding rows are cleared."""
-    T, k, n, H = _token_rows(X, "X", pos, rows, m_indices)
-    _typed(rows, "rows", torch.bfloat16, rows.shape)
-    _check(lib.dg_moe_dispatch_bf16(_ptr(X), _ptr(pos), _ptr(m_indices), _ptr(rows), T, k, n, H, _stream(stream)))
+    T, k, n, H, shape = _token_rows(X, "X", pos, rows)
+    dev = _on(X, "X")
+    status = lib.dg_moe_dispatch_bf16(
+        _arg(X, "X", _BF, (T, H), dev), _arg(pos, "pos", _I32, (T, k), dev), _opt(m_indices, "m_indices", _I32, (n,), dev),
+        _arg(rows, "rows", _BF, shape, dev), T, k, n, H, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return rows
 
 
@@ -780,26 +820,33 @@ def dg_moe_dispatch_fp8(X, pos, m_indices, rows, sf, stream=None):
     sf: float32 [H/128, R] (rows [R,H]) or [G, H/128, M_max] (rows [G,M_max,H]); int32 words of packed UE8M0
     scales in the same place ([ceil(H/512), R], [G, ceil(H/512), M_max]) select power-of-two scales.
     """
-    T, k, n, H = _token_rows(X, "X", pos, rows, m_indices)
-    _fp8(rows, "rows")
-    ue8m0 = sf.dtype == torch.int32
-    kb = _cdiv(H, 512) if ue8m0 else H // 128
-    _typed(sf, "sf", torch.int32 if ue8m0 else torch.float32, (*rows.shape[:-2], kb, rows.shape[-2]))
-    _check(lib.dg_moe_dispatch_fp8(_ptr(X), _ptr(pos), _ptr(m_indices), _ptr(rows), _ptr(sf), T, k, n,
-                                   rows.shape[-2], H, int(ue8m0), _stream(stream)))
+    T, k, n, H, shape = _token_rows(X, "X", pos, rows)
+    dev = _on(X, "X")
+    dtype = rows.dtype
+    if dtype not in (torch.float8_e4m3fn, torch.uint8):
+        _fp8(rows, "rows")
+    ue8m0 = sf.dtype is _I32
+    kb = (H + 511) // 512 if ue8m0 else H // 128
+    status = lib.dg_moe_dispatch_fp8(
+        _arg(X, "X", _BF, (T, H), dev), _arg(pos, "pos", _I32, (T, k), dev), _opt(m_indices, "m_indices", _I32, (n,), dev),
+        _arg(rows, "rows", dtype, shape, dev),
+        _arg(sf, "sf", _I32 if ue8m0 else _F32, (*shape[:-2], kb, shape[-2]), dev), T, k, n, shape[-2], H, ue8m0,
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return rows
 
 
 def dg_moe_combine(rows, pos, weights, residual, Y, stream=None):
     """Y[t] = residual[t] + sum_j weights[t,j] * rows[pos[t,j]] (weights, residual may be None: 1, none)."""
-    T, k, n, N = _token_rows(Y, "Y", pos, rows, None)
-    _typed(rows, "rows", torch.bfloat16, rows.shape)
-    if weights is not None:
-        _typed(weights, "weights", torch.float32, (T, k))
-    if residual is not None:
-        _typed(residual, "residual", torch.bfloat16, (T, N))
-    _check(lib.dg_moe_combine(_ptr(rows), _ptr(pos), _ptr(weights), _ptr(residual), _ptr(Y), T, k, n, N,
-                              _stream(stream)))
+    T, k, n, N, shape = _token_rows(Y, "Y", pos, rows)
+    dev = _on(Y, "Y")
+    status = lib.dg_moe_combine(
+        _arg(rows, "rows", _BF, shape, dev), _arg(pos, "pos", _I32, (T, k), dev),
+        _opt(weights, "weights", _F32, (T, k), dev), _opt(residual, "residual", _BF, (T, N), dev),
+        _arg(Y, "Y", _BF, (T, N), dev), T, k, n, N, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return Y
 
 
@@ -808,18 +855,17 @@ def dg_moe_combine_backward(dY, rows, pos, weights, m_indices, d_rows, d_weights
 
     d_weights None: not computed (rows may be None).  Padding rows of the contiguous layout are cleared.
     """
-    T, k, n, N = _token_rows(dY, "dY", pos, d_rows, m_indices)
-    _typed(d_rows, "d_rows", torch.bfloat16, d_rows.shape)
-    if rows is not None:
-        _typed(rows, "rows", torch.bfloat16, d_rows.shape)
-    elif d_weights is not None:
+    T, k, n, N, shape = _token_rows(dY, "dY", pos, d_rows, "d_rows")
+    if rows is None and d_weights is not None:
         raise ValueError("d_weights needs rows")
-    if weights is not None:
-        _typed(weights, "weights", torch.float32, (T, k))
-    if d_weights is not None:
-        _typed(d_weights, "d_weights", torch.float32, (T, k))
-    _check(lib.dg_moe_combine_backward(_ptr(dY), _ptr(rows), _ptr(pos), _ptr(weights), _ptr(m_indices), _ptr(d_rows),
-                                       _ptr(d_weights), T, k, n, N, _stream(stream)))
+    dev = _on(dY, "dY")
+    status = lib.dg_moe_combine_backward(
+        _arg(dY, "dY", _BF, (T, N), dev), _opt(rows, "rows", _BF, shape, dev), _arg(pos, "pos", _I32, (T, k), dev),
+        _opt(weights, "weights", _F32, (T, k), dev), _opt(m_indices, "m_indices", _I32, (n,), dev),
+        _arg(d_rows, "d_rows", _BF, shape, dev), _opt(d_weights, "d_weights", _F32, (T, k), dev), T, k, n, N,
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return d_rows
 
 
@@ -837,26 +883,28 @@ class _Epilogue(ctypes.Structure):      # dg_epilogue
 
 
 def _activation(name) -> int:
-    if name not in ACTIVATIONS:
+    act = ACTIVATIONS.get(name)
+    if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
-    return ACTIVATIONS[name]
+    return act
 
 
-def _epilogue(D, lead, bias, activation, residual, Z):
-    """The dg_epilogue of D [*, N] with bias [*lead, N]."""
-    e = _Epilogue(activation=_activation(activation))
+def _epilogue(D, bias_shape, bias, activation, residual, Z, dev):
+    """The dg_epilogue of D with bias of this shape."""
+    shape, wide = D.shape, 0
     if bias is not None:
-        if bias.dtype not in (torch.float32, torch.bfloat16):
+        wide = bias.dtype is not _F32
+        if wide and bias.dtype is not _BF:
             raise TypeError(f"bias must be float32 or bfloat16, got {bias.dtype}")
-        _typed(bias, "bias", bias.dtype, (*lead, D.shape[-1]))
-        e.bias, e.bias_type = bias.data_ptr(), int(bias.dtype == torch.bfloat16)
-    if residual is not None:
-        _typed(residual, "residual", torch.bfloat16, D.shape)
-        e.residual = residual.data_ptr()
-    if Z is not None:
-        _typed(Z, "Z", torch.bfloat16, D.shape)
-        e.Z = Z.data_ptr()
-    return ctypes.byref(e)
+        bias = _arg(bias, "bias", _BF if wide else _F32, bias_shape, dev)
+    return ctypes.byref(_Epilogue(bias, wide, _activation(activation), _opt(residual, "residual", _BF, shape, dev),
+                                  _opt(Z, "Z", _BF, shape, dev)))
+
+
+def _fp8_arg(t, name, shape, dev):
+    if t.dtype is not torch.uint8:
+        return _arg(t, name, torch.float8_e4m3fn, shape, dev)
+    return _arg(t, name, torch.uint8, shape, dev)
 
 
 def dg_bf16_gemm_nt_epilogue(A, B, D, bias=None, activation="none", residual=None, Z=None, stream=None):
@@ -865,10 +913,12 @@ def dg_bf16_gemm_nt_epilogue(A, B, D, bias=None, activation="none", residual=Non
     A [M,K], B [N,K], D, residual and Z [M,N] bfloat16, bias [N] float32 or bfloat16."""
     M, K = A.shape
     N = B.shape[0]
-    _bf(A, "A", (M, K)); _bf(B, "B", (N, K))
-    _out(D, (M, N))
-    e = _epilogue(D, (), bias, activation, residual, Z)
-    _check(lib.dg_bf16_gemm_nt_epilogue(_ptr(A), _ptr(B), e, _ptr(D), M, N, K, _stream(stream)))
+    dev = _on(A, "A")
+    e = _epilogue(D, (N,), bias, activation, residual, Z, dev)
+    status = lib.dg_bf16_gemm_nt_epilogue(_arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (N, K), dev), e,
+                                          _arg(D, "D", _BF, (M, N), dev), M, N, K, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
@@ -877,12 +927,13 @@ def dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(A, B, m_indices, D, bias=None,
     """Contiguous M-grouped form: B [G,N,K], bias [G,N], m_indices int32 [M]."""
     M, K = A.shape
     G, N = B.shape[0], B.shape[1]
-    _bf(A, "A", (M, K)); _bf(B, "B", (G, N, K))
-    _typed(m_indices, "m_indices", torch.int32, (M,))
-    _out(D, (M, N))
-    e = _epilogue(D, (G,), bias, activation, residual, Z)
-    _check(lib.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(_ptr(A), _ptr(B), _ptr(m_indices), e, _ptr(D), M, N, K, G,
-                                                             _stream(stream)))
+    dev = _on(A, "A")
+    e = _epilogue(D, (G, N), bias, activation, residual, Z, dev)
+    status = lib.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(
+        _arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (G, N, K), dev), _arg(m_indices, "m_indices", _I32, (M,), dev),
+        e, _arg(D, "D", _BF, (M, N), dev), M, N, K, G, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
@@ -891,60 +942,62 @@ def dg_m_grouped_bf16_gemm_nt_masked_epilogue(A, B, masked_m, D, bias=None, acti
     """Masked M-grouped form: A [G,M_max,K], B [G,N,K], bias [G,N], masked_m int32 [G]."""
     G, M_max, K = A.shape
     N = B.shape[1]
-    _bf(A, "A", (G, M_max, K)); _bf(B, "B", (G, N, K))
-    _typed(masked_m, "masked_m", torch.int32, (G,))
-    _out(D, (G, M_max, N))
-    e = _epilogue(D, (G,), bias, activation, residual, Z)
-    _check(lib.dg_m_grouped_bf16_gemm_nt_masked_epilogue(_ptr(A), _ptr(B), _ptr(masked_m), e, _ptr(D), M_max, N, K, G,
-                                                         _stream(stream)))
+    dev = _on(A, "A")
+    e = _epilogue(D, (G, N), bias, activation, residual, Z, dev)
+    status = lib.dg_m_grouped_bf16_gemm_nt_masked_epilogue(
+        _arg(A, "A", _BF, (G, M_max, K), dev), _arg(B, "B", _BF, (G, N, K), dev),
+        _arg(masked_m, "masked_m", _I32, (G,), dev), e, _arg(D, "D", _BF, (G, M_max, N), dev), M_max, N, K, G,
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
 def dg_fp8_gemm_nt_epilogue(A, sfa, B, sfb, D, bias=None, activation="none", residual=None, Z=None, stream=None):
     """As dg_bf16_gemm_nt_epilogue with E4M3 operands and FP32 scales (layouts of dg_fp8_gemm_nt)."""
-    _fp8(A, "A"); _fp8(B, "B")
     M, K = A.shape
     N = B.shape[0]
-    if B.shape[1] != K:
-        raise ValueError("A and B must share K")
-    _f32(sfa, "sfa", (_cdiv(K, 128), M)); _f32(sfb, "sfb", (_cdiv(N, 128), _cdiv(K, 128)))
-    _out(D, (M, N))
-    e = _epilogue(D, (), bias, activation, residual, Z)
-    _check(lib.dg_fp8_gemm_nt_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), e, _ptr(D), M, N, K, _stream(stream)))
+    kb, dev = _cdiv(K, 128), _on(A, "A")
+    e = _epilogue(D, (N,), bias, activation, residual, Z, dev)
+    status = lib.dg_fp8_gemm_nt_epilogue(
+        _fp8_arg(A, "A", (M, K), dev), _arg(sfa, "sfa", _F32, (kb, M), dev), _fp8_arg(B, "B", (N, K), dev),
+        _arg(sfb, "sfb", _F32, (_cdiv(N, 128), kb), dev), e, _arg(D, "D", _BF, (M, N), dev), M, N, K,
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
 def dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(A, sfa, B, sfb, m_indices, D, bias=None, activation="none",
                                                  residual=None, Z=None, stream=None):
     """Contiguous M-grouped FP8 form (layouts of dg_m_grouped_fp8_gemm_nt_contiguous), bias [G,N]."""
-    _fp8(A, "A"); _fp8(B, "B")
     M, K = A.shape
     G, N = B.shape[0], B.shape[1]
-    if B.shape[2] != K:
-        raise ValueError("A and B must share K")
-    _f32(sfa, "sfa", (_cdiv(K, 128), M)); _f32(sfb, "sfb", (G, _cdiv(N, 128), _cdiv(K, 128)))
-    _typed(m_indices, "m_indices", torch.int32, (M,))
-    _out(D, (M, N))
-    e = _epilogue(D, (G,), bias, activation, residual, Z)
-    _check(lib.dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(m_indices), e,
-                                                            _ptr(D), M, N, K, G, _stream(stream)))
+    kb, dev = _cdiv(K, 128), _on(A, "A")
+    e = _epilogue(D, (G, N), bias, activation, residual, Z, dev)
+    status = lib.dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(
+        _fp8_arg(A, "A", (M, K), dev), _arg(sfa, "sfa", _F32, (kb, M), dev), _fp8_arg(B, "B", (G, N, K), dev),
+        _arg(sfb, "sfb", _F32, (G, _cdiv(N, 128), kb), dev), _arg(m_indices, "m_indices", _I32, (M,), dev), e,
+        _arg(D, "D", _BF, (M, N), dev), M, N, K, G, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
 def dg_m_grouped_fp8_gemm_nt_masked_epilogue(A, sfa, B, sfb, masked_m, D, bias=None, activation="none", residual=None,
                                              Z=None, stream=None):
     """Masked M-grouped FP8 form (layouts of dg_m_grouped_fp8_gemm_nt_masked), bias [G,N]."""
-    _fp8(A, "A"); _fp8(B, "B")
     G, M_max, K = A.shape
     N = B.shape[1]
-    if B.shape[0] != G or B.shape[2] != K:
-        raise ValueError("B must be [G, N, K]")
-    _f32(sfa, "sfa", (G, _cdiv(K, 128), M_max)); _f32(sfb, "sfb", (G, _cdiv(N, 128), _cdiv(K, 128)))
-    _typed(masked_m, "masked_m", torch.int32, (G,))
-    _out(D, (G, M_max, N))
-    e = _epilogue(D, (G,), bias, activation, residual, Z)
-    _check(lib.dg_m_grouped_fp8_gemm_nt_masked_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(masked_m), e,
-                                                        _ptr(D), M_max, N, K, G, _stream(stream)))
+    kb, dev = _cdiv(K, 128), _on(A, "A")
+    e = _epilogue(D, (G, N), bias, activation, residual, Z, dev)
+    status = lib.dg_m_grouped_fp8_gemm_nt_masked_epilogue(
+        _fp8_arg(A, "A", (G, M_max, K), dev), _arg(sfa, "sfa", _F32, (G, kb, M_max), dev),
+        _fp8_arg(B, "B", (G, N, K), dev), _arg(sfb, "sfb", _F32, (G, _cdiv(N, 128), kb), dev),
+        _arg(masked_m, "masked_m", _I32, (G,), dev), e, _arg(D, "D", _BF, (G, M_max, N), dev), M_max, N, K, G,
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
@@ -955,28 +1008,23 @@ def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=No
     (contiguous layout) dbias is [G,N], and dZ of padding rows is cleared."""
     if dD.dim() != 2:
         raise ValueError("dD must be [M, N]")
-    M, N = dD.shape
-    act = _activation(activation)
-    _bf(dD, "dD", (M, N))
-    if act:
-        if Z is None:
-            raise ValueError("Z is needed with an activation")
-        _bf(Z, "Z", (M, N))
-    if dZ is not None:
-        _bf(dZ, "dZ", (M, N))
-    z = _ptr(Z) if act else None
+    shape, act, dev = dD.shape, _activation(activation), _on(dD, "dD")
+    M, N = shape
+    if act and Z is None:
+        raise ValueError("Z is needed with an activation")
+    args = (_arg(dD, "dD", _BF, shape, dev), _arg(Z, "Z", _BF, shape, dev) if act else None, act)
+    dz = _opt(dZ, "dZ", _BF, shape, dev)
     if m_indices is None:
-        if dbias is not None:
-            _typed(dbias, "dbias", torch.float32, (N,))
-        _check(lib.dg_epilogue_backward(_ptr(dD), z, act, _ptr(dZ), _ptr(dbias), M, N, _stream(stream)))
+        status = lib.dg_epilogue_backward(*args, dz, _opt(dbias, "dbias", _F32, (N,), dev), M, N,
+                                          _raw_stream(stream, dev))
     else:
-        _typed(m_indices, "m_indices", torch.int32, (M,))
-        G = 65535                       # without a bias any row that names an expert is one
-        if dbias is not None:
-            G = dbias.shape[0]
-            _typed(dbias, "dbias", torch.float32, (G, N))
-        _check(lib.dg_m_grouped_epilogue_backward_contiguous(_ptr(dD), z, act, _ptr(m_indices), _ptr(dZ), _ptr(dbias), M,
-                                                             N, G, _stream(stream)))
+        # without a bias any row that names an expert is one
+        G = 65535 if dbias is None else dbias.shape[0]
+        status = lib.dg_m_grouped_epilogue_backward_contiguous(
+            *args, _arg(m_indices, "m_indices", _I32, (M,), dev), dz, _opt(dbias, "dbias", _F32, (G, N), dev), M, N, G,
+            _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return dZ
 
 
@@ -985,11 +1033,12 @@ def dg_bf16_gemm_nn(A, B, C, D, stream=None):
     """D = C + A @ B with A [M,K], B [K,N] bfloat16, C None or float32 [M,N]."""
     M, K = A.shape
     N = B.shape[1]
-    _bf(A, "A", (M, K)); _bf(B, "B", (K, N))
-    if C is not None:
-        _f32(C, "C", (M, N))
-    _out(D, (M, N))
-    _check(lib.dg_bf16_gemm_nn(_ptr(A), _ptr(B), _ptr(C), _ptr(D), M, N, K, _stream(stream)))
+    dev = _on(A, "A")
+    status = lib.dg_bf16_gemm_nn(_arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (K, N), dev),
+                                 _opt(C, "C", _F32, (M, N), dev), _arg(D, "D", _BF, (M, N), dev), M, N, K,
+                                 _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
@@ -997,13 +1046,12 @@ def dg_m_grouped_bf16_gemm_nn_contiguous(A, B, m_indices, C, D, stream=None):
     """Contiguous M-grouped: row m of D is C[m] + A[m] @ B[m_indices[m]], B [G,K,N]."""
     M, K = A.shape
     G, N = B.shape[0], B.shape[2]
-    _bf(A, "A", (M, K)); _bf(B, "B", (G, K, N))
-    _typed(m_indices, "m_indices", torch.int32, (M,))
-    if C is not None:
-        _f32(C, "C", (M, N))
-    _out(D, (M, N))
-    _check(lib.dg_m_grouped_bf16_gemm_nn_contiguous(_ptr(A), _ptr(B), _ptr(m_indices), _ptr(C), _ptr(D), M, N, K, G,
-                                                    _stream(stream)))
+    dev = _on(A, "A")
+    status = lib.dg_m_grouped_bf16_gemm_nn_contiguous(
+        _arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (G, K, N), dev), _arg(m_indices, "m_indices", _I32, (M,), dev),
+        _opt(C, "C", _F32, (M, N), dev), _arg(D, "D", _BF, (M, N), dev), M, N, K, G, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
@@ -1011,24 +1059,23 @@ def dg_bf16_gemm_tn(A, B, C, D, stream=None):
     """D = C + A.T @ B with A [K,M], B [K,N] bfloat16 (any K), C None or float32 [M,N]."""
     K, M = A.shape
     N = B.shape[1]
-    _bf(A, "A", (K, M)); _bf(B, "B", (K, N))
-    if C is not None:
-        _f32(C, "C", (M, N))
-    _out(D, (M, N))
-    _check(lib.dg_bf16_gemm_tn(_ptr(A), _ptr(B), _ptr(C), _ptr(D), M, N, K, _stream(stream)))
+    dev = _on(A, "A")
+    status = lib.dg_bf16_gemm_tn(_arg(A, "A", _BF, (K, M), dev), _arg(B, "B", _BF, (K, N), dev),
+                                 _opt(C, "C", _F32, (M, N), dev), _arg(D, "D", _BF, (M, N), dev), M, N, K,
+                                 _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
 
 
 def dg_k_grouped_bf16_gemm_tn_contiguous(A, B, ks, C, D, stream=None):
     """D[g] = C[g] + A_seg.T @ B_seg over the K segments ks int32 [G]; A [K,M], B [K,N], C, D [G,M,N]."""
     K, M = A.shape
-    N = B.shape[1]
-    G = ks.numel()
-    _bf(A, "A", (K, M)); _bf(B, "B", (K, N))
-    _typed(ks, "ks", torch.int32, (G,))
-    if C is not None:
-        _f32(C, "C", (G, M, N))
-    _out(D, (G, M, N))
-    _check(lib.dg_k_grouped_bf16_gemm_tn_contiguous(_ptr(A), _ptr(B), _ptr(ks), _ptr(C), _ptr(D), M, N, K, G,
-                                                    _stream(stream)))
+    N, G = B.shape[1], ks.numel()
+    dev = _on(A, "A")
+    status = lib.dg_k_grouped_bf16_gemm_tn_contiguous(
+        _arg(A, "A", _BF, (K, M), dev), _arg(B, "B", _BF, (K, N), dev), _arg(ks, "ks", _I32, (G,), dev),
+        _opt(C, "C", _F32, (G, M, N), dev), _arg(D, "D", _BF, (G, M, N), dev), M, N, K, G, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return D
