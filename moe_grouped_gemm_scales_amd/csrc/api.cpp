@@ -97,7 +97,7 @@ std::atomic<int> g_num_cus_limit{0};   // 0: use the device's count
 // nodes that are never erased, and workspaces a call outgrows are retired, not
 // freed, so the pointers stay valid.
 struct WarmCall {
-    int kind = -1, rows = 0, n = 0, k = 0, g = 0, has_c = 0, sf = 0, ep = 0, dev = -1, limit = 0;
+    int kind = -1, rows = 0, n = 0, k = 0, g = 0, has_c = 0, sf = 0, extra = 0, dev = -1, limit = 0;
     uint64_t env = 0;
     hipStream_t stream = nullptr;
     const Plan* plan = nullptr;
@@ -251,7 +251,8 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
                  const int32_t* grp, const float* C, void* D, void* stream_ptr, bool noalloc = false,
                  const EpilogueArgs& ep = {}) {
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
-    const bool rewrite = p.kind == kKGrouped || p.a_k_outer || p.b_k_outer;
+    const bool rewrite = !p.direct && (p.kind == kKGrouped || p.a_k_outer || p.b_k_outer);
+    const int extra = p.ep.code() * 2 + p.direct;      // what the sizes do not say about the kernels
     // ---- warm call: the previous call of this thread had the same key
     int dev_now = 0;
     if (hipGetDevice(&dev_now) != hipSuccess) dev_now = -1;
@@ -260,7 +261,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     const int limit = g_num_cus_limit.load(std::memory_order_relaxed);
     WarmCall& w = t_warm;
     if (!noalloc && !rewrite && w.plan && w.kind == p.kind && w.rows == p.rows && w.n == p.n && w.k == p.k &&
-        w.g == p.g && w.has_c == p.has_c && w.sf == p.sf && w.ep == p.ep.code() && w.dev == dev_now && w.stream == stream &&
+        w.g == p.g && w.has_c == p.has_c && w.sf == p.sf && w.extra == extra && w.dev == dev_now && w.stream == stream &&
         w.env == env && w.limit == limit)
         return launch_segments(*w.plan, p, A, sfa, B, sfb, grp, C, D, stream, w.partials, w.counters, w.status, ep);
     std::lock_guard<std::mutex> lock(g_mu);
@@ -270,7 +271,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     if (s != DG_OK) return s;
     const int cus = effective_cus(*st);
     const char* forced = std::getenv("DG_FORCE_CONFIG");
-    PlanKey key{p.kind, p.rows, p.n, p.k, p.g, p.has_c, p.sf, p.ep.code(), cus,
+    PlanKey key{p.kind, p.rows, p.n, p.k, p.g, p.has_c, p.sf, extra, cus,
                 std::string(forced ? forced : "") + "|" + jit_extra_option()};
     auto it = st->plans.find(key);
     if (noalloc) {
@@ -350,8 +351,8 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     auto rewrite_k_major = [&](const void* x, void* xt, int rows_k, int cols, int groups) -> dg_status {
         if (p.sf == 3) {       // BF16: K in elements; K-grouped K is padded with zeros to whole K blocks
             const bool kg = p.kind == kKGrouped;
-            return transpose_bf16(x, xt, groups, kg ? p.k_rows : rows_k / 2, cols, kg ? p.kt : rows_k / 2, p.k / 2,
-                                  stream_ptr);
+            const int k = kg ? p.kt : rows_k / 2;
+            return transpose_bf16(x, xt, groups, k, cols, (k + 63) / 64 * 64, p.k / 2, stream_ptr);
         }
         const uint64_t blocks = (uint64_t)(rows_k / 64) * (uint64_t)((cols + 63) / 64);
         if (blocks >= (1ull << 31) || groups > 65535)
@@ -364,7 +365,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     };
     // TN / NN / TT layouts: the K-outermost operand(s) rewritten K-contiguous in the
     // stream's workspace, then the NT kernels run on them
-    if (p.kind != kKGrouped && (p.a_k_outer || p.b_k_outer)) {
+    if (rewrite && p.kind != kKGrouped) {
         const size_t a_bytes = p.a_k_outer ? (size_t)p.rows * (size_t)p.k : 0;
         const size_t b_bytes = p.b_k_outer ? (size_t)p.g * (size_t)p.n * (size_t)p.k : 0;
         uint8_t* buf = nullptr;
@@ -383,7 +384,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     }
     // K-grouped: rewrite A [kt][M] and B [kt][N] as [M][k] and [N][k] (k: the
     // padded pitch) in the stream's workspace; the GEMM reads those
-    if (p.kind == kKGrouped) {
+    if (rewrite && p.kind == kKGrouped) {
         uint8_t* buf = nullptr;
         s = ensure_kmajor(*st, stream, ((size_t)p.rows + (size_t)p.n) * (size_t)p.k, &buf);
         if (s != DG_OK) return s;
@@ -421,7 +422,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     if (s != DG_OK) return s;
     if (!rewrite && !print) {
         WarmCall& r = t_warm;
-        r.kind = p.kind; r.rows = p.rows; r.n = p.n; r.k = p.k; r.g = p.g; r.has_c = p.has_c; r.sf = p.sf; r.ep = p.ep.code();
+        r.kind = p.kind; r.rows = p.rows; r.n = p.n; r.k = p.k; r.g = p.g; r.has_c = p.has_c; r.sf = p.sf; r.extra = extra;
         r.dev = dev; r.limit = limit; r.env = env; r.stream = stream; r.plan = &it->second;
         r.partials = partials; r.counters = counters; r.status = st->status;
     }
@@ -522,6 +523,12 @@ dg_status read_epilogue(const dg_epilogue* e, Epilogue* ep, EpilogueArgs* args) 
     return DG_OK;
 }
 
+// A BF16 operand [K][cols] can be read as it is stored if its rows stay 16-byte
+// aligned and 32-bit offsets reach all of it; otherwise it is rewritten K-contiguous.
+bool reads_k_outermost(int64_t cols, int64_t K) {
+    return cols % 8 == 0 && (K + 64) * cols * 2 < (int64_t(1) << 32);
+}
+
 // BF16 x BF16, the three M forms: no scales; the kernels count K in bytes
 dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, const float* C, void* D, int rows,
                     int N, int K, int num_groups, void* stream, int b_k_outer = 0, const Epilogue& ep = {},
@@ -542,8 +549,19 @@ dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, 
     if (rows == 0) return DG_OK;
     Problem p{kind, rows, N, 2 * K, kind == kDense ? 1 : num_groups, C ? 1 : 0, 3};
     p.b_k_outer = b_k_outer;
+    p.direct = b_k_outer && reads_k_outermost(N, K);
     p.ep = ep;
     return launch(p, A, nullptr, B, nullptr, grp, C, D, stream, false, args);
+}
+
+// The problem of a BF16 TN product.  Read as stored, K is no constant of the
+// kernel: one serves every token count.
+Problem tn_problem(int M, int N, int K, int num_groups, int has_c) {
+    const bool direct = reads_k_outermost(M, K) && reads_k_outermost(N, K);
+    Problem p{kKGrouped, M, N, direct ? 1024 : std::max(1024, k_grouped_pitch(2 * K)), num_groups, has_c, 3};
+    p.direct = direct;
+    p.kt = K;
+    return p;
 }
 
 // BF16 TN (A [K][M], B [K][N]): K-grouped, or one group of any K (ks NULL)
@@ -553,13 +571,9 @@ dg_status bf16_gemm_tn(const void* A, const void* B, const int32_t* ks, const fl
     if (M < 0 || N <= 0 || K < 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M and K may be 0)");
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || (C && !aligned(C, 16)))
         return set_error(DG_ERR_ALIGNMENT, "A, B, C and D must be 16-byte aligned");
-    const int64_t pitch = ((int64_t)2 * K + 1023) / 1024 * 1024;
-    if ((uint64_t)pitch * 256u >= (1ull << 32)) return set_error(DG_ERR_UNSUPPORTED, "sizes exceed 32-bit buffer offsets");
+    if (((uint64_t)K + 512u) * 2u * 256u >= (1ull << 32)) return set_error(DG_ERR_UNSUPPORTED, "sizes exceed 32-bit buffer offsets");
     if (M == 0) return DG_OK;
-    Problem p{kKGrouped, M, N, (int)std::max<int64_t>(pitch, 1024), num_groups, C ? 1 : 0, 3};
-    p.k_rows = K;
-    p.kt = (K + 63) / 64 * 64;
-    return launch(p, A, nullptr, B, nullptr, ks, C, D, stream);
+    return launch(tn_problem(M, N, K, num_groups, C ? 1 : 0), A, nullptr, B, nullptr, ks, C, D, stream);
 }
 
 dg_status k_grouped(const void* A, const float* sfa, const void* B, const float* sfb, const int32_t* ks,
@@ -656,7 +670,7 @@ Epilogue epilogue_flags(int* kind) {
 
 // the kernels' K: BF16 rows are counted in bytes; K-grouped operands use the padded pitch
 int kernel_k(int kind, int sf, int K) {
-    if (sf == 3) return kind == kKGrouped ? k_grouped_pitch(2 * K) : 2 * K;
+    if (sf == 3) return 2 * K;
     return kind == kKGrouped ? k_grouped_pitch(K) : K;
 }
 
@@ -667,6 +681,7 @@ dg_status dg_precompile(int kind, int rows, int N, int K, int num_groups, int ha
         return set_error(DG_ERR_INVALID_ARG, "dg_precompile: bad arguments");
     if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
     Problem p{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
+    if (kind == kKGrouped && sf == 3) p = tn_problem(rows, N, K, num_groups, has_c ? 1 : 0);
     p.ep = ep;
     for (const KernelConfig& cfg : select_plan(p, num_cus > 0 ? num_cus : 256)) {
         std::vector<char> code;
@@ -694,6 +709,7 @@ dg_status dg_describe_config(int kind, int rows, int N, int K, int num_groups, i
         cus = effective_cus(*st);
     }
     Problem p{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
+    if (kind == kKGrouped && sf == 3) p = tn_problem(rows, N, K, num_groups, has_c ? 1 : 0);
     p.ep = ep;
     std::string key;
     for (const KernelConfig& c : select_plan(p, cus)) key += (key.empty() ? "" : "+") + c.key();

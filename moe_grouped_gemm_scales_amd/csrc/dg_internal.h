@@ -60,6 +60,7 @@ struct KernelConfig {
     int bstream = 0;           // each B block is read by at most two row blocks of the launch
                                // (dense or masked, few rows): B loads carry the non-temporal hint
     Epilogue ep;               // fused epilogue of the *_epilogue entry points (none: plain D)
+    int a_kout = 0, b_kout = 0;   // BF16: A ([K][M], K-grouped) or B ([K][N]) read K-outermost as stored
 
     int n_begin() const { return nb; }
     int n_end() const { return ne > 0 ? ne : n; }
@@ -102,8 +103,8 @@ struct Problem {
     int has_c;
     int sf = 0;    // scale format: as KernelConfig::sf
     int kt = 0;    // K-grouped: K rows of the operands (n, k above: N and the padded pitch)
-    int k_rows = 0;   // BF16 K-grouped: K before it is rounded up to whole K blocks (kt)
     int a_k_outer = 0, b_k_outer = 0;   // A stored [K][rows] (T), B stored [(G)][K][N] (N)
+    int direct = 0;   // BF16: the K-outermost operands are read as stored, without a rewrite
     Epilogue ep;
 };
 

@@ -118,6 +118,10 @@ int unit_per_wave_v1(const KernelConfig& c) {
 bool valid(const KernelConfig& c, const Problem& p) {
     if (c.bm % (16 * c.wm) || c.bn % (16 * c.wn)) return false;
     if (c.ne > 0 && (c.nb < 0 || c.nb % 16 || c.nb >= c.ne || c.ne > p.n)) return false;
+    // operands read K-outermost: power-of-two tiles through LDS, aligned rows
+    auto kout_tile = [](int t, int w) { return (t == 64 || t == 128 || t == 256) && ((t / w) & (t / w - 1)) == 0; };
+    if (c.b_kout && (!kout_tile(c.bn, c.wn) || p.n % 8 || (c.variant != 0 && c.variant != 6) || c.kstep != 1)) return false;
+    if (c.a_kout && (!kout_tile(c.bm, c.wm) || p.rows % 8)) return false;
     if (c.splitk < 1 || (c.splitk > 1 && p.kind != kDense)) return false;   // split-K: dense only
     if (c.sf != p.sf) return false;
     // variant 4: variant 0 with A requested a K block ahead of B (two B slots, three A
@@ -344,6 +348,8 @@ std::vector<KernelConfig> select_plan(const Problem& p, int num_cus) {
     base.k = p.k;
     base.g = (p.kind == kDense) ? 1 : p.g;
     base.ep = p.ep;
+    base.a_kout = p.direct && p.kind == kKGrouped;
+    base.b_kout = p.direct;
 
     std::vector<KernelConfig> forced = parse_forced(base);
     if (valid_plan(forced, p)) return with_b_streams(forced, p);

@@ -75,6 +75,8 @@ std::vector<std::string> compile_options(const KernelConfig& c) {
         def("DG_RES", c.ep.res);
         def("DG_ZOUT", c.ep.zout);
     }
+    if (c.a_kout) def("DG_A_KOUT", 1);
+    if (c.b_kout) def("DG_B_KOUT", 1);
     if (c.ne > 0) {
         def("DG_NB", c.nb);
         def("DG_NE", c.ne);
@@ -199,6 +201,7 @@ std::string KernelConfig::key() const {
     if (sf == 3) s << "_bf16";
     if (sf == 4) s << "_f4f4";
     if (sf == 5) s << "_e8m0x2";
+    if (a_kout || b_kout) s << (a_kout ? "_tn" : "_nn");
     if (ep.any()) s << "_ep" << ep.bias << ep.act << ep.res << ep.zout;
     if (ne > 0) s << "_cols" << nb << "-" << ne;
     return s.str();

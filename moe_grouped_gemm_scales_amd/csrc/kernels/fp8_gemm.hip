@@ -122,6 +122,16 @@ typedef u16 v4u16 __attribute__((ext_vector_type(4)));
 #ifndef DG_ZOUT
 #define DG_ZOUT 0
 #endif
+// K-outermost operands read as they are stored (BF16, variant 0 and the split
+// refill): DG_B_KOUT: B [K][N] (grouped [G][K][N]); DG_A_KOUT: A [K][M] (K-grouped
+// only).  The matrix core wants each lane's K values side by side, so the
+// fragments are read from LDS with the transposing 64-bit read.
+#ifndef DG_A_KOUT
+#define DG_A_KOUT 0
+#endif
+#ifndef DG_B_KOUT
+#define DG_B_KOUT 0
+#endif
 #define DG_EPI (DG_BIAS || DG_ACT || DG_RES || DG_ZOUT)
 
 namespace dg {
@@ -319,6 +329,14 @@ __device__ __forceinline__ u32 lds_addr(const void* p) {
 typedef __attribute__((address_space(3))) const v4i lds_v4i;
 typedef __attribute__((address_space(3))) const float lds_f32;
 typedef __attribute__((address_space(3))) const u8 lds_u8;
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+template <int V> struct int_c { static constexpr int value = V; };
+// Transposing read: in each group of 16 lanes, lane j gets element j % 4 of the
+// eight bytes at the addresses of lanes j / 4, 4 + j / 4, 8 + j / 4, 12 + j / 4.
+__device__ __forceinline__ v2i lds_read_tr16(lds_u8* p) {
+    return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16*)p));
+}
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 // the two 16-byte halves of a fragment as BF16 MFMA operands (8 elements each)
 __device__ __forceinline__ v8bf bf_lo(v8i x) { return __builtin_bit_cast(v8bf, v4i{x[0], x[1], x[2], x[3]}); }
@@ -449,8 +467,9 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
             for (int h = 0; h < g; ++h) off += p.grp[h] > 0 ? p.grp[h] : 0;
             len = p.grp[g] > 0 ? p.grp[g] : 0;
         }
-        const int kbt = p.kt / KROWS;
-        int kb0 = off / KROWS, kb1 = (off + len) / KROWS;
+        // (one BF16 group may end inside a K block: its rows past kt read as zeros)
+        const int kbt = (p.kt + KROWS - 1) / KROWS;
+        int kb0 = off / KROWS, kb1 = (off + len + (BF16 ? KROWS - 1 : 0)) / KROWS;
         kb0 = kb0 < kbt ? kb0 : kbt;
         kb1 = kb1 < kbt ? kb1 : kbt;
         // grouped order inside the group: 8 row blocks per column sweep
@@ -896,6 +915,21 @@ constexpr int ROWB_B = FP4B ? 64 : ROWB;
 constexpr int RPI_B = 1024 / ROWB_B;
 constexpr int ROWB_A = FP4A ? 64 : ROWB;        // FP4 A: the same 64-byte rows as FP4 B
 constexpr int RPI_A = 1024 / ROWB_A;
+// K-outermost operands: a K block is 64 rows of BM (BN) columns, 2 BM (2 BN) bytes
+// a row, so the tile takes the same LDS bytes and DMA instructions; an instruction
+// covers KRPI rows of CPR 16-byte chunks (8 columns each).  Chunk c of row k is
+// stored at chunk c ^ kswz(k): the transposing read of a fragment takes 32 bytes
+// (two chunks) from each of 16 rows, 8q + 4r + i (i = 0..3, lane group q), and the
+// swizzle sends the eight rows of two neighbouring lane groups to different banks.
+constexpr bool A_KOUT = DG_A_KOUT != 0, B_KOUT = DG_B_KOUT != 0;
+static_assert(!(A_KOUT || B_KOUT) || (BF16 && KSTEP == 1 && N % 8 == 0), "K-outermost operands: BF16, aligned rows");
+static_assert(!A_KOUT || (KG && B_KOUT), "A K-outermost: K-grouped, with B");
+static_assert((!A_KOUT || BM == 64 || BM == 128 || BM == 256) && (!B_KOUT || BN == 64 || BN == 128 || BN == 256),
+              "K-outermost tiles: 64, 128 or 256 columns");
+template <int COLS>
+__device__ __forceinline__ constexpr int kswz(int k) {
+    return COLS >= 128 ? 2 * ((k & 3) | ((k >> 1) & 4)) : 2 * (((k >> 1) & 1) | ((k >> 2) & 2));
+}
 constexpr int NA_INS = BM / RPI_A;              // 1 KB DMA instructions for A
 constexpr int NB_INS = BN / RPI_B;              // ... for B
 constexpr int NS_PER_KB = BF16 ? 0 : (BM + 63) / 64;   // 256 B DMA instructions for one K block of sfa
@@ -983,12 +1017,17 @@ constexpr int SPREAD = DG_SPREAD < TN - 1 ? DG_SPREAD : TN - 1;
 #endif
 constexpr bool SPLIT = DG_SPLIT != 0;
 constexpr int HALF_TN = TN / 2;
+// With B K-outermost an instruction holds every column of a few K rows, so B
+// cannot be handed back by halves: the mid group is A alone and the end group
+// all of B, which has landed (with the next block's A) by the end of the block.
 constexpr int NB_HALF = NB_INS / 2;                      // B DMA instructions of one half
-constexpr int IBH = (NB_HALF + NWAVES - 1) / NWAVES;    // ... per wave
+constexpr int IBH = B_KOUT ? 0 : (NB_HALF + NWAVES - 1) / NWAVES;    // ... per wave
 constexpr int NSC_PER_WAVE = INS_PER_WAVE - IA - IB;    // scale DMA instructions per wave
 constexpr int G_MID = IA + IBH + NSC_PER_WAVE;
-constexpr int G_END = IBH;
+constexpr int G_END = B_KOUT ? IB : IBH;
 constexpr int SPLIT_PENDING = (STAGES - 1) * (G_MID + G_END);
+// ... pending at the end of a block, when the next one's groups have to be in
+constexpr int SPLIT_PENDING_END = B_KOUT ? (STAGES - 1) * G_MID + (STAGES - 2) * G_END : SPLIT_PENDING;
 static_assert(!SPLIT || (KSTEP == 1 && !AAHEAD && TN % 2 == 0 && TN >= 4 && !FP4A && !FP4B),
               "split refill: FP8 or BF16 operands, one K block a slot, an even number of n sub-tiles");
 // B instruction i covers 8 rows inside one 16-row n sub-tile of one wave column
@@ -1100,8 +1139,21 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
             a_rows_total = p.M;
             const int n_rows = N_END - tl.n0 < BN ? N_END - tl.n0 : BN;
             const u8* b_base = p.B + ((u64)(KG ? 0 : tl.g) * N + tl.n0) * KB_B;
-            const v4i rs_a = make_rsrc(a_base, (u32)tl.rows * KB_A);
-            const v4i rs_b = make_rsrc(b_base, (u32)n_rows * KB_B);
+            u32 a_bytes = (u32)tl.rows * KB_A, b_bytes = (u32)n_rows * KB_B;
+            // K-outermost: from the tile's first column of K row 0 to the end of the operand, so that
+            // rows past K read as zeros (columns past N or M of an earlier row hold the next row's
+            // values: they only reach columns that are never stored)
+            const u32 k_rows = KG ? (u32)p.kt : (u32)K / 2u;
+            if constexpr (A_KOUT) {
+                a_base = p.A + (u64)tl.m0 * 2u;
+                a_bytes = (k_rows * (u32)p.M - (u32)tl.m0) * 2u;
+            }
+            if constexpr (B_KOUT) {
+                b_base = p.B + ((u64)(KG ? 0 : tl.g) * (K / 2) * N + tl.n0) * 2u;
+                b_bytes = (k_rows * (u32)N - (u32)tl.n0) * 2u;
+            }
+            const v4i rs_a = make_rsrc(a_base, a_bytes);
+            const v4i rs_b = make_rsrc(b_base, b_bytes);
             const v4i rs_s = make_rsrc(sfa_base, (u32)(FP4A ? KBLKS : SF_KB) * a_rows_total * (FP4A ? 4u : (u32)SF_BYTES));
             const v4i rs_t = FP4B ? make_rsrc(p.sfb + ((u64)tl.g * N + tl.n0) * KBLKS, (u32)n_rows * KBLKS * 4u)
                              : KG ? make_rsrc(p.sfb, (u32)(p.kt / KBLK) * N * 4u)
@@ -1161,6 +1213,25 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                 }
             }
 
+            // K-outermost DMA: lane l of instruction i fetches row KRPI i + l / CPR, the
+            // chunk that belongs at physical place l % CPR (the swizzle of the row is the
+            // xor of the lane's and the instruction's parts)
+            constexpr int CPR_A = BM / 8, CPR_B = BN / 8, KRPI_A = 64 / CPR_A, KRPI_B = 64 / CPR_B;
+            const u32 ko_row_a = (u32)(lane / CPR_A) * (u32)p.M * 2u;
+            const u32 ko_chunk_a = (u32)((lane % CPR_A) ^ kswz<BM>(lane / CPR_A)) * 16u;
+            const u32 ko_row_b = (u32)(lane / CPR_B) * (u32)N * 2u;
+            const u32 ko_chunk_b = (u32)((lane % CPR_B) ^ kswz<BN>(lane / CPR_B)) * 16u;
+            auto dma_kout_a = [&](v4i r, int i, int kb, u32 lds) {
+                const u32 sw = (u32)__builtin_amdgcn_readfirstlane(kswz<BM>(i * KRPI_A) * 16);
+                dma16(r, ko_row_a + (ko_chunk_a ^ sw),
+                      __builtin_amdgcn_readfirstlane((u32)(kb * KROWS + i * KRPI_A) * (u32)p.M * 2u), lds);
+            };
+            auto dma_kout_b = [&](v4i r, int i, int kb, u32 lds) {
+                const u32 sw = (u32)__builtin_amdgcn_readfirstlane(kswz<BN>(i * KRPI_B) * 16);
+                dma16b(r, ko_row_b + (ko_chunk_b ^ sw),
+                       __builtin_amdgcn_readfirstlane((u32)(kb * KROWS + i * KRPI_B) * (u32)N * 2u), lds);
+            };
+
             // one scale instruction per wave: an A-scale one (waves 0 .. NS_INS-1) or a B-scale one
             const bool is_a_sc = wave < NS_INS;
             const u32 voff_sc = is_a_sc ? voff_s[0] : voff_t[0];
@@ -1187,7 +1258,9 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                 };
                 if (j < IA) {
                     const int i = min(wave + j * NWAVES, NA_INS - 1);
-                    if constexpr (FP4A)
+                    if constexpr (A_KOUT)
+                        dma_kout_a(lim(rs_a), i, kb, st + A_OFF + i * 1024);
+                    else if constexpr (FP4A)
                         dma16(lim(rs_a), voff_b4a + (u32)__builtin_amdgcn_readfirstlane((u32)(i * RPI_A) * (u32)KB_A),
                               __builtin_amdgcn_readfirstlane((u32)kb * (KBLK / 2)), st + A_OFF + i * 1024);
                     else
@@ -1195,7 +1268,9 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                               __builtin_amdgcn_readfirstlane((u32)kb * KBLK), st + A_OFF + i * 1024);
                 } else if (j < IA + IB) {
                     const int i = min(wave + (j - IA) * NWAVES, NB_INS - 1);
-                    if constexpr (FP4B)
+                    if constexpr (B_KOUT)
+                        dma_kout_b(lim(rs_b), i, kb, st + B_OFF + i * 1024);
+                    else if constexpr (FP4B)
                         dma16b(lim(rs_b), voff_b4 + (u32)__builtin_amdgcn_readfirstlane((u32)(i * RPI_B) * (u32)KB_B),
                               __builtin_amdgcn_readfirstlane((u32)kb * (KBLK / 2)), st + B_OFF + i * 1024);
                     else
@@ -1241,7 +1316,8 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                 else issue_one(j - IBH + IB, kb, stage, live);
             };
             auto issue_end = [&](int j, int kb, int stage, bool live) {
-                issue_b_half(min(wave + j * NWAVES, NB_HALF - 1), true, kb, stage, live);
+                if constexpr (B_KOUT) issue_one(IA + j, kb, stage, live);
+                else issue_b_half(min(wave + j * NWAVES, NB_HALF - 1), true, kb, stage, live);
             };
             // A ahead: instruction j of one iteration's issue, in the order B, sfb (K block
             // kb_b into B slot sl_b), then A, sfa (K block kb_a into A slot sl_a), so that
@@ -1348,12 +1424,36 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                 const u32 a_frag = a_frag_off + a_chunk_lo, a_frag_hi = a_frag_off + chunk_hi;
                 // B fragment of the sub-tile at byte offset off of a K block (lo/hi:
                 // the block's base plus this lane's chunk offsets)
-                auto read_fb = [&](lds_u8* lo, lds_u8* hi, int off) __attribute__((always_inline)) {
-                    if constexpr (FP4B) return lds_read_frag4(lo, off);
+                // K-outermost: lane (l16, q) reads K rows 8q + 4r + l16 / 4 (lo; + 32: hi), four
+                // columns from 4 (l16 % 4), and holds after the transposing read the four K
+                // values of column l16: the K order of the K-contiguous fragment.  The row's
+                // swizzle is the same for every fragment; a fragment's first chunk (two chunks a
+                // sub-tile) enters by xor.
+                const u32 ko_lane_row = (u32)(8 * q + (l16 >> 2));
+                const u32 ko_frag_a = ko_lane_row * (BM * 2) + 8u * (l16 & 1) +
+                                      (((u32)(wm * WAVE_M / 8) | ((l16 >> 1) & 1)) ^ (u32)kswz<BM>(8 * (q & 1) + (l16 >> 2))) * 16u;
+                const u32 ko_frag_b = ko_lane_row * (BN * 2) + 8u * (l16 & 1) +
+                                      (((u32)(wn * WAVE_N / 8) | ((l16 >> 1) & 1)) ^ (u32)kswz<BN>(8 * (q & 1) + (l16 >> 2))) * 16u;
+                static_assert(!A_KOUT || (WAVE_M & (WAVE_M - 1)) == 0, "the sub-tile's chunk enters by xor");
+                static_assert(!B_KOUT || (WAVE_N & (WAVE_N - 1)) == 0, "the sub-tile's chunk enters by xor");
+                auto read_kout = [&](lds_u8* tile, u32 frag, int sub, auto pitch) __attribute__((always_inline)) {
+                    lds_u8* const at = tile + (frag ^ (u32)(sub * 32));
+                    constexpr int PITCH = decltype(pitch)::value;
+                    const v2i a = lds_read_tr16(at), b = lds_read_tr16(at + 4 * PITCH);
+                    const v2i c = lds_read_tr16(at + 32 * PITCH), d = lds_read_tr16(at + 36 * PITCH);
+                    return v8i{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+                };
+                // fragment of sub-tile `sub` (lo, hi: K-contiguous bases; tile: the operand's slot)
+                auto read_fb = [&](lds_u8* tile, lds_u8* lo, lds_u8* hi, int sub) __attribute__((always_inline)) {
+                    const int off = sub * 16 * ROWB_B;
+                    if constexpr (B_KOUT) return read_kout(tile, ko_frag_b, sub, int_c<BN * 2>{});
+                    else if constexpr (FP4B) return lds_read_frag4(lo, off);
                     else return lds_read_frag(lo, hi, off);
                 };
-                auto read_fa = [&](lds_u8* lo, lds_u8* hi, int off) __attribute__((always_inline)) {
-                    if constexpr (FP4A) return lds_read_frag4(lo, off);
+                auto read_fa = [&](lds_u8* tile, lds_u8* lo, lds_u8* hi, int sub) __attribute__((always_inline)) {
+                    const int off = sub * 16 * ROWB_A;
+                    if constexpr (A_KOUT) return read_kout(tile, ko_frag_a, sub, int_c<BM * 2>{});
+                    else if constexpr (FP4A) return lds_read_frag4(lo, off);
                     else return lds_read_frag(lo, hi, off);
                 };
                 // FP4 B scales: this lane's row of each n sub-tile, one word per K block
@@ -1409,7 +1509,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
 
                 // stage 0 in LDS (this wave's DMA, then everyone's), then its registers
                 if constexpr (AAHEAD) wait_vmcnt<IA + IS>();     // all but A of K block 1
-                else if constexpr (SPLIT) wait_vmcnt<SPLIT_PENDING>();   // the mid group of block 0
+                else if constexpr (SPLIT) wait_vmcnt<SPLIT_PENDING_END>();   // the mid group of block 0
                 else if (STAGES - 1 <= nst) wait_stages<STAGES - 2>();
                 else wait_vmcnt<0>();
                 __syncthreads();
@@ -1418,8 +1518,8 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                     lds_u8* const kb0 = b_tile(0);
                     read_scales(0, 0);
 #pragma unroll
-                    for (int a = 0; a < TM; ++a) fa[a] = read_fa(ka0 + a_frag, ka0 + a_frag_hi, a * 16 * ROWB_A);
-                    fb = read_fb(kb0 + b_frag, kb0 + b_frag_hi, 0);
+                    for (int a = 0; a < TM; ++a) fa[a] = read_fa(ka0, ka0 + a_frag, ka0 + a_frag_hi, a);
+                    fb = read_fb(kb0, kb0 + b_frag, kb0 + b_frag_hi, 0);
                 }
 
 #pragma unroll 1
@@ -1484,7 +1584,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                                     issue_end(j, tl.kb0 + min(f, nst - 1), f % STAGES, f < nst);
                             }
                             if (b + 1 == HALF_TN) {
-                                wait_vmcnt<SPLIT_PENDING>();      // end group of this block landed
+                                if constexpr (!B_KOUT) wait_vmcnt<SPLIT_PENDING>();      // end group of this block landed
                                 __syncthreads();
                             }
                             if (b + 1 >= HALF_TN && b + 1 < TN) {
@@ -1511,7 +1611,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                         }
                         const bool last = b + 1 == TN;
                         v8i fb_next;
-                        if (!last) fb_next = read_fb(b_lo, b_hi, (b + 1) * 16 * ROWB_B);
+                        if (!last) fb_next = read_fb(kbp, b_lo, b_hi, b + 1);
                         // scales of sub-tile b-1 (promoted now) and, in the last sub-tile, of
                         // b itself (carried), taken before the next K block's replace them
                         sc_t sc_prev[TM], s_last[TM];
@@ -1531,7 +1631,7 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                                 // everyone's; all reads of this stage are in registers.  A ahead:
                                 // everything but A of K block it+2 (issued last) has landed
                                 if constexpr (AAHEAD) wait_vmcnt<IA + IS>();
-                                else if constexpr (SPLIT) wait_vmcnt<SPLIT_PENDING>();   // next block's mid group
+                                else if constexpr (SPLIT) wait_vmcnt<SPLIT_PENDING_END>();   // next block's mid group
                                 else wait_stages<STAGES - 2>();
                                 __syncthreads();
                             }
@@ -1563,14 +1663,14 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                             }
                             // the last sub-tile's MFMA has taken fa[a]: fetch the next K block's
                             // (after the tile's last block these reads are unused)
-                            if (last) fa[a] = read_fa(kan + a_frag, kan + a_frag_hi, a * 16 * ROWB_A);
+                            if (last) fa[a] = read_fa(kan, kan + a_frag, kan + a_frag_hi, a);
                             __builtin_amdgcn_sched_barrier(0);
                         }
                         if constexpr (DG_SETPRIO != 0) __builtin_amdgcn_s_setprio(0);
                         if (!last) {
                             fb = fb_next;
                         } else {
-                            fb = read_fb(kbn + b_frag, kbn + b_frag_hi, 0);
+                            fb = read_fb(kbn, kbn + b_frag, kbn + b_frag_hi, 0);
 #pragma unroll
                             for (int a = 0; a < TM; ++a) s_carry[a] = s_last[a];
                         }
