@@ -511,6 +511,7 @@ dg_status dg_init(void);
 #define DG_BF16 16           /* BF16 x BF16 without scales (K in elements) */
 #define DG_SCALE_FP4_FP4 32  /* FP4 x FP4 */
 #define DG_SCALE_UE8M0_I16 64   /* UE8M0 pairs in 16-bit words, MN-major */
+#define DG_LAYOUT_NN 128     /* with DG_BF16: the NN product (B stored [K][N]) */
 /* ... and for the parts of a fused epilogue (DG_EPI_ACT takes a dg_activation) */
 #define DG_EPI_BIAS_F32 0x100
 #define DG_EPI_BIAS_BF16 0x200
@@ -524,7 +525,7 @@ dg_status dg_init(void);
  * 1 contiguous, 2 masked, 3 K-grouped (K = the K rows; the FP32 scale form
  * or BF16) (| DG_SCALE_UE8M0 for packed UE8M0 scales, | DG_SCALE_UE8M0_I16 for
  * UE8M0 pairs in 16-bit words, | DG_SCALE_FP8_FP4 for FP8 x FP4, | DG_BF16,
- * | DG_SCALE_FP4_FP4, | DG_EPI_* for a fused epilogue); has_c:
+ * | DG_SCALE_FP4_FP4, | DG_LAYOUT_NN, | DG_EPI_* for a fused epilogue); has_c:
  * 0/1; rows = M (dense/contiguous) or M_max.
  * Needs no GPU: the code object is built for gfx950 and stored in the cache
  * directory (DG_CACHE_DIR, else <library dir>/jit_cache).

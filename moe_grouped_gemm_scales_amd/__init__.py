@@ -23,7 +23,7 @@ from .dg import (DGError, describe_config, dg_fp8_gemm_nt, dg_m_grouped_fp8_gemm
                  fp4_fp4_gemm_nt, m_grouped_fp4_fp4_gemm_nt_contiguous, m_grouped_fp4_fp4_gemm_nt_masked)
 from .dg import (dg_moe_combine, dg_moe_combine_backward, dg_moe_dispatch_bf16, dg_moe_dispatch_fp8,  # noqa: F401
                  dg_moe_sort_contiguous, dg_moe_sort_masked, moe_sorted_rows)
-from .dg import (ACTIVATIONS, EPI_BIAS_BF16, EPI_BIAS_F32, EPI_RESIDUAL, EPI_Z, dg_bf16_gemm_nn, dg_bf16_gemm_nt_epilogue, dg_bf16_gemm_tn,  # noqa: F401
+from .dg import (ACTIVATIONS, EPI_BIAS_BF16, EPI_BIAS_F32, EPI_RESIDUAL, EPI_Z, LAYOUT_NN, dg_bf16_gemm_nn, dg_bf16_gemm_nt_epilogue, dg_bf16_gemm_tn,  # noqa: F401
                  dg_epilogue_backward, dg_fp8_gemm_nt_epilogue, dg_k_grouped_bf16_gemm_tn_contiguous,
                  dg_m_grouped_bf16_gemm_nn_contiguous, dg_m_grouped_bf16_gemm_nt_contiguous_epilogue,
                  dg_m_grouped_bf16_gemm_nt_masked_epilogue, dg_m_grouped_fp8_gemm_nt_contiguous_epilogue,

@@ -674,18 +674,34 @@ int kernel_k(int kind, int sf, int K) {
     return kind == kKGrouped ? k_grouped_pitch(K) : K;
 }
 
-dg_status dg_precompile(int kind, int rows, int N, int K, int num_groups, int has_c, int num_cus) {
+// The problem that a call with these sizes and flags poses to select_plan.
+dg_status described_problem(int kind, int rows, int N, int K, int num_groups, int has_c, Problem* p) {
+    const bool nn = (kind & DG_LAYOUT_NN) != 0;
+    kind &= ~DG_LAYOUT_NN;
     const Epilogue ep = epilogue_flags(&kind);
     const int sf = scale_format(&kind);
-    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH)
-        return set_error(DG_ERR_INVALID_ARG, "dg_precompile: bad arguments");
-    if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
-    Problem p{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
-    if (kind == kKGrouped && sf == 3) p = tn_problem(rows, N, K, num_groups, has_c ? 1 : 0);
-    p.ep = ep;
+    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH ||
+        (nn && sf != 3))
+        return set_error(DG_ERR_INVALID_ARG, "bad arguments");
+    if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64))
+        return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
+    if (kind == kKGrouped && sf == 3) *p = tn_problem(rows, N, K, num_groups, has_c ? 1 : 0);
+    else *p = Problem{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
+    if (nn) {
+        p->b_k_outer = 1;
+        p->direct = reads_k_outermost(N, K);
+    }
+    p->ep = ep;
+    return DG_OK;
+}
+
+dg_status dg_precompile(int kind, int rows, int N, int K, int num_groups, int has_c, int num_cus) {
+    Problem p{};
+    dg_status s = described_problem(kind, rows, N, K, num_groups, has_c, &p);
+    if (s != DG_OK) return s;
     for (const KernelConfig& cfg : select_plan(p, num_cus > 0 ? num_cus : 256)) {
         std::vector<char> code;
-        dg_status s = compile_code(cfg, &code);
+        s = compile_code(cfg, &code);
         if (s != DG_OK) return s;
     }
     return DG_OK;
@@ -693,24 +709,19 @@ dg_status dg_precompile(int kind, int rows, int N, int K, int num_groups, int ha
 
 dg_status dg_describe_config(int kind, int rows, int N, int K, int num_groups, int has_c, int num_cus, char* buf,
                              int len) {
-    const Epilogue ep = epilogue_flags(&kind);
-    const int sf = scale_format(&kind);
-    if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH || !buf ||
-        len <= 0)
-        return set_error(DG_ERR_INVALID_ARG, "dg_describe_config: bad arguments");
-    if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64)) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
+    if (!buf || len <= 0) return set_error(DG_ERR_INVALID_ARG, "bad arguments");
+    Problem p{};
+    dg_status s = described_problem(kind, rows, N, K, num_groups, has_c, &p);
+    if (s != DG_OK) return s;
     int cus = num_cus;
     if (cus <= 0) {
         std::lock_guard<std::mutex> lock(g_mu);
         DeviceState* st = nullptr;
         int dev = 0;
-        dg_status s = device_state(&st, &dev);
+        s = device_state(&st, &dev);
         if (s != DG_OK) return s;
         cus = effective_cus(*st);
     }
-    Problem p{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
-    if (kind == kKGrouped && sf == 3) p = tn_problem(rows, N, K, num_groups, has_c ? 1 : 0);
-    p.ep = ep;
     std::string key;
     for (const KernelConfig& c : select_plan(p, cus)) key += (key.empty() ? "" : "+") + c.key();
     std::snprintf(buf, (size_t)len, "%s", key.c_str());

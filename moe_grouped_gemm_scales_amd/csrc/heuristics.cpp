@@ -281,6 +281,71 @@ std::vector<KernelConfig> tuned(const Problem& p, int num_cus, const KernelConfi
     return out;
 }
 
+// The products with a fused epilogue and the BF16 NN and TN products choose among
+// these structures by a short cost sum fitted to sweeps of them on an MI355X (20
+// shapes of 1 to 8704 rows, BF16 and FP8, every form, 3300 configurations):
+//
+//   rounds * K blocks * us  (+ what a split of K costs)
+//
+// with rounds = ceil(tiles / 256 CUs) and us the measured time a CU takes
+// for one 128-byte K block of the tile.  Structures that several workgroups of a CU
+// share have their smaller time with the CU full.  What decides, measured (the
+// general model's choice in brackets): 517 x 2112 x 1536 BF16 14.4 us (17.3); 64 x
+// 4096 x 7168 16.8 (28.6); 1024 x 4096 x 4096 39.7 (48.2); 5 experts' 2176 x 2048 x
+// 2048 36.6 as 128 x 256 and 32.6 as 128 x 192 (53.8); masked 8 x 256 x 2048 x 4096
+// FP8 33.0 (53.5); 4 experts' 8704 x 4096 x 7168 FP8 261 as 128 x 128, whose 2176
+// tiles leave 6 % of the last round idle, against 348 as 256 x 256 (544 tiles, 29 %
+// idle), where 8192 x 4096 x 7168 BF16 (512 tiles) runs 348 as 256 x 256 and over
+// 430 as 128 x 128.
+struct Structure {
+    int bm, bn, wm, wn, stages, variant;
+    int shares_cu;                 // only with more than one round: two workgroups a CU
+    double us_bf16, us_fp8;        // (FP8: a block is 128 K values, and its scales are applied)
+};
+const Structure kStructures[] = {
+    {256, 256, 4, 2, 2, 6, 0, 1.55, 1.85}, {128, 256, 2, 4, 3, 0, 0, 0.89, 1.00},
+    {128, 192, 2, 4, 3, 0, 0, 0.68, 0.83}, {128, 128, 4, 2, 4, 0, 0, 0.58, 0.62},
+    {128, 128, 2, 2, 2, 6, 1, 0.48, 0.52}, {128, 64, 4, 2, 4, 0, 0, 0.39, 0.39},
+    {64, 128, 2, 4, 4, 0, 0, 0.40, 0.40},  {64, 64, 2, 2, 4, 0, 0, 0.23, 0.23},
+    {32, 64, 1, 4, 4, 0, 0, 0.22, 0.22},   {16, 64, 1, 4, 4, 0, 0, 0.20, 0.20},
+    {16, 32, 1, 2, 6, 0, 0, 0.14, 0.14},
+};
+
+bool uses_structures(const Problem& p) {
+    return p.ep.any() || p.direct || (p.sf == 3 && (p.kind == kKGrouped || p.b_k_outer));
+}
+
+std::vector<KernelConfig> choose_structure(const Problem& p, int num_cus, const KernelConfig& base) {
+    // row blocks of a masked group: half its rows valid on average, the last block part full
+    auto row_blocks = [&](int bm) {
+        if (p.kind == kMasked) return (0.5 * p.rows / bm + 0.5) * p.g;
+        return (double)((p.rows + bm - 1) / bm) * (p.kind == kKGrouped ? p.g : 1);
+    };
+    const int kb = p.k / 128;           // (K-grouped: no constant, and the same for every structure)
+    double best = 1e30;
+    std::vector<KernelConfig> out;
+    for (const Structure& st : kStructures) {
+        const double tiles = row_blocks(st.bm) * ((p.n + st.bn - 1) / st.bn);
+        for (int sk = 1; sk <= 16; ++sk) {
+            if (sk > 1 && (p.kind != kDense || kb % sk || kb / sk < 4)) continue;
+            const double rounds = std::max(1.0, std::ceil(tiles * sk / num_cus));
+            if (sk > 1 && rounds > 1) break;
+            if (st.shares_cu && rounds < 2) continue;
+            double us = rounds * (kb / sk) * (p.sf == 3 ? st.us_bf16 : st.us_fp8);
+            // a split: the hand-off, and its FP32 partials out and back at about 4 TB/s
+            if (sk > 1) us += 1.5 + 8.0 * p.rows * p.n * sk / 4.0e6;
+            KernelConfig c = base;
+            c.bm = st.bm; c.bn = st.bn; c.wm = st.wm; c.wn = st.wn;
+            c.stages = st.stages; c.variant = st.variant; c.splitk = sk; c.kstep = 1;
+            if (us < best && valid(c, p)) {
+                best = us;
+                out = {c};
+            }
+        }
+    }
+    return out;
+}
+
 // DG_FORCE_CONFIG="bm,bn,wm,wn,stages,splitk[,kstep[,variant[,nb,ne]]]", or
 // several such launches over column ranges [nb, ne) separated by ';'.
 std::vector<KernelConfig> parse_forced(const KernelConfig& base) {
@@ -348,12 +413,18 @@ std::vector<KernelConfig> select_plan(const Problem& p, int num_cus) {
     base.k = p.k;
     base.g = (p.kind == kDense) ? 1 : p.g;
     base.ep = p.ep;
+    // operands read as stored keep that through every choice below
     base.a_kout = p.direct && p.kind == kKGrouped;
     base.b_kout = p.direct;
 
     std::vector<KernelConfig> forced = parse_forced(base);
     if (valid_plan(forced, p)) return with_b_streams(forced, p);
-    std::vector<KernelConfig> table = with_b_streams(tuned(p, num_cus, base), p);
+    std::vector<KernelConfig> table;
+    // (the contiguous entries are for any large row count; the structures weigh its rounds)
+    if (!uses_structures(p) || p.kind == kDense || p.kind == kMasked) table = tuned(p, num_cus, base);
+    if (p.direct) table.clear();
+    if (table.empty() && uses_structures(p)) table = choose_structure(p, num_cus, base);
+    table = with_b_streams(table, p);
     if (valid_plan(table, p)) {
         if (env_flag("DG_PRINT_CONFIGS"))
             for (const KernelConfig& c : table)

@@ -73,47 +73,61 @@ dg_transpose_bf16_kernel(const u16* __restrict__ X, u16* __restrict__ Xt, int ro
 }
 
 // ---------------------------------------------------------------- activation and bias gradient
-// d act / d z in FP32 (the device library's exp and erf: the bias gradient stays
-// FP32, so these are not rounded to BF16).  Past |z| = 16 the slopes are 0 or 1 to
-// the last bit (SiLU: past 200 its tail is below FP32); z is cut there, so that
-// no infinity meets a zero.  A NaN stays a NaN.
+// d act / d z in FP32.  exp2 and the reciprocal are the hardware's (1 ulp), Phi is
+// Abramowitz and Stegun 7.1.26 as in the forward epilogue (|error| < 0.75e-7, its
+// e^(-z^2/2) shared with the density): errors of FP32's own size, which the bias
+// gradient's sum averages.  With the device library's expf, erff and division the
+// pass was bound by its arithmetic: BEFOREAFTER.
+// Past |z| = 16 the slopes are 0 or 1 to the last bit (SiLU: past 200 its tail is
+// below FP32); z is cut there, so that no infinity meets a zero.  A NaN stays a NaN.
+__device__ __forceinline__ float cut(float z, float far) { return z > far ? far : z < -far ? -far : z; }
+__device__ __forceinline__ float logistic2(float x) {      // 1 / (1 + 2^-x)
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x));
+}
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
     if constexpr (ACT == DG_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
     if constexpr (ACT == DG_ACT_SILU) {
-        z = z > 200.f ? 200.f : z < -200.f ? -200.f : z;
-        const float s = 1.f / (1.f + expf(-z));
-        return s * (1.f + z * (1.f - s));
+        z = cut(z, 200.f);
+        const float s = logistic2(1.44269504f * z);
+        return s * __builtin_fmaf(z, 1.f - s, 1.f);
     }
     if constexpr (ACT == DG_ACT_GELU) {
-        z = z > 16.f ? 16.f : z < -16.f ? -16.f : z;
-        return 0.5f * (1.f + erff(0.70710678f * z)) + 0.39894228f * z * expf(-0.5f * z * z);
+        z = cut(z, 16.f);
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.70710678f, __builtin_fabsf(z), 1.f));
+        const float e = __builtin_amdgcn_exp2f(-0.72134752f * z * z);
+        float y = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+        y = __builtin_fmaf(t, y, 1.421413741f);
+        y = __builtin_fmaf(t, y, -0.284496736f);
+        y = __builtin_fmaf(t, y, 0.254829592f);
+        const float half_erfc = 0.5f * t * y * e;
+        return __builtin_fmaf(0.39894228f * z, e, z < 0.f ? half_erfc : 1.f - half_erfc);
     }
     if constexpr (ACT == DG_ACT_GELU_TANH) {
-        z = z > 16.f ? 16.f : z < -16.f ? -16.f : z;
-        const float s = 1.f / (1.f + expf(-1.59576912f * z * (1.f + 0.044715f * z * z)));
-        return s + z * s * (1.f - s) * 1.59576912f * (1.f + 0.134145f * z * z);
+        z = cut(z, 16.f);
+        const float s = logistic2(2.30220820f * z * __builtin_fmaf(0.044715f * z, z, 1.f));
+        return __builtin_fmaf(z * s * (1.f - s), __builtin_fmaf(0.21406445f * z, z, 1.59576912f), s);
     }
     return 1.f;
 }
 
 // dZ = dD slope(Z), and the column sums of dZ (FP32, before its rounding) of the
-// workgroup's rows.  A workgroup takes 512 columns of kChunk rows: 8 columns a
-// lane, its four waves every fourth row.  A wave's loads are all issued before
-// its first use of one (kChunk / 4 rows of dD and Z in flight), the waves' sums
-// meet in LDS and are added in wave order.  Contiguous form: the rows of a chunk
-// (kChunk divides 128) belong to the expert of its first row; padding rows (-1)
+// workgroup's rows.  A workgroup takes 512 columns of `chunk` rows, 16 at a time:
+// 8 columns a lane, its four waves every fourth row.  A wave's loads of the 16
+// are all issued before its first use of one (4 rows of dD and Z in flight), the
+// waves' sums meet in LDS and are added in wave order.  Contiguous form: the rows
+// of a chunk (it divides 128) belong to the expert of its first row; padding rows (-1)
 // get dZ = 0, rows past the last segment are untouched.  partial [chunks][N], or
 // nullptr: no bias gradient.
-constexpr int kChunk = 16;
-constexpr int kWaveRows = kChunk / 4;
+constexpr int kStep = 16;                 // rows a workgroup holds at once
+constexpr int kWaveRows = kStep / 4;
 struct BackwardArgs {
     const u16* dD;
     const u16* Z;
     const int* m_indices;
     u16* dZ;
     float* partial;
-    int rows, N, G;
+    int rows, N, G, chunk;
 };
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256) dg_epilogue_backward_kernel(const BackwardArgs a) {
@@ -126,18 +140,10 @@ __global__ void __launch_bounds__(256) dg_epilogue_backward_kernel(const Backwar
     __shared__ float sums[4][512];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = (int)blockIdx.y * 512;
-    const int r0 = (int)blockIdx.x * kChunk;
+    const int first = (int)blockIdx.x * a.chunk;
+    const int last = rows - first < a.chunk ? rows : first + a.chunk;
     auto col = [&](int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 64 * i; };
-    // row i of this wave, its expert (a padding row's or none: below 0), and whether it is read
-    int expert[kWaveRows];
-#pragma unroll
-    for (int i = 0; i < kWaveRows; ++i) {
-        const int r = r0 + wave + 4 * i;
-        expert[i] = r >= rows ? kPadding - 1 : m_indices ? m_indices[r] : 0;
-    }
-    const int owner = m_indices ? m_indices[r0] : 0;
-    u32x4 d[kWaveRows], z[kWaveRows];      // eight BF16 each
-    auto load = [&](const u16* p) {
+    auto load = [&](const u16* p) {        // eight BF16
         u32x4 w = {0u, 0u, 0u, 0u};
         if constexpr (VEC) {
             if (col(0) < N) w = *(const u32x4*)(p + col(0));
@@ -148,40 +154,49 @@ __global__ void __launch_bounds__(256) dg_epilogue_backward_kernel(const Backwar
         }
         return w;
     };
-#pragma unroll
-    for (int i = 0; i < kWaveRows; ++i) {
-        d[i] = z[i] = u32x4{0u, 0u, 0u, 0u};
-        if ((u32)expert[i] < (u32)G) {
-            const u64 at = (u64)(r0 + wave + 4 * i) * N;
-            d[i] = load(dD + at);
-            if constexpr (ACT != DG_ACT_NONE) z[i] = load(Z + at);
-        }
-    }
+    const int owner = m_indices ? m_indices[first] : 0;
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int r0 = first + wave; r0 < last; r0 += kStep) {
+        // the expert of each of this wave's four rows (below 0: padding, or no row)
+        int expert[kWaveRows];
 #pragma unroll
-    for (int i = 0; i < kWaveRows; ++i) {
-        const bool real = (u32)expert[i] < (u32)G;
-        if (!real && expert[i] != kPadding) continue;
-        float v[8];
+        for (int i = 0; i < kWaveRows; ++i)
+            expert[i] = r0 + 4 * i >= last ? kPadding - 1 : m_indices ? m_indices[r0 + 4 * i] : 0;
+        u32x4 d[kWaveRows], z[kWaveRows];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = e & 1 ? bf16_hi(d[i][e >> 1]) : bf16_lo(d[i][e >> 1]);
-            if constexpr (ACT != DG_ACT_NONE)
-                if (real) v[e] *= slope<ACT>(e & 1 ? bf16_hi(z[i][e >> 1]) : bf16_lo(z[i][e >> 1]));
-            if (real && expert[i] == owner) acc[e] += v[e];
+        for (int i = 0; i < kWaveRows; ++i) {
+            d[i] = z[i] = u32x4{0u, 0u, 0u, 0u};
+            if ((u32)expert[i] < (u32)G) {
+                const u64 at = (u64)(r0 + 4 * i) * N;
+                d[i] = load(dD + at);
+                if constexpr (ACT != DG_ACT_NONE) z[i] = load(Z + at);
+            }
         }
-        if (!dZ) continue;
-        u16* dst = dZ + (u64)(r0 + wave + 4 * i) * N;
-        if constexpr (VEC) {
-            if (col(0) < N)
-                *(u32x4*)(dst + col(0)) = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
-                                                to_bf16x2(v[6], v[7])};
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col(e) < N) dst[col(e)] = to_bf16(v[e]);
+        for (int i = 0; i < kWaveRows; ++i) {
+            const bool real = (u32)expert[i] < (u32)G;
+            if (!real && expert[i] != kPadding) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = e & 1 ? bf16_hi(d[i][e >> 1]) : bf16_lo(d[i][e >> 1]);
+                if constexpr (ACT != DG_ACT_NONE)
+                    if (real) v[e] *= slope<ACT>(e & 1 ? bf16_hi(z[i][e >> 1]) : bf16_lo(z[i][e >> 1]));
+                if (real && expert[i] == owner) acc[e] += v[e];
+            }
+            if (!dZ) continue;
+            u16* dst = dZ + (u64)(r0 + 4 * i) * N;
+            if constexpr (VEC) {
+                if (col(0) < N)
+                    *(u32x4*)(dst + col(0)) = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                                                    to_bf16x2(v[6], v[7])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col(e) < N) dst[col(e)] = to_bf16(v[e]);
+            }
         }
     }
     if (!partial) return;
@@ -203,7 +218,7 @@ struct BiasSumArgs {
     const float* partial;
     const int* m_indices;
     float* dbias;
-    int chunks, N;
+    int chunks, chunk, N;
 };
 __global__ void __launch_bounds__(64 * kSumWaves) dg_bias_sum_kernel(const BiasSumArgs a) {
     const float* __restrict__ partial = a.partial;
@@ -218,7 +233,7 @@ __global__ void __launch_bounds__(64 * kSumWaves) dg_bias_sum_kernel(const BiasS
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const bool mine = c + i < last && (!m_indices || m_indices[(u64)(c + i) * kChunk] == g);
+            const bool mine = c + i < last && (!m_indices || m_indices[(u64)(c + i) * a.chunk] == g);
             v[i] = mine && n < a.N ? partial[(u64)(c + i) * a.N + n] : 0.f;
         }
 #pragma unroll
@@ -260,7 +275,10 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
     if (G > 65535 || N > 65535 * 512)
         return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many groups or columns for one launch");
     const hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
-    const int chunks = (int)(((int64_t)rows + kChunk - 1) / kChunk);
+    // 64 rows a workgroup where that still gives four to each compute unit, else 16
+    const int64_t wide = ((int64_t)rows + 63) / 64 * ((N + 511) / 512);
+    const int chunk = wide >= 1024 ? 64 : kStep;
+    const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
     float* partial = nullptr;
     if (dbias && chunks > 0) {
         dg_status s = stream_scratch(stream_ptr, (size_t)chunks * (size_t)N * sizeof(float), &partial);
@@ -272,13 +290,13 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
                 : act == DG_ACT_GELU ? launch_backward<DG_ACT_GELU>
                 : act == DG_ACT_GELU_TANH ? launch_backward<DG_ACT_GELU_TANH> : launch_backward<DG_ACT_NONE>;
         f(grid, stream, BackwardArgs{static_cast<const u16*>(dD), static_cast<const u16*>(Z), m_indices,
-                                     static_cast<u16*>(dZ), partial, rows, N, G});
+                                     static_cast<u16*>(dZ), partial, rows, N, G, chunk});
         dg_status s = launched("epilogue_backward");
         if (s != DG_OK) return s;
     }
     if (dbias) {
         hipLaunchKernelGGL(dg_bias_sum_kernel, dim3((N + 63) / 64, G), dim3(64 * kSumWaves), 0, stream,
-                           BiasSumArgs{partial, m_indices, dbias, chunks, N});
+                           BiasSumArgs{partial, m_indices, dbias, chunks, chunk, N});
         return launched("epilogue_backward (bias)");
     }
     return DG_OK;

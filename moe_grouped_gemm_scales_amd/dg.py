@@ -583,6 +583,7 @@ m_grouped_fp8_gemm_nn_contiguous = dg_m_grouped_fp8_gemm_nn_contiguous
 
 # ---------------------------------------------------------------- BF16 x BF16 (unscaled)
 KIND_BF16 = 16       # DG_BF16: OR into `kind` of precompile / describe_config (K in elements)
+LAYOUT_NN = 128      # DG_LAYOUT_NN: with KIND_BF16, the NN product
 
 
 def _bf(t: torch.Tensor, name: str, shape):
