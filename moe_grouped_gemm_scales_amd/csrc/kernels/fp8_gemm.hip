@@ -565,22 +565,30 @@ __device__ __forceinline__ v4f bf16x4(v2u32 w) {
                __builtin_bit_cast(float, w.y << 16), __builtin_bit_cast(float, w.y & 0xffff0000u)};
 }
 constexpr bool VEC4 = N % 4 == 0 && N_END % 4 == 0;      // a lane's four columns are one aligned piece
+// Two values as BF16 by the hardware's packed conversion (nearest-even, a NaN quiet):
+// one instruction where the bit arithmetic of the plain epilogue takes about twelve,
+// which beside an activation is time: CVTMEASURED.
+__device__ __forceinline__ u32 cvt_pair(float x, float y) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(u32, __builtin_convertvector((v2f{x, y}), v2bf));
+}
 
 // Four columns n .. n + 3 of a lane at element offset off, as BF16.
 __device__ __forceinline__ void store4(u16* base, u64 off, int n, v4f v) {
     if constexpr (VEC4) {
-        if (n < N_END) *(v4u16*)(base + off) = v4u16{f32_to_bf16(v.x), f32_to_bf16(v.y), f32_to_bf16(v.z), f32_to_bf16(v.w)};
+        if (n < N_END) *(v2u32*)(base + off) = v2u32{cvt_pair(v.x, v.y), cvt_pair(v.z, v.w)};
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (n + e < N_END) base[off + e] = f32_to_bf16(v[e]);
+            if (n + e < N_END) base[off + e] = (u16)cvt_pair(v[e], 0.f);
     }
 }
 // Two sub-tiles' columns (n and n + 16) of a lane as one 16-byte store: lanes 16
 // apart swap four values (see the plain epilogue).  Every lane of the row calls it.
 __device__ __forceinline__ void store_pair(u16* base, u64 row_off, int n, bool odd, v4f v0, v4f v1) {
-    const u32 lo0 = bf16_pair(v0.x, v0.y), hi0 = bf16_pair(v0.z, v0.w);
-    const u32 lo1 = bf16_pair(v1.x, v1.y), hi1 = bf16_pair(v1.z, v1.w);
+    const u32 lo0 = cvt_pair(v0.x, v0.y), hi0 = cvt_pair(v0.z, v0.w);
+    const u32 lo1 = cvt_pair(v1.x, v1.y), hi1 = cvt_pair(v1.z, v1.w);
     const u32 r_lo = (u32)__builtin_amdgcn_ds_swizzle((int)(odd ? lo0 : lo1), 0x401F);
     const u32 r_hi = (u32)__builtin_amdgcn_ds_swizzle((int)(odd ? hi0 : hi1), 0x401F);
     const int n_out = odd ? n + 12 : n;
