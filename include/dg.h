@@ -390,10 +390,15 @@ dg_status dg_m_grouped_epilogue_backward_contiguous(const void *dD, const void *
  *   tn  A [K][M], B [K][N]; any K, 0 included (D = C, or zeros)
  *   k_grouped tn  A [K][M], B [K][N], ks int32 [G] (device): consecutive K
  *       segments of the groups, multiples of 128, as for the FP8 form; C, D
- *       [G][M][N], an empty group gets C or zeros; K a multiple of 128
- * Operands stored K-outermost are first rewritten K-contiguous into the
- * stream's workspace: G * N * K * 2 bytes for nn, (M + N) * ceil(K/512) * 1024
- * for tn.
+ *       [G][M][N], an empty group gets C or zeros; K a multiple of 128.  A
+ *       segment's padding rows are part of its sum: they must be zero in one
+ *       operand (dispatch and the epilogue's backward pass clear them) and
+ *       finite in the other (a product leaves them untouched, so clear a new
+ *       buffer once); rows past the segments are not read
+ * The K-outermost operands are read as they are stored where their rows are
+ * 16-byte aligned (N, for tn also M, a multiple of 8) and under 4 GiB (a group
+ * of them); otherwise they are first rewritten K-contiguous into the stream's
+ * workspace: G * N * K * 2 bytes for nn, (M + N) * ceil(K/512) * 1024 for tn.
  */
 dg_status dg_bf16_gemm_nn(const void *A, const void *B, const float *C, void *D, int M, int N, int K, void *stream);
 dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void *A, const void *B, const int32_t *m_indices, const float *C,

@@ -868,77 +868,97 @@ dg_status dg_m_grouped_fp4_fp4_gemm_nt_masked(const void* A, const int32_t* sfa,
 // ---- fused epilogue
 dg_status dg_bf16_gemm_nt_epilogue(const void* A, const void* B, const dg_epilogue* epilogue, void* D, int M, int N,
                                    int K, void* stream) {
-    Epilogue ep;
-    EpilogueArgs args;
-    dg_status s = read_epilogue(epilogue, &ep, &args);
-    return s != DG_OK ? s : bf16_gemm(kDense, A, B, nullptr, nullptr, D, M, N, K, 1, stream, 0, ep, args);
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : bf16_gemm(kDense, A, B, nullptr, nullptr, D, M, N, K, 1, stream, 0, ep, args);
+    });
 }
 
 dg_status dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(const void* A, const void* B, const int32_t* m_indices,
                                                         const dg_epilogue* epilogue, void* D, int M, int N, int K,
                                                         int num_groups, void* stream) {
-    Epilogue ep;
-    EpilogueArgs args;
-    dg_status s = read_epilogue(epilogue, &ep, &args);
-    return s != DG_OK ? s : bf16_gemm(kContiguous, A, B, m_indices, nullptr, D, M, N, K, num_groups, stream, 0, ep, args);
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : bf16_gemm(kContiguous, A, B, m_indices, nullptr, D, M, N, K, num_groups, stream, 0, ep, args);
+    });
 }
 
 dg_status dg_m_grouped_bf16_gemm_nt_masked_epilogue(const void* A, const void* B, const int32_t* masked_m,
                                                     const dg_epilogue* epilogue, void* D, int M_max, int N, int K,
                                                     int num_groups, void* stream) {
-    Epilogue ep;
-    EpilogueArgs args;
-    dg_status s = read_epilogue(epilogue, &ep, &args);
-    return s != DG_OK ? s : bf16_gemm(kMasked, A, B, masked_m, nullptr, D, M_max, N, K, num_groups, stream, 0, ep, args);
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : bf16_gemm(kMasked, A, B, masked_m, nullptr, D, M_max, N, K, num_groups, stream, 0, ep, args);
+    });
 }
 
 dg_status dg_fp8_gemm_nt_epilogue(const void* A, const float* sfa, const void* B, const float* sfb,
                                   const dg_epilogue* epilogue, void* D, int M, int N, int K, void* stream) {
-    Epilogue ep;
-    EpilogueArgs args;
-    dg_status s = read_epilogue(epilogue, &ep, &args);
-    return s != DG_OK ? s : dense(A, sfa, B, sfb, nullptr, D, M, N, K, 0, stream, 0, 0, ep, args);
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : dense(A, sfa, B, sfb, nullptr, D, M, N, K, 0, stream, 0, 0, ep, args);
+    });
 }
 
 dg_status dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(const void* A, const float* sfa, const void* B, const float* sfb,
                                                        const int32_t* m_indices, const dg_epilogue* epilogue, void* D,
                                                        int M, int N, int K, int num_groups, void* stream) {
-    Epilogue ep;
-    EpilogueArgs args;
-    dg_status s = read_epilogue(epilogue, &ep, &args);
-    return s != DG_OK ? s : contiguous(A, sfa, B, sfb, m_indices, nullptr, D, M, N, K, num_groups, 0, stream, 0, ep, args);
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : contiguous(A, sfa, B, sfb, m_indices, nullptr, D, M, N, K, num_groups, 0, stream, 0, ep, args);
+    });
 }
 
 dg_status dg_m_grouped_fp8_gemm_nt_masked_epilogue(const void* A, const float* sfa, const void* B, const float* sfb,
                                                    const int32_t* masked_m, const dg_epilogue* epilogue, void* D,
                                                    int M_max, int N, int K, int num_groups, void* stream) {
-    Epilogue ep;
-    EpilogueArgs args;
-    dg_status s = read_epilogue(epilogue, &ep, &args);
-    return s != DG_OK ? s : masked(A, sfa, B, sfb, masked_m, nullptr, D, M_max, N, K, num_groups, 0, stream, ep, args);
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : masked(A, sfa, B, sfb, masked_m, nullptr, D, M_max, N, K, num_groups, 0, stream, ep, args);
+    });
 }
 
 // ---- BF16 products of the backward pass
 dg_status dg_bf16_gemm_nn(const void* A, const void* B, const float* C, void* D, int M, int N, int K, void* stream) {
-    return bf16_gemm(kDense, A, B, nullptr, C, D, M, N, K, 1, stream, 1);
+    return guarded([&]() -> dg_status {
+        return bf16_gemm(kDense, A, B, nullptr, C, D, M, N, K, 1, stream, 1);
+    });
 }
 
 dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void* A, const void* B, const int32_t* m_indices, const float* C,
                                                void* D, int M, int N, int K, int num_groups, void* stream) {
-    return bf16_gemm(kContiguous, A, B, m_indices, C, D, M, N, K, num_groups, stream, 1);
+    return guarded([&]() -> dg_status {
+        return bf16_gemm(kContiguous, A, B, m_indices, C, D, M, N, K, num_groups, stream, 1);
+    });
 }
 
 dg_status dg_bf16_gemm_tn(const void* A, const void* B, const float* C, void* D, int M, int N, int K, void* stream) {
-    return bf16_gemm_tn(A, B, nullptr, C, D, M, N, K, 1, stream);
+    return guarded([&]() -> dg_status {
+        return bf16_gemm_tn(A, B, nullptr, C, D, M, N, K, 1, stream);
+    });
 }
 
 dg_status dg_k_grouped_bf16_gemm_tn_contiguous(const void* A, const void* B, const int32_t* ks, const float* C, void* D,
                                                int M, int N, int K, int num_groups, void* stream) {
-    if (!ks) return set_error(DG_ERR_INVALID_ARG, "ks must be non-NULL");
-    if (num_groups <= 0) return set_error(DG_ERR_INVALID_ARG, "num_groups must be positive");
-    if (!aligned(ks, 4)) return set_error(DG_ERR_ALIGNMENT, "ks must be 4-byte aligned");
-    if (K % 128 != 0) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (whole segments)");
-    return bf16_gemm_tn(A, B, ks, C, D, M, N, K, num_groups, stream);
+    return guarded([&]() -> dg_status {
+        if (!ks) return set_error(DG_ERR_INVALID_ARG, "ks must be non-NULL");
+        if (num_groups <= 0) return set_error(DG_ERR_INVALID_ARG, "num_groups must be positive");
+        if (!aligned(ks, 4)) return set_error(DG_ERR_ALIGNMENT, "ks must be 4-byte aligned");
+        if (K % 128 != 0) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (whole segments)");
+        return bf16_gemm_tn(A, B, ks, C, D, M, N, K, num_groups, stream);
+    });
 }
 
 }  // extern "C"

@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -162,5 +163,20 @@ dg_status stream_scratch(void* stream, size_t bytes, float** out);
 // Errors (api.cpp).
 dg_status set_error(dg_status s, const std::string& msg);
 bool env_flag(const char* name);
+
+// Body of a C entry point: an exception (an allocation that fails in the plan or
+// workspace maps, a message that cannot be built) comes back as a status.
+template <typename F>
+dg_status guarded(F&& body) noexcept {
+    try {
+        return body();
+    } catch (const std::exception& e) {
+        try {
+            return set_error(DG_ERR_HIP, std::string("host error: ") + e.what());
+        } catch (...) {
+            return DG_ERR_HIP;
+        }
+    }
+}
 
 }  // namespace dg

@@ -325,16 +325,20 @@ extern "C" {
 
 dg_status dg_epilogue_backward(const void* dD, const void* Z, int activation, void* dZ, float* dbias, int M, int N,
                                void* stream) {
-    return epilogue_backward(dD, Z, activation, nullptr, dZ, dbias, M, N, 1, stream);
+    return guarded([&]() -> dg_status {
+        return epilogue_backward(dD, Z, activation, nullptr, dZ, dbias, M, N, 1, stream);
+    });
 }
 
 dg_status dg_m_grouped_epilogue_backward_contiguous(const void* dD, const void* Z, int activation,
                                                     const int32_t* m_indices, void* dZ, float* dbias, int M, int N,
                                                     int num_groups, void* stream) {
-    if (!m_indices && M != 0) return set_error(DG_ERR_INVALID_ARG, "m_indices must be non-NULL");
-    if (M > 0 && M % dg_get_mk_alignment_for_contiguous_layout() != 0)
-        return set_error(DG_ERR_ALIGNMENT, "contiguous M must be a multiple of the M alignment (128)");
-    return epilogue_backward(dD, Z, activation, m_indices, dZ, dbias, M, N, num_groups, stream);
+    return guarded([&]() -> dg_status {
+        if (!m_indices && M != 0) return set_error(DG_ERR_INVALID_ARG, "m_indices must be non-NULL");
+        if (M > 0 && M % dg_get_mk_alignment_for_contiguous_layout() != 0)
+            return set_error(DG_ERR_ALIGNMENT, "contiguous M must be a multiple of the M alignment (128)");
+        return epilogue_backward(dD, Z, activation, m_indices, dZ, dbias, M, N, num_groups, stream);
+    });
 }
 
 }  // extern "C"

@@ -676,98 +676,110 @@ int64_t dg_moe_sorted_rows(int T, int topk, int num_experts) {
 
 dg_status dg_moe_sort_contiguous(const int32_t* expert_ids, int32_t* pos, int32_t* m_indices, int32_t* ks, int T,
                                  int topk, int num_experts, int rows, void* stream) {
-    dg_status s = check_sort(expert_ids, pos, ks, T, topk, num_experts);
-    if (s != DG_OK) return s;
-    if (rows != 0 && !m_indices) return set_error(DG_ERR_INVALID_ARG, "moe_sort: NULL pointer");
-    if (!aligned(m_indices, 4)) return set_error(DG_ERR_ALIGNMENT, "moe_sort: arrays must be 4-byte aligned");
-    if (rows < 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: rows must not be negative");
-    if (rows % kAlign) return set_error(DG_ERR_ALIGNMENT, "moe_sort: rows must be a multiple of the M alignment (128)");
-    return sort(expert_ids, pos, m_indices, ks, T, topk, num_experts, 0, rows, stream);
+    return guarded([&]() -> dg_status {
+        dg_status s = check_sort(expert_ids, pos, ks, T, topk, num_experts);
+        if (s != DG_OK) return s;
+        if (rows != 0 && !m_indices) return set_error(DG_ERR_INVALID_ARG, "moe_sort: NULL pointer");
+        if (!aligned(m_indices, 4)) return set_error(DG_ERR_ALIGNMENT, "moe_sort: arrays must be 4-byte aligned");
+        if (rows < 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: rows must not be negative");
+        if (rows % kAlign) return set_error(DG_ERR_ALIGNMENT, "moe_sort: rows must be a multiple of the M alignment (128)");
+        return sort(expert_ids, pos, m_indices, ks, T, topk, num_experts, 0, rows, stream);
+    });
 }
 
 dg_status dg_moe_sort_masked(const int32_t* expert_ids, int32_t* pos, int32_t* masked_m, int T, int topk,
                              int num_experts, int M_max, void* stream) {
-    dg_status s = check_sort(expert_ids, pos, masked_m, T, topk, num_experts);
-    if (s != DG_OK) return s;
-    if (M_max <= 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: M_max must be positive");
-    if ((int64_t)M_max * num_experts > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_sort: more than 2^31 rows");
-    return sort(expert_ids, pos, nullptr, masked_m, T, topk, num_experts, M_max, M_max * num_experts, stream);
+    return guarded([&]() -> dg_status {
+        dg_status s = check_sort(expert_ids, pos, masked_m, T, topk, num_experts);
+        if (s != DG_OK) return s;
+        if (M_max <= 0) return set_error(DG_ERR_INVALID_ARG, "moe_sort: M_max must be positive");
+        if ((int64_t)M_max * num_experts > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_sort: more than 2^31 rows");
+        return sort(expert_ids, pos, nullptr, masked_m, T, topk, num_experts, M_max, M_max * num_experts, stream);
+    });
 }
 
 dg_status dg_moe_dispatch_bf16(const void* X, const int32_t* pos, const int32_t* m_indices, void* rows_out, int T,
                                int topk, int rows, int H, void* stream) {
-    dg_status s = check_rows("moe_dispatch_bf16", X, pos, rows_out, T, topk, rows, H);
-    if (s != DG_OK) return s;
-    if (m_indices && !aligned(m_indices, 4))
-        return set_error(DG_ERR_ALIGNMENT, "moe_dispatch_bf16: m_indices must be 4-byte aligned");
-    const int pieces = (H + kPiece - 1) / kPiece;
-    const int64_t units = ((int64_t)T + (m_indices ? pad_blocks(rows) : 0)) * pieces;
-    if (units == 0) return DG_OK;
-    const unsigned grid = grid_of(units);
-    if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_bf16: too many tokens for one launch");
-    hipLaunchKernelGGL(H % 8 == 0 ? dg_moe_dispatch_bf16_kernel<true> : dg_moe_dispatch_bf16_kernel<false>, dim3(grid),
-                       dim3(256), 0, static_cast<hipStream_t>(stream),
-                       DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, nullptr, T, topk, rows, rows, H, pieces});
-    return launched("moe_dispatch_bf16");
+    return guarded([&]() -> dg_status {
+        dg_status s = check_rows("moe_dispatch_bf16", X, pos, rows_out, T, topk, rows, H);
+        if (s != DG_OK) return s;
+        if (m_indices && !aligned(m_indices, 4))
+            return set_error(DG_ERR_ALIGNMENT, "moe_dispatch_bf16: m_indices must be 4-byte aligned");
+        const int pieces = (H + kPiece - 1) / kPiece;
+        const int64_t units = ((int64_t)T + (m_indices ? pad_blocks(rows) : 0)) * pieces;
+        if (units == 0) return DG_OK;
+        const unsigned grid = grid_of(units);
+        if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_bf16: too many tokens for one launch");
+        hipLaunchKernelGGL(H % 8 == 0 ? dg_moe_dispatch_bf16_kernel<true> : dg_moe_dispatch_bf16_kernel<false>, dim3(grid),
+                           dim3(256), 0, static_cast<hipStream_t>(stream),
+                           DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, nullptr, T, topk, rows, rows, H, pieces});
+        return launched("moe_dispatch_bf16");
+    });
 }
 
 dg_status dg_moe_dispatch_fp8(const void* X, const int32_t* pos, const int32_t* m_indices, void* rows_out, void* sf,
                               int T, int topk, int rows, int group_rows, int H, int ue8m0, void* stream) {
-    dg_status s = check_rows("moe_dispatch_fp8", X, pos, rows_out, T, topk, rows, H);
-    if (s != DG_OK) return s;
-    if (!sf && rows != 0) return set_error(DG_ERR_INVALID_ARG, "moe_dispatch_fp8: NULL pointer");
-    if (!aligned(sf, 4) || (m_indices && !aligned(m_indices, 4)))
-        return set_error(DG_ERR_ALIGNMENT, "moe_dispatch_fp8: scales and m_indices must be 4-byte aligned");
-    if (H % 128) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: H must be a multiple of 128 (the scale block)");
-    if (rows > 0 && (group_rows <= 0 || rows % group_rows))
-        return set_error(DG_ERR_INVALID_ARG, "moe_dispatch_fp8: rows must be a multiple of group_rows");
-    const int pieces = (H + kPiece - 1) / kPiece;
-    const int64_t units = ((int64_t)T + (m_indices ? pad_blocks(rows) : 0)) * pieces;
-    if (units == 0 || rows == 0) return DG_OK;
-    const unsigned grid = grid_of(units);
-    if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: too many tokens for one launch");
-    hipLaunchKernelGGL(ue8m0 ? dg_moe_dispatch_fp8_kernel<true> : dg_moe_dispatch_fp8_kernel<false>, dim3(grid),
-                       dim3(256), 0, static_cast<hipStream_t>(stream),
-                       DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, static_cast<u32*>(sf), T, topk, rows,
-                                    group_rows, H, pieces});
-    return launched("moe_dispatch_fp8");
+    return guarded([&]() -> dg_status {
+        dg_status s = check_rows("moe_dispatch_fp8", X, pos, rows_out, T, topk, rows, H);
+        if (s != DG_OK) return s;
+        if (!sf && rows != 0) return set_error(DG_ERR_INVALID_ARG, "moe_dispatch_fp8: NULL pointer");
+        if (!aligned(sf, 4) || (m_indices && !aligned(m_indices, 4)))
+            return set_error(DG_ERR_ALIGNMENT, "moe_dispatch_fp8: scales and m_indices must be 4-byte aligned");
+        if (H % 128) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: H must be a multiple of 128 (the scale block)");
+        if (rows > 0 && (group_rows <= 0 || rows % group_rows))
+            return set_error(DG_ERR_INVALID_ARG, "moe_dispatch_fp8: rows must be a multiple of group_rows");
+        const int pieces = (H + kPiece - 1) / kPiece;
+        const int64_t units = ((int64_t)T + (m_indices ? pad_blocks(rows) : 0)) * pieces;
+        if (units == 0 || rows == 0) return DG_OK;
+        const unsigned grid = grid_of(units);
+        if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: too many tokens for one launch");
+        hipLaunchKernelGGL(ue8m0 ? dg_moe_dispatch_fp8_kernel<true> : dg_moe_dispatch_fp8_kernel<false>, dim3(grid),
+                           dim3(256), 0, static_cast<hipStream_t>(stream),
+                           DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, static_cast<u32*>(sf), T, topk, rows,
+                                        group_rows, H, pieces});
+        return launched("moe_dispatch_fp8");
+    });
 }
 
 dg_status dg_moe_combine(const void* rows_in, const int32_t* pos, const float* weights, const void* residual, void* Y,
                          int T, int topk, int rows, int N, void* stream) {
-    dg_status s = check_rows("moe_combine", Y, pos, rows_in, T, topk, rows, N);
-    if (s != DG_OK) return s;
-    if ((residual && !aligned(residual, 16)) || (weights && !aligned(weights, 4)))
-        return set_error(DG_ERR_ALIGNMENT, "moe_combine: residual must be 16-byte, weights 4-byte aligned");
-    const int pieces = (N + 511) / 512;
-    if (T == 0) return DG_OK;
-    const unsigned grid = grid_of((int64_t)T * pieces);
-    if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_combine: too many tokens for one launch");
-    hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_kernel<true> : dg_moe_combine_kernel<false>, dim3(grid), dim3(256), 0,
-                       static_cast<hipStream_t>(stream),
-                       CombineArgs{static_cast<const u16*>(rows_in), pos, weights, static_cast<const u16*>(residual),
-                                   static_cast<u16*>(Y), T, topk, rows, N, pieces});
-    return launched("moe_combine");
+    return guarded([&]() -> dg_status {
+        dg_status s = check_rows("moe_combine", Y, pos, rows_in, T, topk, rows, N);
+        if (s != DG_OK) return s;
+        if ((residual && !aligned(residual, 16)) || (weights && !aligned(weights, 4)))
+            return set_error(DG_ERR_ALIGNMENT, "moe_combine: residual must be 16-byte, weights 4-byte aligned");
+        const int pieces = (N + 511) / 512;
+        if (T == 0) return DG_OK;
+        const unsigned grid = grid_of((int64_t)T * pieces);
+        if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_combine: too many tokens for one launch");
+        hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_kernel<true> : dg_moe_combine_kernel<false>, dim3(grid), dim3(256), 0,
+                           static_cast<hipStream_t>(stream),
+                           CombineArgs{static_cast<const u16*>(rows_in), pos, weights, static_cast<const u16*>(residual),
+                                       static_cast<u16*>(Y), T, topk, rows, N, pieces});
+        return launched("moe_combine");
+    });
 }
 
 dg_status dg_moe_combine_backward(const void* dY, const void* rows_in, const int32_t* pos, const float* weights,
                                   const int32_t* m_indices, void* d_rows, float* d_weights, int T, int topk, int rows,
                                   int N, void* stream) {
-    dg_status s = check_rows("moe_combine_backward", dY, pos, d_rows, T, topk, rows, N);
-    if (s != DG_OK) return s;
-    if (d_weights && !rows_in && rows != 0)
-        return set_error(DG_ERR_INVALID_ARG, "moe_combine_backward: the weights' gradient needs the rows");
-    if ((rows_in && !aligned(rows_in, 16)) || (weights && !aligned(weights, 4)) || (d_weights && !aligned(d_weights, 4)) ||
-        (m_indices && !aligned(m_indices, 4)))
-        return set_error(DG_ERR_ALIGNMENT, "moe_combine_backward: rows must be 16-byte, the other arrays 4-byte aligned");
-    const int64_t blocks = (int64_t)T + (m_indices ? pad_blocks(rows) : 0);
-    if (blocks == 0) return DG_OK;
-    if (blocks > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_combine_backward: too many tokens for one launch");
-    hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_backward_kernel<true> : dg_moe_combine_backward_kernel<false>,
-                       dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
-                       CombineBackwardArgs{static_cast<const u16*>(dY), static_cast<const u16*>(rows_in), pos, weights,
-                                           m_indices, static_cast<u16*>(d_rows), d_weights, T, topk, rows, N});
-    return launched("moe_combine_backward");
+    return guarded([&]() -> dg_status {
+        dg_status s = check_rows("moe_combine_backward", dY, pos, d_rows, T, topk, rows, N);
+        if (s != DG_OK) return s;
+        if (d_weights && !rows_in && rows != 0)
+            return set_error(DG_ERR_INVALID_ARG, "moe_combine_backward: the weights' gradient needs the rows");
+        if ((rows_in && !aligned(rows_in, 16)) || (weights && !aligned(weights, 4)) || (d_weights && !aligned(d_weights, 4)) ||
+            (m_indices && !aligned(m_indices, 4)))
+            return set_error(DG_ERR_ALIGNMENT, "moe_combine_backward: rows must be 16-byte, the other arrays 4-byte aligned");
+        const int64_t blocks = (int64_t)T + (m_indices ? pad_blocks(rows) : 0);
+        if (blocks == 0) return DG_OK;
+        if (blocks > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_combine_backward: too many tokens for one launch");
+        hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_backward_kernel<true> : dg_moe_combine_backward_kernel<false>,
+                           dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+                           CombineBackwardArgs{static_cast<const u16*>(dY), static_cast<const u16*>(rows_in), pos, weights,
+                                               m_indices, static_cast<u16*>(d_rows), d_weights, T, topk, rows, N});
+        return launched("moe_combine_backward");
+    });
 }
 
 }  // extern "C"
