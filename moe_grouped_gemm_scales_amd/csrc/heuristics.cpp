@@ -282,8 +282,8 @@ std::vector<KernelConfig> tuned(const Problem& p, int num_cus, const KernelConfi
 }
 
 // The products with a fused epilogue and the BF16 NN and TN products choose among
-// these structures by a short cost sum fitted to sweeps of them on an MI355X (20
-// shapes of 1 to 8704 rows, BF16 and FP8, every form, 3300 configurations):
+// these structures by a short cost sum fitted to sweeps of them on an MI355X (31
+// shapes of 1 to 17408 rows, BF16 and FP8, every form, 4100 configurations):
 //
 //   rounds * K blocks * us  (+ what a split of K costs)
 //
@@ -292,7 +292,8 @@ std::vector<KernelConfig> tuned(const Problem& p, int num_cus, const KernelConfi
 // share have their smaller time with the CU full.  What decides, measured (the
 // general model's choice in brackets): 517 x 2112 x 1536 BF16 14.4 us (17.3); 64 x
 // 4096 x 7168 16.8 (28.6); 1024 x 4096 x 4096 39.7 (48.2); 5 experts' 2176 x 2048 x
-// 2048 36.6 as 128 x 256 and 32.6 as 128 x 192 (53.8); masked 8 x 256 x 2048 x 4096
+// 2048 36.6 as 128 x 256 and 32.6 as 128 x 192 (53.8); 3000 x 2048 x 2048 33.9 as
+// 128 x 256 and 30.0 as 192 x 128; masked 8 x 256 x 2048 x 4096
 // FP8 33.0 (53.5); 4 experts' 8704 x 4096 x 7168 FP8 261 as 128 x 128, whose 2176
 // tiles leave 6 % of the last round idle, against 348 as 256 x 256 (544 tiles, 29 %
 // idle), where 8192 x 4096 x 7168 BF16 (512 tiles) runs 348 as 256 x 256 and over
@@ -304,11 +305,11 @@ struct Structure {
 };
 const Structure kStructures[] = {
     {256, 256, 4, 2, 2, 6, 0, 1.55, 1.85}, {128, 256, 2, 4, 3, 0, 0, 0.89, 1.00},
-    {128, 192, 2, 4, 3, 0, 0, 0.68, 0.83}, {128, 128, 4, 2, 4, 0, 0, 0.58, 0.62},
-    {128, 128, 2, 2, 2, 6, 1, 0.48, 0.52}, {128, 64, 4, 2, 4, 0, 0, 0.39, 0.39},
-    {64, 128, 2, 4, 4, 0, 0, 0.40, 0.40},  {64, 64, 2, 2, 4, 0, 0, 0.23, 0.23},
-    {32, 64, 1, 4, 4, 0, 0, 0.22, 0.22},   {16, 64, 1, 4, 4, 0, 0, 0.20, 0.20},
-    {16, 32, 1, 2, 6, 0, 0, 0.14, 0.14},
+    {128, 192, 2, 4, 3, 0, 0, 0.76, 0.83}, {192, 128, 4, 2, 3, 0, 0, 0.72, 0.83},
+    {128, 128, 4, 2, 4, 0, 0, 0.58, 0.62}, {128, 128, 2, 2, 2, 6, 1, 0.48, 0.52},
+    {128, 64, 4, 2, 4, 0, 0, 0.39, 0.39},  {64, 128, 2, 4, 4, 0, 0, 0.40, 0.40},
+    {64, 64, 2, 2, 4, 0, 0, 0.23, 0.23},   {32, 64, 1, 4, 4, 0, 0, 0.22, 0.22},
+    {16, 64, 1, 4, 4, 0, 0, 0.20, 0.20},   {16, 32, 1, 2, 6, 0, 0, 0.14, 0.14},
 };
 
 bool uses_structures(const Problem& p) {

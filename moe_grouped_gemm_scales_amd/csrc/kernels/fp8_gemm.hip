@@ -566,8 +566,7 @@ __device__ __forceinline__ v4f bf16x4(v2u32 w) {
 }
 constexpr bool VEC4 = N % 4 == 0 && N_END % 4 == 0;      // a lane's four columns are one aligned piece
 // Two values as BF16 by the hardware's packed conversion (nearest-even, a NaN quiet):
-// one instruction where the bit arithmetic of the plain epilogue takes about twelve,
-// which beside an activation is time: CVTMEASURED.
+// one instruction where the bit arithmetic of the plain epilogue takes about twelve.
 __device__ __forceinline__ u32 cvt_pair(float x, float y) {
     typedef float v2f __attribute__((ext_vector_type(2)));
     typedef __bf16 v2bf __attribute__((ext_vector_type(2)));

@@ -77,7 +77,8 @@ dg_transpose_bf16_kernel(const u16* __restrict__ X, u16* __restrict__ Xt, int ro
 // Abramowitz and Stegun 7.1.26 as in the forward epilogue (|error| < 0.75e-7, its
 // e^(-z^2/2) shared with the density): errors of FP32's own size, which the bias
 // gradient's sum averages.  With the device library's expf, erff and division the
-// pass was bound by its arithmetic: BEFOREAFTER.
+// pass was bound by its arithmetic (8192 x 4096, GELU: 55 us against 45; 2304 x
+// 2112, tanh form: 12.4 against 9.2).
 // Past |z| = 16 the slopes are 0 or 1 to the last bit (SiLU: past 200 its tail is
 // below FP32); z is cut there, so that no infinity meets a zero.  A NaN stays a NaN.
 __device__ __forceinline__ float cut(float z, float far) { return z > far ? far : z < -far ? -far : z; }

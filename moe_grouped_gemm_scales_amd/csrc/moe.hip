@@ -28,7 +28,6 @@ typedef unsigned short u16;
 typedef unsigned int u32;
 typedef unsigned long long u64;
 typedef u32 u32x4 __attribute__((ext_vector_type(4)));
-typedef u32 u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAlign = 128;            // rows an expert's segment starts on a multiple of
 constexpr int kMaxExperts = 1024;      // the sort's per-wave counters live in LDS
@@ -212,7 +211,7 @@ dg_moe_place_kernel(const SortArgs a) {
 // `fill(row)` for each row of the kPadRows-row block `blk` whose index is -1.
 // Rows past the last segment (-2) are left alone.  16 rows a wave: with 128 the
 // waves that clear a nearly empty segment outlive all others (1021 tokens x 3
-// to 7 experts, width 1000: 8.0 us; with 16 PADUS).
+// to 7 experts, width 1000: 8.0 us; with 16 3.7).
 constexpr int kPadRows = 16;
 template <typename F>
 __device__ __forceinline__ void for_padding_rows(const int* __restrict__ m_indices, int blk, int rows, F&& fill) {

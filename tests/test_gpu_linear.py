@@ -403,3 +403,36 @@ def test_layer_replays_from_a_graph():
         torch.cuda.synchronize()
         for i, (a, b) in enumerate(zip(captured, eager)):
             assert torch.equal(a, b), (seed, i)
+
+
+def test_output_past_four_gigabytes():
+    """Rows of D, Z and the residual past 32-bit byte offsets."""
+    M, N, K = 300032, 7168, 64
+    A, B = _bf((M, K), 1).cuda(), _bf((N, K), 2).cuda()
+    res = torch.ones((M, N), dtype=torch.bfloat16, device="cuda")
+    D, Z = torch.zeros_like(res), torch.zeros_like(res)
+    dg.dg_bf16_gemm_nt_epilogue(A, B, D, activation="relu", residual=res, Z=Z)
+    for r in (slice(0, 200), slice(M - 200, M), slice(149700, 149900)):
+        z = A[r].double() @ B.double().T
+        _close(Z[r].cpu(), z.cpu().numpy(), "Z")
+        _close(D[r].cpu(), (z.clamp(min=0) + 1).cpu().numpy(), "D")
+    dz, db = torch.zeros_like(res), torch.empty(N, device="cuda")
+    dg.dg_epilogue_backward(res, Z, "relu", dz, db)
+    assert torch.equal(dz[M - 200:], (Z[M - 200:] > 0).to(torch.bfloat16))
+    assert torch.equal(db.double(), (Z > 0).sum(0).double())            # counts: exact in FP32
+
+
+@pytest.mark.parametrize("N", [8184, 8200])
+def test_tn_operand_around_four_gigabytes(N):
+    """An operand just under 4 GiB is read as stored, one just over it is rewritten first."""
+    K, M = 262144, 64
+    A, B = _bf((K, M), 1).cuda(), torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    cols = torch.tensor([0, 7, 4096, N - 9, N - 1], device="cuda")
+    B[:, cols] = _bf((K, 5), 2).cuda()
+    D = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    dg.dg_bf16_gemm_tn(A, B, None, D)
+    want = A.double().T @ B[:, cols].double()
+    _close(D[:, cols].cpu(), want.cpu().numpy(), f"tn {N}")
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[cols] = False
+    assert not D[:, rest].any()

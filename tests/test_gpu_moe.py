@@ -335,3 +335,32 @@ def test_another_stream_and_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(captured, eager):
             assert torch.equal(a, b), seed
+
+
+def test_rows_past_four_gigabytes():
+    """Row and scale offsets past 32 bits: the last rows of a buffer of over 4 GiB (BF16, E4M3) are reached."""
+    H = 7168
+    R = ((1 << 32) // (2 * H) // 128 + 3) * 128
+    x = _bf((3, H), 1).cuda()
+    pos = torch.tensor([[R - 1], [R - 130], [0]], dtype=torch.int32, device="cuda")
+    rows = torch.zeros((R, H), dtype=torch.bfloat16, device="cuda")
+    dg.dg_moe_dispatch_bf16(x, pos, None, rows)
+    at = pos[:, 0].long()
+    assert torch.equal(rows[at], x) and not rows[R - 129:R - 1].any() and not rows[1:100].any()
+    y = torch.empty_like(x)
+    dg.dg_moe_combine(rows, pos, None, None, y)
+    assert torch.equal(y, x)
+    d_rows, dw = torch.zeros_like(rows), torch.empty((3, 1), device="cuda")
+    dg.dg_moe_combine_backward(x, rows, pos, None, None, d_rows, dw)
+    assert torch.equal(d_rows[at], x)
+    want = x.double().square().sum(1, keepdim=True)
+    assert torch.all((dw.double() - want).abs() <= (H + 16) * 2.0 ** -24 * want)
+    del rows, d_rows
+    R *= 2
+    pos = torch.tensor([[R - 1], [R - 130], [0]], dtype=torch.int32, device="cuda")
+    codes = torch.zeros((R, H), dtype=torch.uint8, device="cuda")
+    sf = torch.zeros((H // 128, R), device="cuda")
+    dg.dg_moe_dispatch_fp8(x, pos, None, codes, sf)
+    qc, qs, _ = ref.quantise(x.float().cpu().numpy())
+    at = pos[:, 0].long()
+    assert np.array_equal(codes[at].cpu().numpy(), qc) and np.array_equal(sf[:, at].cpu().numpy().T, qs)

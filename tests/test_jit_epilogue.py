@@ -50,3 +50,19 @@ def test_unknown_activation_is_refused():
         dg.precompile(0 | BF16 | (5 << 12), 64, 64, 64, num_cus=256)
     key = dg.describe_config(0 | dg.KIND_BF16 | dg.EPI_BIAS_F32 | dg.EPI_Z | ACT["gelu"], 64, 512, 512, num_cus=256)
     assert key.endswith("_ep1301")
+
+
+def test_every_structure_is_chosen_somewhere():
+    """Shapes over the whole range reach each of the tile structures."""
+    import itertools
+
+    import moe_grouped_gemm_scales_amd as dg
+    seen = set()
+    for kind, fp8 in itertools.product((0, 1, 2), (False, True)):
+        for M, N, K in itertools.product((1, 16, 24, 64, 200, 517, 1024, 3000, 8192, 32768), (520, 2112, 4096, 7168), (1536, 7168)):
+            if kind == 1:
+                M = (M + 127) // 128 * 128
+            key = dg.describe_config(kind | (0 if fp8 else BF16) | BIAS, M, N, K, 1 if kind == 0 else 4, num_cus=256)
+            seen.add(re.search(r"_m(\d+n\d+)_", key).group(1))
+    want = {"256n256", "128n256", "128n192", "192n128", "128n128", "128n64", "64n128", "64n64", "32n64", "16n64", "16n32"}
+    assert want <= seen, want - seen
