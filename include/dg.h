@@ -320,7 +320,7 @@ dg_status dg_m_grouped_fp4_fp4_gemm_nt_masked(const void *A, const int32_t *sfa,
                                               int num_groups, void *stream);
 
 /*
- * The BF16 and FP8 (FP32-scale) forms with a fused epilogue:
+ * The BF16 and FP8 forms with a fused epilogue:
  *
  *     Z = A . B^T + bias,   D = activation(Z) + residual
  *
@@ -361,6 +361,18 @@ dg_status dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(const void *A, const floa
 dg_status dg_m_grouped_fp8_gemm_nt_masked_epilogue(const void *A, const float *sfa, const void *B, const float *sfb,
                                                    const int32_t *masked_m, const dg_epilogue *epilogue, void *D,
                                                    int M_max, int N, int K, int num_groups, void *stream);
+
+/* ... with packed UE8M0 scales (layouts of the *_ue8m0 entry points). */
+dg_status dg_fp8_gemm_nt_ue8m0_epilogue(const void *A, const int32_t *sfa, const void *B, const int32_t *sfb,
+                                        const dg_epilogue *epilogue, void *D, int M, int N, int K, void *stream);
+dg_status dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0_epilogue(const void *A, const int32_t *sfa, const void *B,
+                                                             const int32_t *sfb, const int32_t *m_indices,
+                                                             const dg_epilogue *epilogue, void *D, int M, int N, int K,
+                                                             int num_groups, void *stream);
+dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue(const void *A, const int32_t *sfa, const void *B,
+                                                         const int32_t *sfb, const int32_t *masked_m,
+                                                         const dg_epilogue *epilogue, void *D, int M_max, int N, int K,
+                                                         int num_groups, void *stream);
 
 /*
  * Backward pass of the fused epilogue.  With dD the gradient of D [M][N] and Z
@@ -453,7 +465,7 @@ dg_status dg_k_grouped_bf16_gemm_tn_contiguous(const void *A, const void *B, con
  * array without elements (T or rows 0) may be NULL.  Two
  * assignments never share a row in a pos that dg_moe_sort_* made; given one in
  * which they do, either may win.  dg_moe_sort_contiguous and _masked of more
- * than 2048 assignments use the stream's workspace.
+ * than 4096 assignments use the stream's workspace.
  */
 int64_t dg_moe_sorted_rows(int T, int topk, int num_experts);
 dg_status dg_moe_sort_contiguous(const int32_t *expert_ids, int32_t *pos, int32_t *m_indices, int32_t *ks,

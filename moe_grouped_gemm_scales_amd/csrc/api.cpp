@@ -930,6 +930,41 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_epilogue(const void* A, const float* s
     });
 }
 
+dg_status dg_fp8_gemm_nt_ue8m0_epilogue(const void* A, const int32_t* sfa, const void* B, const int32_t* sfb,
+                                        const dg_epilogue* epilogue, void* D, int M, int N, int K, void* stream) {
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : dense(A, sfa, B, sfb, nullptr, D, M, N, K, 1, stream, 0, 0, ep, args);
+    });
+}
+
+dg_status dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0_epilogue(const void* A, const int32_t* sfa, const void* B,
+                                                             const int32_t* sfb, const int32_t* m_indices,
+                                                             const dg_epilogue* epilogue, void* D, int M, int N, int K,
+                                                             int num_groups, void* stream) {
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s
+                          : contiguous(A, sfa, B, sfb, m_indices, nullptr, D, M, N, K, num_groups, 1, stream, 0, ep, args);
+    });
+}
+
+dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue(const void* A, const int32_t* sfa, const void* B,
+                                                         const int32_t* sfb, const int32_t* masked_m,
+                                                         const dg_epilogue* epilogue, void* D, int M_max, int N, int K,
+                                                         int num_groups, void* stream) {
+    return guarded([&]() -> dg_status {
+        Epilogue ep;
+        EpilogueArgs args;
+        dg_status s = read_epilogue(epilogue, &ep, &args);
+        return s != DG_OK ? s : masked(A, sfa, B, sfb, masked_m, nullptr, D, M_max, N, K, num_groups, 1, stream, ep, args);
+    });
+}
+
 // ---- BF16 products of the backward pass
 dg_status dg_bf16_gemm_nn(const void* A, const void* B, const float* C, void* D, int M, int N, int K, void* stream) {
     return guarded([&]() -> dg_status {

@@ -108,6 +108,9 @@ def _load():
                        ("dg_fp8_gemm_nt_epilogue", [vp] * 6 + [i32] * 3 + [vp]),
                        ("dg_m_grouped_fp8_gemm_nt_contiguous_epilogue", [vp] * 7 + [i32] * 4 + [vp]),
                        ("dg_m_grouped_fp8_gemm_nt_masked_epilogue", [vp] * 7 + [i32] * 4 + [vp]),
+                       ("dg_fp8_gemm_nt_ue8m0_epilogue", [vp] * 6 + [i32] * 3 + [vp]),
+                       ("dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0_epilogue", [vp] * 7 + [i32] * 4 + [vp]),
+                       ("dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue", [vp] * 7 + [i32] * 4 + [vp]),
                        ("dg_epilogue_backward", [vp, vp, i32, vp, vp, i32, i32, vp]),
                        ("dg_m_grouped_epilogue_backward_contiguous", [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp]),
                        ("dg_bf16_gemm_nn", [vp] * 4 + [i32] * 3 + [vp]),
@@ -954,15 +957,21 @@ def dg_m_grouped_bf16_gemm_nt_masked_epilogue(A, B, masked_m, D, bias=None, acti
     return D
 
 
+def _scale_type(sfa, K):
+    """(dtype, entries along K, packed UE8M0) of a call's scales: int32 words select UE8M0, as for the plain forms."""
+    ue8m0 = sfa.dtype is _I32
+    return (_I32, _cdiv(K, 512), True) if ue8m0 else (_F32, _cdiv(K, 128), False)
+
+
 def dg_fp8_gemm_nt_epilogue(A, sfa, B, sfb, D, bias=None, activation="none", residual=None, Z=None, stream=None):
-    """As dg_bf16_gemm_nt_epilogue with E4M3 operands and FP32 scales (layouts of dg_fp8_gemm_nt)."""
+    """As dg_bf16_gemm_nt_epilogue with E4M3 operands and FP32 or packed UE8M0 scales (layouts of dg_fp8_gemm_nt)."""
     M, K = A.shape
     N = B.shape[0]
-    kb, dev = _cdiv(K, 128), _on(A, "A")
+    (st, kb, ue8m0), dev = _scale_type(sfa, K), _on(A, "A")
     e = _epilogue(D, (N,), bias, activation, residual, Z, dev)
-    status = lib.dg_fp8_gemm_nt_epilogue(
-        _fp8_arg(A, "A", (M, K), dev), _arg(sfa, "sfa", _F32, (kb, M), dev), _fp8_arg(B, "B", (N, K), dev),
-        _arg(sfb, "sfb", _F32, (_cdiv(N, 128), kb), dev), e, _arg(D, "D", _BF, (M, N), dev), M, N, K,
+    status = (lib.dg_fp8_gemm_nt_ue8m0_epilogue if ue8m0 else lib.dg_fp8_gemm_nt_epilogue)(
+        _fp8_arg(A, "A", (M, K), dev), _arg(sfa, "sfa", st, (kb, M), dev), _fp8_arg(B, "B", (N, K), dev),
+        _arg(sfb, "sfb", st, (_cdiv(N, 128), kb), dev), e, _arg(D, "D", _BF, (M, N), dev), M, N, K,
         _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -974,11 +983,12 @@ def dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(A, sfa, B, sfb, m_indices, D, b
     """Contiguous M-grouped FP8 form (layouts of dg_m_grouped_fp8_gemm_nt_contiguous), bias [G,N]."""
     M, K = A.shape
     G, N = B.shape[0], B.shape[1]
-    kb, dev = _cdiv(K, 128), _on(A, "A")
+    (st, kb, ue8m0), dev = _scale_type(sfa, K), _on(A, "A")
     e = _epilogue(D, (G, N), bias, activation, residual, Z, dev)
-    status = lib.dg_m_grouped_fp8_gemm_nt_contiguous_epilogue(
-        _fp8_arg(A, "A", (M, K), dev), _arg(sfa, "sfa", _F32, (kb, M), dev), _fp8_arg(B, "B", (G, N, K), dev),
-        _arg(sfb, "sfb", _F32, (G, _cdiv(N, 128), kb), dev), _arg(m_indices, "m_indices", _I32, (M,), dev), e,
+    status = (lib.dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0_epilogue if ue8m0 else
+              lib.dg_m_grouped_fp8_gemm_nt_contiguous_epilogue)(
+        _fp8_arg(A, "A", (M, K), dev), _arg(sfa, "sfa", st, (kb, M), dev), _fp8_arg(B, "B", (G, N, K), dev),
+        _arg(sfb, "sfb", st, (G, _cdiv(N, 128), kb), dev), _arg(m_indices, "m_indices", _I32, (M,), dev), e,
         _arg(D, "D", _BF, (M, N), dev), M, N, K, G, _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -990,11 +1000,12 @@ def dg_m_grouped_fp8_gemm_nt_masked_epilogue(A, sfa, B, sfb, masked_m, D, bias=N
     """Masked M-grouped FP8 form (layouts of dg_m_grouped_fp8_gemm_nt_masked), bias [G,N]."""
     G, M_max, K = A.shape
     N = B.shape[1]
-    kb, dev = _cdiv(K, 128), _on(A, "A")
+    (st, kb, ue8m0), dev = _scale_type(sfa, K), _on(A, "A")
     e = _epilogue(D, (G, N), bias, activation, residual, Z, dev)
-    status = lib.dg_m_grouped_fp8_gemm_nt_masked_epilogue(
-        _fp8_arg(A, "A", (G, M_max, K), dev), _arg(sfa, "sfa", _F32, (G, kb, M_max), dev),
-        _fp8_arg(B, "B", (G, N, K), dev), _arg(sfb, "sfb", _F32, (G, _cdiv(N, 128), kb), dev),
+    status = (lib.dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue if ue8m0 else
+              lib.dg_m_grouped_fp8_gemm_nt_masked_epilogue)(
+        _fp8_arg(A, "A", (G, M_max, K), dev), _arg(sfa, "sfa", st, (G, kb, M_max), dev),
+        _fp8_arg(B, "B", (G, N, K), dev), _arg(sfb, "sfb", st, (G, _cdiv(N, 128), kb), dev),
         _arg(masked_m, "masked_m", _I32, (G,), dev), e, _arg(D, "D", _BF, (G, M_max, N), dev), M_max, N, K, G,
         _raw_stream(stream, dev))
     if status:

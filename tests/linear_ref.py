@@ -44,11 +44,14 @@ def values(p):
     a, b = of(p.A), of(p.B)
     K = a.shape[-1]
     if not p.bf16:
-        sfa = p.sfa.double().numpy()
-        sfa = np.moveaxis(sfa, -2, -1)                           # [.., rows, K/128]
-        a = a * np.repeat(sfa, 128, -1)
-        sfb = np.repeat(np.repeat(p.sfb.double().numpy(), 128, -2)[..., :b.shape[-2], :], 128, -1)
-        b = b * sfb
+        sfa, sfb = np.moveaxis(p.sfa.numpy(), -2, -1), p.sfb.numpy()        # [.., rows, K/128], [.., N/128, K/128]
+        if p.ue8m0:                                                         # four exponents a word
+            def unpack(w):
+                e = (w.view(np.uint32)[..., None] >> np.array([0, 8, 16, 24], np.uint32)) & 255
+                return np.ldexp(1.0, e.astype(np.int64) - 127).reshape(*w.shape[:-1], -1)[..., :K // 128]
+            sfa, sfb = unpack(np.ascontiguousarray(sfa)), unpack(sfb)
+        a = a * np.repeat(sfa.astype(np.float64), 128, -1)
+        b = b * np.repeat(np.repeat(sfb.astype(np.float64), 128, -2)[..., :b.shape[-2], :], 128, -1)
     return a.reshape(-1, K), b.reshape(-1, *b.shape[-2:])
 
 

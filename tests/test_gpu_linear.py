@@ -96,6 +96,16 @@ def test_fp8_dense(M, N, K, act):
     _check(gen.make_dense(M, N, K, seed=M + N), True, act, True, True, 8, bias_dtype=torch.bfloat16, what="fp8")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (100, 302, 1152), (300, 515, 640)])
+def test_fp8_ue8m0(M, N, K):
+    """Packed power-of-two scales: dense and both grouped forms, every part of the epilogue."""
+    _check(gen.make_dense(M, N, K, seed=M + N, ue8m0=True), True, "silu", True, True, 8, what="ue8m0 dense")
+    p = gen.make_contiguous([128, 0, M], N, K, seed=5, pad_rows=128, ue8m0=True)
+    _check(p, True, "gelu", True, True, 9, what="ue8m0 contiguous")
+    p = gen.make_masked(3, 200, N, K, seed=6, masked_m=[200, 0, 77], ue8m0=True)
+    _check(p, True, "relu", False, True, 10, what="ue8m0 masked")
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("N", [256, 333, 1024])
 def test_grouped(bf16, N):
