@@ -21,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 KERNEL = os.path.join(CSRC, "kernels", "fp8_gemm.hip")
 INC = os.path.join(CSRC, "kernel_source.inc")
 LIB = os.path.join(PKG, "libdg.so")
+PYCHECK = os.path.join(PKG, "_pycheck.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["api.cpp", "jit.cpp", "heuristics.cpp"]
@@ -71,6 +72,24 @@ def build_library(verbose: bool = False) -> str:
     return LIB
 
 
+def build_pycheck(verbose: bool = False) -> str:
+    """The binding's tensor check (csrc/pycheck.cpp), a Python extension against torch's headers."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for path in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "pycheck.cpp"), "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-lc10", "-ltorch_cpu", "-ltorch_python", "-o", PYCHECK + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(PYCHECK + ".tmp", PYCHECK)
+    return PYCHECK
+
+
 # kind, rows, N, K, groups, has_c: the five benchmark workloads (plus C variant) and the K-grouped one
 STANDARD_SHAPES = [
     (0, 64, 2112, 7168, 1, 0),
@@ -108,5 +127,6 @@ def precompile(shapes=STANDARD_SHAPES, num_cus: int = 256) -> None:
 
 if __name__ == "__main__":
     build_library(verbose=True)
+    build_pycheck(verbose=True)
     if "--precompile" in sys.argv:
         precompile()

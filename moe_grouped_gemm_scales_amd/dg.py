@@ -35,6 +35,18 @@ class DGError(RuntimeError):
         self.status = status
 
 
+def _load_pycheck():
+    """csrc/pycheck.cpp, loaded by path (it needs torch, imported above)."""
+    import importlib.util
+    path = os.path.join(_HERE, "_pycheck.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run `python moe_grouped_gemm_scales_amd/build.py`")
+    spec = importlib.util.spec_from_file_location("_pycheck", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python moe_grouped_gemm_scales_amd/build.py`")
@@ -708,10 +720,12 @@ m_grouped_fp4_fp4_gemm_nt_masked = dg_m_grouped_fp4_fp4_gemm_nt_masked
 
 
 # ---------------------------------------------------------------- tokens to experts and back
-# The calls of a decode step are a few microseconds of GPU work each, so the checks of these functions are
-# kept to one short pass a tensor: _arg() returns the address, and only a tensor that fails goes on to
-# _refuse(), which says why.
+# The calls of a decode step are a few microseconds of GPU work each, so the tensors of these functions are
+# checked in C (csrc/pycheck.cpp: _arg gives the address of a contiguous tensor of this type and shape on this
+# device, _opt takes None too); a tensor that fails comes to _refuse(), which says why.
 def _refuse(t, name: str, dtype, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -720,15 +734,9 @@ def _refuse(t, name: str, dtype, shape):
     raise ValueError(f"{name} is not on the other tensors' device")
 
 
-def _arg(t, name: str, dtype, shape, dev: int) -> int:
-    """Address of a contiguous tensor of this type and shape on device `dev`."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, name, dtype, shape)
-    return t.data_ptr()
-
-
-def _opt(t, name: str, dtype, shape, dev: int):
-    return None if t is None else _arg(t, name, dtype, shape, dev)
+_pycheck = _load_pycheck()
+_pycheck.refuse_with(_refuse)
+_arg, _opt = _pycheck.arg, _pycheck.opt
 
 
 def _on(t, name: str) -> int:
