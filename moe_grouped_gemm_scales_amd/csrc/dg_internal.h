@@ -156,6 +156,10 @@ dg_status scratch_address(void** out);
 // call can be captured in a graph)
 dg_status clear_words(uint32_t* p, int n, void* stream);
 
+// Bytes a pass reads and writes from which its kernels carry the non-temporal hint:
+// half the Infinity Cache (measured both sides where it is used)
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
 // The stream's scratch buffer on the current device, at least `bytes` large (api.cpp; the
 // split-K partials' buffer: work on one stream runs in order, so its calls share it).
 dg_status stream_scratch(void* stream, size_t bytes, float** out);

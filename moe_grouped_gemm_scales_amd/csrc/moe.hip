@@ -44,6 +44,25 @@ __device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(floa
 __device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
 __device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
 
+// 16 bytes a lane.  STREAM: with the non-temporal hint, for calls that read and
+// write more than the caches keep until the next pass (kStreamBytes).  Measured
+// (two sets of buffers in turn, top 4 of 32, width 7168; plain against streamed,
+// us): combine of 1024 tokens (88 MB) 14.4 / 15.4, 2048 (176 MB) 33.6 / 29.7, 8192
+// 132 / 118.5; its gradient 512 (66 MB) 21.1 / 28.2, 1024 (132 MB) 39.9 / 39.4, 4096
+// 118.5 / 111.9; dispatch in BF16 1024 (73 MB) 17.7 / 19.3, 2048 (147 MB) 34.0 / 29.2,
+// in FP8 2048 (88 MB) 21.4 / 20.9, 4096 (176 MB) 44.3 / 36.3.  (The FP8 dispatch streams its stores only: with
+// its loads too it gives half of that back.)
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load16(const void* p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+    else return *static_cast<const u32x4*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, u32x4 v) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x4*>(p));
+    else *static_cast<u32x4*>(p) = v;
+}
+
 // ---------------------------------------------------------------- sort
 // Block b counts the experts of its chunk of the ids.
 __global__ void __launch_bounds__(kSortThreads) dg_moe_count_kernel(const int* __restrict__ ids, int n, int G,
@@ -286,7 +305,7 @@ struct DispatchArgs {
 
 // BF16.  VEC: rows are 16-byte aligned (H % 8 == 0), a lane moves two groups of
 // 8 elements; otherwise 16 single elements, 64 apart.
-template <bool VEC>
+template <bool VEC, bool STREAM>
 __global__ void __launch_bounds__(256)
 dg_moe_dispatch_bf16_kernel(const DispatchArgs a) {
     const u16* __restrict__ X = a.X;
@@ -311,8 +330,8 @@ dg_moe_dispatch_bf16_kernel(const DispatchArgs a) {
                 for (int i = 0; i < kAhead; ++i) {
                     if (r[i] < 0) continue;
                     u16* dst = out + (u64)r[i] * H;
-                    if (ca < H) *(u32x4*)(dst + ca) = va;
-                    if (cb < H) *(u32x4*)(dst + cb) = vb;
+                    if (ca < H) store16<STREAM>(dst + ca, va);
+                    if (cb < H) store16<STREAM>(dst + cb, vb);
                 }
             }
         } else {
@@ -354,7 +373,7 @@ dg_moe_dispatch_bf16_kernel(const DispatchArgs a) {
 // integers the magnitudes order with infinities and NaN on top, so a block that
 // holds one gets a scale that says so.
 // UE8M0: scales are powers of two, four K blocks to a word (sf int32 [H/512][rows]).
-template <bool UE8M0>
+template <bool UE8M0, bool STREAM>
 __global__ void __launch_bounds__(256)
 dg_moe_dispatch_fp8_kernel(const DispatchArgs args) {
     const u16* __restrict__ X = args.X;
@@ -444,7 +463,7 @@ dg_moe_dispatch_fp8_kernel(const DispatchArgs args) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 if (r[i] < 0) continue;
-                if (c < H) *(u32x4*)(out + (u64)r[i] * H + c) = q;
+                if (c < H) store16<STREAM>(out + (u64)r[i] * H + c, q);
                 if (scale_lane) sf[sf_at(r[i])] = entry;
             }
             j0 += kAhead;
@@ -474,7 +493,7 @@ struct CombineArgs {
     u16* Y;
     int T, k, rows, N, pieces;
 };
-template <bool VEC>
+template <bool VEC, bool STREAM>
 __global__ void __launch_bounds__(256) dg_moe_combine_kernel(const CombineArgs a) {
     const u16* __restrict__ in = a.in;
     const int* __restrict__ pos = a.pos;
@@ -493,7 +512,7 @@ __global__ void __launch_bounds__(256) dg_moe_combine_kernel(const CombineArgs a
     auto load = [&](const u16* p) {            // eight BF16, two a word
         u32x4 w = {0u, 0u, 0u, 0u};
         if constexpr (VEC) {
-            if (in_range) w = *(const u32x4*)(p + col(0));
+            if (in_range) w = load16<STREAM>(p + col(0));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -528,8 +547,8 @@ __global__ void __launch_bounds__(256) dg_moe_combine_kernel(const CombineArgs a
     u16* dst = Y + (u64)t * N;
     if constexpr (VEC) {
         if (in_range)
-            *(u32x4*)(dst + col(0)) = u32x4{to_bf16x2(acc[0], acc[1]), to_bf16x2(acc[2], acc[3]),
-                                            to_bf16x2(acc[4], acc[5]), to_bf16x2(acc[6], acc[7])};
+            store16<STREAM>(dst + col(0), u32x4{to_bf16x2(acc[0], acc[1]), to_bf16x2(acc[2], acc[3]),
+                                                to_bf16x2(acc[4], acc[5]), to_bf16x2(acc[6], acc[7])});
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -552,7 +571,7 @@ struct CombineBackwardArgs {
     float* d_weights;
     int T, k, rows, N;
 };
-template <bool VEC>
+template <bool VEC, bool STREAM>
 __global__ void __launch_bounds__(256) dg_moe_combine_backward_kernel(const CombineBackwardArgs a) {
     const u16* __restrict__ dY = a.dY;
     const u16* __restrict__ in = a.in;
@@ -569,7 +588,7 @@ __global__ void __launch_bounds__(256) dg_moe_combine_backward_kernel(const Comb
     auto load = [&](const u16* p, int c0, float (&v)[8]) {
         if constexpr (VEC) {
             u32x4 w = {0u, 0u, 0u, 0u};
-            if (col(c0, 0) < N) w = *(const u32x4*)(p + col(c0, 0));
+            if (col(c0, 0) < N) w = load16<STREAM>(p + col(c0, 0));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[2 * i] = bf16_lo(w[i]);
@@ -583,8 +602,8 @@ __global__ void __launch_bounds__(256) dg_moe_combine_backward_kernel(const Comb
     auto store = [&](u16* p, int c0, const float (&v)[8]) {
         if constexpr (VEC) {
             if (col(c0, 0) < N)
-                *(u32x4*)(p + col(c0, 0)) = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
-                                                  to_bf16x2(v[6], v[7])};
+                store16<STREAM>(p + col(c0, 0), u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]),
+                                                      to_bf16x2(v[4], v[5]), to_bf16x2(v[6], v[7])});
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -756,7 +775,9 @@ dg_status dg_moe_dispatch_bf16(const void* X, const int32_t* pos, const int32_t*
         if (units == 0) return DG_OK;
         const unsigned grid = grid_of(units);
         if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_bf16: too many tokens for one launch");
-        hipLaunchKernelGGL(H % 8 == 0 ? dg_moe_dispatch_bf16_kernel<true> : dg_moe_dispatch_bf16_kernel<false>, dim3(grid),
+        const bool stream_it = 2 * (int64_t)T * (topk + (int64_t)1) * H >= kStreamBytes;
+        hipLaunchKernelGGL((H % 8 ? dg_moe_dispatch_bf16_kernel<false, false>
+                            : stream_it ? dg_moe_dispatch_bf16_kernel<true, true> : dg_moe_dispatch_bf16_kernel<true, false>), dim3(grid),
                            dim3(256), 0, static_cast<hipStream_t>(stream),
                            DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, nullptr, T, topk, rows, rows, H, pieces});
         return launched("moe_dispatch_bf16");
@@ -779,7 +800,9 @@ dg_status dg_moe_dispatch_fp8(const void* X, const int32_t* pos, const int32_t* 
         if (units == 0 || rows == 0) return DG_OK;
         const unsigned grid = grid_of(units);
         if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: too many tokens for one launch");
-        hipLaunchKernelGGL(ue8m0 ? dg_moe_dispatch_fp8_kernel<true> : dg_moe_dispatch_fp8_kernel<false>, dim3(grid),
+        const bool stream_it = (int64_t)T * (topk + (int64_t)2) * H >= kStreamBytes;
+        hipLaunchKernelGGL((ue8m0 ? (stream_it ? dg_moe_dispatch_fp8_kernel<true, true> : dg_moe_dispatch_fp8_kernel<true, false>)
+                                  : (stream_it ? dg_moe_dispatch_fp8_kernel<false, true> : dg_moe_dispatch_fp8_kernel<false, false>)), dim3(grid),
                            dim3(256), 0, static_cast<hipStream_t>(stream),
                            DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, static_cast<u32*>(sf), T, topk, rows,
                                         group_rows, H, pieces});
@@ -798,7 +821,9 @@ dg_status dg_moe_combine(const void* rows_in, const int32_t* pos, const float* w
         if (T == 0) return DG_OK;
         const unsigned grid = grid_of((int64_t)T * pieces);
         if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_combine: too many tokens for one launch");
-        hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_kernel<true> : dg_moe_combine_kernel<false>, dim3(grid), dim3(256), 0,
+        const bool stream_it = 2 * (int64_t)T * (topk + (int64_t)(residual ? 2 : 1)) * N >= kStreamBytes;
+        hipLaunchKernelGGL((N % 8 ? dg_moe_combine_kernel<false, false>
+                            : stream_it ? dg_moe_combine_kernel<true, true> : dg_moe_combine_kernel<true, false>), dim3(grid), dim3(256), 0,
                            static_cast<hipStream_t>(stream),
                            CombineArgs{static_cast<const u16*>(rows_in), pos, weights, static_cast<const u16*>(residual),
                                        static_cast<u16*>(Y), T, topk, rows, N, pieces});
@@ -820,7 +845,9 @@ dg_status dg_moe_combine_backward(const void* dY, const void* rows_in, const int
         const int64_t blocks = (int64_t)T + (m_indices ? pad_blocks(rows) : 0);
         if (blocks == 0) return DG_OK;
         if (blocks > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_combine_backward: too many tokens for one launch");
-        hipLaunchKernelGGL(N % 8 == 0 ? dg_moe_combine_backward_kernel<true> : dg_moe_combine_backward_kernel<false>,
+        const bool stream_it = 2 * (int64_t)T * (topk * (int64_t)(d_weights ? 2 : 1) + 1) * N >= kStreamBytes;
+        hipLaunchKernelGGL((N % 8 ? dg_moe_combine_backward_kernel<false, false>
+                            : stream_it ? dg_moe_combine_backward_kernel<true, true> : dg_moe_combine_backward_kernel<true, false>),
                            dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
                            CombineBackwardArgs{static_cast<const u16*>(dY), static_cast<const u16*>(rows_in), pos, weights,
                                                m_indices, static_cast<u16*>(d_rows), d_weights, T, topk, rows, N});
