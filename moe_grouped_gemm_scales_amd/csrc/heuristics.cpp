@@ -306,7 +306,7 @@ struct Structure {
 const Structure kStructures[] = {
     {256, 256, 4, 2, 2, 6, 0, 1.55, 1.85}, {128, 256, 2, 4, 3, 0, 0, 0.89, 1.00},
     {128, 192, 2, 4, 3, 0, 0, 0.76, 0.83}, {192, 128, 4, 2, 3, 0, 0, 0.72, 0.83},
-    {128, 128, 4, 2, 4, 0, 0, 0.58, 0.62}, {128, 128, 2, 2, 2, 6, 1, 0.48, 0.52},
+    {128, 128, 4, 2, 4, 0, 0, 0.58, 0.62}, {128, 128, 2, 2, 2, 6, 1, 0.50, 0.52},
     {128, 64, 4, 2, 4, 0, 0, 0.39, 0.39},  {64, 128, 2, 4, 4, 0, 0, 0.40, 0.40},
     {64, 64, 2, 2, 4, 0, 0, 0.23, 0.23},   {32, 64, 1, 4, 4, 0, 0, 0.22, 0.22},
     {16, 64, 1, 4, 4, 0, 0, 0.20, 0.20},   {16, 32, 1, 2, 6, 0, 0, 0.14, 0.14},
