@@ -34,17 +34,19 @@
  *     (group indices, masks) on the host.
  *   - The library owns its compiled-kernel cache and a per-stream device
  *     workspace (split-K partials and arrival counters; the K-contiguous copies
- *     of K-outermost operands), created on first use (or by dg_init) and kept
- *     until process exit.  The first call for a new shape compiles a kernel
- *     (hipRTC) and may allocate; later calls with the same shape neither
- *     compile nor allocate.  A workspace a larger call outgrows is replaced by
+ *     of K-outermost operands, a sort's counts, a bias gradient's partial sums),
+ *     created on first use (or by dg_init) and kept until process exit.  The
+ *     first call for a new shape compiles a kernel (hipRTC) and may allocate;
+ *     later calls with the same shape neither compile nor allocate.  Host
+ *     threads may share a stream.  A workspace a larger call outgrows is replaced by
  *     one at least twice its size and is never freed, so a HIP graph that
  *     captured calls keeps valid addresses; replay such a graph on the stream
  *     it was captured on (calls on one stream share that stream's workspace).
  *     Two graphs that captured calls on the same stream share its workspace
  *     too, so they must not be replayed concurrently (on other streams) when
- *     their shapes use split-K (few rows, long K) or a K-contiguous rewrite:
- *     that races on the partial sums and arrival counters and is unsupported.
+ *     their calls use it: split-K (few rows, long K), a K-contiguous rewrite, a
+ *     sort of more than 4096 assignments, a bias gradient.  That races on what
+ *     they keep there and is unsupported.
  *     A call that compiles or allocates cannot run under stream capture: make
  *     the first call of each shape on each stream eagerly, then capture.
  *   - Work queued on different streams must not share output buffers.

@@ -56,7 +56,7 @@ struct Workspace {
     size_t partial_bytes = 0;
     uint32_t* counters = nullptr;
     size_t counter_bytes = 0;
-    uint8_t* kmajor = nullptr;       // K-grouped operands rewritten K-contiguous
+    uint8_t* kmajor = nullptr;       // operands rewritten K-contiguous, and StreamScratch
     size_t kmajor_bytes = 0;
     // Buffers a larger call outgrew.  They stay allocated until the process ends:
     // a HIP graph captured earlier still holds their addresses.
@@ -431,15 +431,16 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
 
 }  // namespace
 
-dg_status stream_scratch(void* stream, size_t bytes, float** out) {
-    std::lock_guard<std::mutex> lock(g_mu);
+dg_status stream_scratch(void* stream, size_t bytes, StreamScratch* out) {
+    out->held = std::unique_lock<std::mutex>(g_mu);
     DeviceState* st = nullptr;
     int dev = 0;
     dg_status s = device_state(&st, &dev);
     if (s != DG_OK) return s;
-    Workspace* w = nullptr;
-    s = ensure_workspace(*st, static_cast<hipStream_t>(stream), bytes, 0, &w);
-    if (s == DG_OK) *out = w->partials;
+    uint8_t* p = nullptr;
+    // (8 MiB at least: most calls' needs in one allocation)
+    s = ensure_kmajor(*st, static_cast<hipStream_t>(stream), std::max(bytes, size_t(8) << 20), &p);
+    out->p = p;
     return s;
 }
 

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <exception>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -160,9 +161,16 @@ dg_status clear_words(uint32_t* p, int n, void* stream);
 // half the Infinity Cache (measured both sides where it is used)
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
-// The stream's scratch buffer on the current device, at least `bytes` large (api.cpp; the
-// split-K partials' buffer: work on one stream runs in order, so its calls share it).
-dg_status stream_scratch(void* stream, size_t bytes, float** out);
+// What one kernel of a call hands to the next through the stream's workspace (api.cpp).  It
+// holds the library's lock until it goes out of scope, after the last of those kernels has
+// been launched: another host thread's call on the stream queued between them would write its
+// own there.  (The buffer is that of the K-contiguous copies, which the lock guards too; split-K
+// partials, which a repeated call uses without the lock, have their own.)
+struct StreamScratch {
+    std::unique_lock<std::mutex> held;
+    void* p = nullptr;
+};
+dg_status stream_scratch(void* stream, size_t bytes, StreamScratch* out);
 
 // Errors (api.cpp).
 dg_status set_error(dg_status s, const std::string& msg);

@@ -296,9 +296,11 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
     const int chunk = wide >= 1024 ? 64 : kStep;
     const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
     float* partial = nullptr;
+    StreamScratch scratch;               // held until both kernels are launched
     if (dbias && chunks > 0) {
-        dg_status s = stream_scratch(stream_ptr, (size_t)chunks * (size_t)N * sizeof(float), &partial);
+        dg_status s = stream_scratch(stream_ptr, (size_t)chunks * (size_t)N * sizeof(float), &scratch);
         if (s != DG_OK) return s;
+        partial = static_cast<float*>(scratch.p);
     }
     if (chunks > 0 && (dZ || dbias)) {
         const dim3 grid(chunks, (N + 511) / 512);

@@ -691,14 +691,14 @@ dg_status sort(const int32_t* ids, int32_t* pos, int32_t* m_indices, int32_t* gr
     // against 1.7 + 4.7 us and a launch between).
     int chunk = kSortStep, blocks = 1;
     u32* hist = nullptr;
+    StreamScratch scratch;               // held until both kernels are launched
     if (n > chunk) {
         const int steps = (n + kSortThreads - 1) / kSortThreads;
         chunk = (steps + kSortBlocks - 1) / kSortBlocks * kSortThreads;
         blocks = (n + chunk - 1) / chunk;
-        float* ws = nullptr;
-        dg_status s = stream_scratch(stream_ptr, (size_t)blocks * G * sizeof(u32), &ws);
+        dg_status s = stream_scratch(stream_ptr, (size_t)blocks * G * sizeof(u32), &scratch);
         if (s != DG_OK) return s;
-        hist = reinterpret_cast<u32*>(ws);
+        hist = static_cast<u32*>(scratch.p);
         hipLaunchKernelGGL(dg_moe_count_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n, G, chunk, hist);
         s = launched("moe_sort (count)");
         if (s != DG_OK) return s;
