@@ -2,28 +2,10 @@
 // activation's gradient with the bias gradient in the same pass, and the
 // K-contiguous rewrite of BF16 operands for the NN and TN products.  The
 // operations are specified in include/dg.h.
-#include <hip/hip_runtime.h>
-
-#include <climits>
-#include <cstdint>
-
-#include "dg_internal.h"
+#include "row_kernels.h"
 
 namespace dg {
 namespace {
-
-typedef unsigned short u16;
-typedef unsigned int u32;
-typedef unsigned long long u64;
-typedef u32 u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kPadding = -1;           // m_indices of a padding row inside a segment
-
-__device__ __forceinline__ float bf16_lo(u32 w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
-__device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
-__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
 
 // ---------------------------------------------------------------- K-contiguous rewrite
 // X [rows_k][cols] -> Xt [cols][pitch], columns [rows_k, k_end) of Xt zero.  One
@@ -31,9 +13,17 @@ __device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf
 // stores along K.  A row of the LDS block is 33 words, so the gather of a
 // column (four lanes 16 rows apart, 16 columns a wave) touches 32 distinct
 // banks.  K blocks fastest, as in the FP8 rewrite.
-__global__ void __launch_bounds__(256)
-dg_transpose_bf16_kernel(const u16* __restrict__ X, u16* __restrict__ Xt, int rows_k, int cols, int k_blocks,
-                         long long pitch) {
+struct TransposeArgs {
+    const u16* X;
+    u16* Xt;
+    int rows_k, cols, k_blocks;
+    long long pitch;
+};
+__global__ void __launch_bounds__(256) dg_transpose_bf16_kernel(const TransposeArgs a) {
+    const u16* __restrict__ X = a.X;
+    u16* __restrict__ Xt = a.Xt;
+    const int rows_k = a.rows_k, cols = a.cols, k_blocks = a.k_blocks;
+    const long long pitch = a.pitch;
     __shared__ __attribute__((aligned(4))) u16 tile[64][66];
     const int tid = threadIdx.x;
     const int k0 = (int)(blockIdx.x % (u32)k_blocks) * 64, c0 = (int)(blockIdx.x / (u32)k_blocks) * 64;
@@ -262,24 +252,16 @@ __global__ void __launch_bounds__(64 * kSumWaves) dg_bias_sum_kernel(const BiasS
     }
 }
 
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-dg_status launched(const char* what) {
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? DG_OK : set_error(DG_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
 template <int ACT>
-void launch_backward(dim3 grid, hipStream_t stream, const BackwardArgs& a) {
+dg_status launch_backward(dim3 grid, void* stream, const BackwardArgs& a) {
     const bool stream_it = int64_t(6) * a.rows * a.N >= kStreamBytes;
-    hipLaunchKernelGGL((a.N % 8 ? dg_epilogue_backward_kernel<ACT, false, false>
-                        : stream_it ? dg_epilogue_backward_kernel<ACT, true, true>
-                                    : dg_epilogue_backward_kernel<ACT, true, false>),
-                       grid, dim3(256), 0, stream, a);
+    auto* kernel = a.N % 8 ? dg_epilogue_backward_kernel<ACT, false, false>
+                 : stream_it ? dg_epilogue_backward_kernel<ACT, true, true> : dg_epilogue_backward_kernel<ACT, true, false>;
+    return launch_rows("epilogue_backward", kernel, grid, 256, stream, a);
 }
 
 dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_t* m_indices, void* dZ, float* dbias,
-                            int rows, int N, int G, void* stream_ptr) {
+                            int rows, int N, int G, void* stream) {
     if (rows != 0 && (!dD || (act != DG_ACT_NONE && !Z)))
         return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: dD and (with an activation) Z must be non-NULL");
     if (act < DG_ACT_NONE || act > DG_ACT_GELU_TANH)
@@ -288,17 +270,16 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
         return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: sizes must be positive (M may be 0)");
     if (!aligned(dD, 16) || !aligned(Z, 16) || !aligned(dZ, 16) || !aligned(dbias, 4) || !aligned(m_indices, 4))
         return set_error(DG_ERR_ALIGNMENT, "epilogue_backward: dD, Z and dZ must be 16-byte, the rest 4-byte aligned");
-    if (G > 65535 || N > 65535 * 512)
-        return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many groups or columns for one launch");
-    const hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     // 64 rows a workgroup where that still gives four to each compute unit, else 16
     const int64_t wide = ((int64_t)rows + 63) / 64 * ((N + 511) / 512);
     const int chunk = wide >= 1024 ? 64 : kStep;
     const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
+    if (G > 65535 || N > 65535 * 512 || !fits_launch(chunks) || !fits_launch((N + 63) / 64, 64 * kSumWaves))
+        return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many rows, groups or columns for one launch");
     float* partial = nullptr;
     StreamScratch scratch;               // held until both kernels are launched
     if (dbias && chunks > 0) {
-        dg_status s = stream_scratch(stream_ptr, (size_t)chunks * (size_t)N * sizeof(float), &scratch);
+        dg_status s = stream_scratch(stream, (size_t)chunks * (size_t)N * sizeof(float), &scratch);
         if (s != DG_OK) return s;
         partial = static_cast<float*>(scratch.p);
     }
@@ -307,17 +288,13 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
         auto* f = act == DG_ACT_RELU ? launch_backward<DG_ACT_RELU> : act == DG_ACT_SILU ? launch_backward<DG_ACT_SILU>
                 : act == DG_ACT_GELU ? launch_backward<DG_ACT_GELU>
                 : act == DG_ACT_GELU_TANH ? launch_backward<DG_ACT_GELU_TANH> : launch_backward<DG_ACT_NONE>;
-        f(grid, stream, BackwardArgs{static_cast<const u16*>(dD), static_cast<const u16*>(Z), m_indices,
-                                     static_cast<u16*>(dZ), partial, rows, N, G, chunk});
-        dg_status s = launched("epilogue_backward");
+        dg_status s = f(grid, stream, BackwardArgs{static_cast<const u16*>(dD), static_cast<const u16*>(Z), m_indices,
+                                                   static_cast<u16*>(dZ), partial, rows, N, G, chunk});
         if (s != DG_OK) return s;
     }
-    if (dbias) {
-        hipLaunchKernelGGL(dg_bias_sum_kernel, dim3((N + 63) / 64, G), dim3(64 * kSumWaves), 0, stream,
-                           BiasSumArgs{partial, m_indices, dbias, chunks, chunk, N});
-        return launched("epilogue_backward (bias)");
-    }
-    return DG_OK;
+    if (!dbias) return DG_OK;
+    return launch_rows("epilogue_backward (bias)", dg_bias_sum_kernel, dim3((N + 63) / 64, G), 64 * kSumWaves, stream,
+                       BiasSumArgs{partial, m_indices, dbias, chunks, chunk, N});
 }
 
 }  // namespace
@@ -326,13 +303,11 @@ dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int co
                          void* stream) {
     const int k_blocks = k_end / 64;
     const uint64_t blocks = (uint64_t)k_blocks * (uint64_t)((cols + 63) / 64);
-    if (blocks >= (1ull << 31) || groups > 65535)
+    if (!fits_launch((int64_t)blocks) || groups > 65535)
         return set_error(DG_ERR_UNSUPPORTED, "operand too large for the K-contiguous rewrite");
     if (blocks == 0) return DG_OK;
-    hipLaunchKernelGGL(dg_transpose_bf16_kernel, dim3((unsigned)blocks, 1, (unsigned)groups), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), static_cast<const u16*>(x), static_cast<u16*>(xt), rows_k, cols,
-                       k_blocks, (long long)pitch);
-    return launched("K-contiguous rewrite");
+    return launch_rows("K-contiguous rewrite", dg_transpose_bf16_kernel, dim3((unsigned)blocks, 1, (unsigned)groups), 256, stream,
+                       TransposeArgs{static_cast<const u16*>(x), static_cast<u16*>(xt), rows_k, cols, k_blocks, (long long)pitch});
 }
 
 }  // namespace dg

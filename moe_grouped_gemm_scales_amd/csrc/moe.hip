@@ -13,21 +13,12 @@
 // Work is cut by token, not by row: a token's hidden state is then read (and
 // quantised) once for its k copies, and a token's k rows meet in one wave's
 // registers, where the sum over j has a fixed order.
-#include <hip/hip_runtime.h>
-
 #include <climits>
-#include <cstdint>
 
-#include "dg_internal.h"
+#include "row_kernels.h"
 
 namespace dg {
 namespace {
-
-typedef unsigned char u8;
-typedef unsigned short u16;
-typedef unsigned int u32;
-typedef unsigned long long u64;
-typedef u32 u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAlign = 128;            // rows an expert's segment starts on a multiple of
 constexpr int kMaxExperts = 1024;      // the sort's per-wave counters live in LDS
@@ -36,13 +27,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortRounds = 4;
 constexpr int kSortStep = kSortRounds * kSortThreads;
 constexpr int kSortBlocks = 256;       // at most, so that one pass over their counts stays short
-constexpr int kPadding = -1;           // m_indices of a padding row inside a segment
 constexpr int kUnused = -2;            // ... of a row past the last segment
-
-__device__ __forceinline__ float bf16_lo(u32 w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
-__device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
-__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
 
 // 16 bytes a lane.  STREAM: with the non-temporal hint, for calls that read and
 // write more than the caches keep until the next pass (kStreamBytes).  Measured
@@ -65,8 +50,15 @@ __device__ __forceinline__ void store16(void* p, u32x4 v) {
 
 // ---------------------------------------------------------------- sort
 // Block b counts the experts of its chunk of the ids.
-__global__ void __launch_bounds__(kSortThreads) dg_moe_count_kernel(const int* __restrict__ ids, int n, int G,
-                                                                    int chunk, u32* __restrict__ hist) {
+struct CountArgs {
+    const int* ids;
+    u32* hist;
+    int n, G, chunk;
+};
+__global__ void __launch_bounds__(kSortThreads) dg_moe_count_kernel(const CountArgs a) {
+    const int* __restrict__ ids = a.ids;
+    u32* __restrict__ hist = a.hist;
+    const int n = a.n, G = a.G, chunk = a.chunk;
     __shared__ u32 h[kMaxExperts];
     for (int g = threadIdx.x; g < G; g += kSortThreads) h[g] = 0u;
     __syncthreads();
@@ -245,7 +237,7 @@ dg_moe_place_kernel(const SortArgs a) {
     // the last one that starts at or before it (empty segments start where the
     // next one does, and the last of equals is the one that holds rows)
     __syncthreads();
-    const int share = (rows + blocks - 1) / blocks;
+    const int share = rows / blocks + 1;
     const int r0 = b * share < rows ? b * share : rows;
     const int r1 = rows - r0 < share ? rows : r0 + share;
     for (int r = r0 + tid; r < r1; r += kSortThreads) {
@@ -273,7 +265,7 @@ __device__ __forceinline__ void for_padding_rows(const int* __restrict__ m_indic
         fill(r0 + at);
     }
 }
-__host__ __device__ constexpr int pad_blocks(int rows) { return (rows + kPadRows - 1) / kPadRows; }
+__host__ __device__ constexpr int pad_blocks(int rows) { return rows / kPadRows + (rows % kPadRows != 0); }
 
 // Rows of assignments j0 .. j0 + 7 of a token, -1 where there is none: eight
 // independent scalar loads.  (A load in front of each store made the decode
@@ -662,13 +654,6 @@ __global__ void __launch_bounds__(256) dg_moe_combine_backward_kernel(const Comb
 }
 
 // ---------------------------------------------------------------- host side
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-dg_status launched(const char* what) {
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? DG_OK : set_error(DG_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
 dg_status check_sort(const void* ids, const void* pos, const void* groups, int T, int topk, int G) {
     // an array of no elements may be NULL (so it is for torch's empty tensors)
     if ((T != 0 && (!ids || !pos)) || !groups) return set_error(DG_ERR_INVALID_ARG, "moe_sort: NULL pointer");
@@ -681,8 +666,7 @@ dg_status check_sort(const void* ids, const void* pos, const void* groups, int T
 }
 
 dg_status sort(const int32_t* ids, int32_t* pos, int32_t* m_indices, int32_t* group_rows, int T, int topk, int G,
-               int masked_rows, int rows, void* stream_ptr) {
-    const hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+               int masked_rows, int rows, void* stream) {
     const int n = T * topk;
     int bits = 0;
     while ((1 << bits) < G) ++bits;
@@ -696,16 +680,15 @@ dg_status sort(const int32_t* ids, int32_t* pos, int32_t* m_indices, int32_t* gr
         const int steps = (n + kSortThreads - 1) / kSortThreads;
         chunk = (steps + kSortBlocks - 1) / kSortBlocks * kSortThreads;
         blocks = (n + chunk - 1) / chunk;
-        dg_status s = stream_scratch(stream_ptr, (size_t)blocks * G * sizeof(u32), &scratch);
+        dg_status s = stream_scratch(stream, (size_t)blocks * G * sizeof(u32), &scratch);
         if (s != DG_OK) return s;
         hist = static_cast<u32*>(scratch.p);
-        hipLaunchKernelGGL(dg_moe_count_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n, G, chunk, hist);
-        s = launched("moe_sort (count)");
+        s = launch_rows("moe_sort (count)", dg_moe_count_kernel, dim3(blocks), kSortThreads, stream,
+                        CountArgs{ids, hist, n, G, chunk});
         if (s != DG_OK) return s;
     }
-    hipLaunchKernelGGL(dg_moe_place_kernel, dim3(blocks), dim3(kSortThreads), 0, stream,
+    return launch_rows("moe_sort (place)", dg_moe_place_kernel, dim3(blocks), kSortThreads, stream,
                        SortArgs{ids, hist, pos, m_indices, group_rows, n, G, bits, chunk, masked_rows, rows});
-    return launched("moe_sort (place)");
 }
 
 // the arguments dispatch, combine and combine backward share
@@ -722,8 +705,8 @@ dg_status check_rows(const char* what, const void* x, const void* pos, const voi
     return DG_OK;
 }
 
-// workgroups of four one-wave units (the kernels count units in 32 bits); 0: too many
-unsigned grid_of(int64_t units) { return units <= INT_MAX - 3 ? (unsigned)((units + 3) / 4) : 0u; }
+// workgroups of four one-wave units; 0: too many for one launch
+unsigned grid_of(int64_t units) { return fits_launch((units + 3) / 4) ? (unsigned)((units + 3) / 4) : 0u; }
 
 }  // namespace
 }  // namespace dg
@@ -776,11 +759,11 @@ dg_status dg_moe_dispatch_bf16(const void* X, const int32_t* pos, const int32_t*
         const unsigned grid = grid_of(units);
         if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_bf16: too many tokens for one launch");
         const bool stream_it = 2 * (int64_t)T * (topk + (int64_t)1) * H >= kStreamBytes;
-        hipLaunchKernelGGL((H % 8 ? dg_moe_dispatch_bf16_kernel<false, false>
-                            : stream_it ? dg_moe_dispatch_bf16_kernel<true, true> : dg_moe_dispatch_bf16_kernel<true, false>), dim3(grid),
-                           dim3(256), 0, static_cast<hipStream_t>(stream),
-                           DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, nullptr, T, topk, rows, rows, H, pieces});
-        return launched("moe_dispatch_bf16");
+        auto* kernel = H % 8 ? dg_moe_dispatch_bf16_kernel<false, false>
+                     : stream_it ? dg_moe_dispatch_bf16_kernel<true, true> : dg_moe_dispatch_bf16_kernel<true, false>;
+        return launch_rows("moe_dispatch_bf16", kernel, dim3(grid), 256, stream,
+                           DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, nullptr, T, topk, rows, rows, H,
+                                        pieces});
     });
 }
 
@@ -801,12 +784,11 @@ dg_status dg_moe_dispatch_fp8(const void* X, const int32_t* pos, const int32_t* 
         const unsigned grid = grid_of(units);
         if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_dispatch_fp8: too many tokens for one launch");
         const bool stream_it = (int64_t)T * (topk + (int64_t)2) * H >= kStreamBytes;
-        hipLaunchKernelGGL((ue8m0 ? (stream_it ? dg_moe_dispatch_fp8_kernel<true, true> : dg_moe_dispatch_fp8_kernel<true, false>)
-                                  : (stream_it ? dg_moe_dispatch_fp8_kernel<false, true> : dg_moe_dispatch_fp8_kernel<false, false>)), dim3(grid),
-                           dim3(256), 0, static_cast<hipStream_t>(stream),
+        auto* kernel = ue8m0 ? (stream_it ? dg_moe_dispatch_fp8_kernel<true, true> : dg_moe_dispatch_fp8_kernel<true, false>)
+                             : (stream_it ? dg_moe_dispatch_fp8_kernel<false, true> : dg_moe_dispatch_fp8_kernel<false, false>);
+        return launch_rows("moe_dispatch_fp8", kernel, dim3(grid), 256, stream,
                            DispatchArgs{static_cast<const u16*>(X), pos, m_indices, rows_out, static_cast<u32*>(sf), T, topk, rows,
                                         group_rows, H, pieces});
-        return launched("moe_dispatch_fp8");
     });
 }
 
@@ -822,12 +804,11 @@ dg_status dg_moe_combine(const void* rows_in, const int32_t* pos, const float* w
         const unsigned grid = grid_of((int64_t)T * pieces);
         if (!grid) return set_error(DG_ERR_UNSUPPORTED, "moe_combine: too many tokens for one launch");
         const bool stream_it = 2 * (int64_t)T * (topk + (int64_t)(residual ? 2 : 1)) * N >= kStreamBytes;
-        hipLaunchKernelGGL((N % 8 ? dg_moe_combine_kernel<false, false>
-                            : stream_it ? dg_moe_combine_kernel<true, true> : dg_moe_combine_kernel<true, false>), dim3(grid), dim3(256), 0,
-                           static_cast<hipStream_t>(stream),
+        auto* kernel = N % 8 ? dg_moe_combine_kernel<false, false>
+                     : stream_it ? dg_moe_combine_kernel<true, true> : dg_moe_combine_kernel<true, false>;
+        return launch_rows("moe_combine", kernel, dim3(grid), 256, stream,
                            CombineArgs{static_cast<const u16*>(rows_in), pos, weights, static_cast<const u16*>(residual),
                                        static_cast<u16*>(Y), T, topk, rows, N, pieces});
-        return launched("moe_combine");
     });
 }
 
@@ -844,14 +825,13 @@ dg_status dg_moe_combine_backward(const void* dY, const void* rows_in, const int
             return set_error(DG_ERR_ALIGNMENT, "moe_combine_backward: rows must be 16-byte, the other arrays 4-byte aligned");
         const int64_t blocks = (int64_t)T + (m_indices ? pad_blocks(rows) : 0);
         if (blocks == 0) return DG_OK;
-        if (blocks > INT_MAX) return set_error(DG_ERR_UNSUPPORTED, "moe_combine_backward: too many tokens for one launch");
+        if (!fits_launch(blocks)) return set_error(DG_ERR_UNSUPPORTED, "moe_combine_backward: too many tokens for one launch");
         const bool stream_it = 2 * (int64_t)T * (topk * (int64_t)(d_weights ? 2 : 1) + 1) * N >= kStreamBytes;
-        hipLaunchKernelGGL((N % 8 ? dg_moe_combine_backward_kernel<false, false>
-                            : stream_it ? dg_moe_combine_backward_kernel<true, true> : dg_moe_combine_backward_kernel<true, false>),
-                           dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+        auto* kernel = N % 8 ? dg_moe_combine_backward_kernel<false, false>
+                     : stream_it ? dg_moe_combine_backward_kernel<true, true> : dg_moe_combine_backward_kernel<true, false>;
+        return launch_rows("moe_combine_backward", kernel, dim3((unsigned)blocks), 256, stream,
                            CombineBackwardArgs{static_cast<const u16*>(dY), static_cast<const u16*>(rows_in), pos, weights,
                                                m_indices, static_cast<u16*>(d_rows), d_weights, T, topk, rows, N});
-        return launched("moe_combine_backward");
     });
 }
 

@@ -1,0 +1,45 @@
+// What the kernels over BF16 rows share (moe.hip, linear.hip): conversions, and
+// the launch of a kernel that takes one by-value struct.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+typedef unsigned char u8;
+typedef unsigned short u16;
+typedef unsigned int u32;
+typedef unsigned long long u64;
+typedef u32 u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPadding = -1;           // m_indices of a padding row inside a segment
+
+__device__ __forceinline__ float bf16_lo(u32 w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+__device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
+__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
+
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// A launch has fewer than 2^32 work items along each axis: workgroups of 256 or 1024
+// items that fit in one axis.
+inline bool fits_launch(int64_t workgroups, int items = 256) { return workgroups * items < (int64_t(1) << 32); }
+
+// Launches kernel(args).  The status is this launch's own: an error that an earlier call of the
+// thread left behind, ours or another library's, is neither reported nor cleared.
+template <typename Args>
+dg_status launch_rows(const char* what, void (*kernel)(Args), dim3 grid, int items, void* stream, Args args) {
+    void* argv[] = {&args};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(items), argv, 0,
+                                         static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? DG_OK : set_error(DG_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace dg

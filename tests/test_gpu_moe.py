@@ -364,3 +364,25 @@ def test_rows_past_four_gigabytes():
     qc, qs, _ = ref.quantise(x.float().cpu().numpy())
     at = pos[:, 0].long()
     assert np.array_equal(codes[at].cpu().numpy(), qc) and np.array_equal(sf[:, at].cpu().numpy().T, qs)
+
+
+def test_an_earlier_error_is_not_this_calls():
+    """An error that another call of the thread left in the runtime is neither reported nor cleared."""
+    from moe_grouped_gemm_scales_amd.dg import lib     # its symbols include the HIP runtime it is linked to
+    ids = _cuda(_ids(9, 2, 4, 1))
+    pos, m, ks = _i32((9, 2)), _i32(1024), _i32(4)
+    x = _bf((9, 64), 2).cuda()
+    rows = torch.zeros((1024, 64), dtype=torch.bfloat16, device="cuda")
+    dw = torch.zeros((9, 2), device="cuda")
+    db = torch.zeros(64, device="cuda")
+    torch.cuda.synchronize()
+    assert lib.hipSetDevice(99) != 0                    # no such device: refused by the runtime
+    try:
+        dg.dg_moe_sort_contiguous(ids, 4, pos, m, ks)
+        dg.dg_moe_dispatch_bf16(x, pos, m, rows)
+        dg.dg_moe_combine_backward(x, rows, pos, None, m, rows, dw)
+        dg.dg_epilogue_backward(x, x, "silu", x, db)
+    finally:
+        left = lib.hipGetLastError()
+    torch.cuda.synchronize()
+    assert left != 0

@@ -102,3 +102,10 @@ def test_binding_refuses_wrong_tensors():
         dg.dg_epilogue_backward(d, None, "swish", d, None)         # no such activation
     with pytest.raises(ValueError):
         dg.dg_epilogue_backward(d[0], None, "none", d, None)       # dD must be [M, N]
+
+
+def test_more_rows_than_one_launch_holds():
+    f = P(FAKE)
+    M = (1 << 31) - 128
+    assert lib.dg_epilogue_backward(f, f, 1, f, f, M, 8, None) == UNSUPPORTED
+    assert lib.dg_m_grouped_epilogue_backward_contiguous(f, f, 1, f, f, f, M, 8, 4, None) == UNSUPPORTED

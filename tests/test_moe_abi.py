@@ -103,3 +103,22 @@ def test_binding_refuses_wrong_tensors():
         dg.dg_moe_combine(x, i, None, None, x)                                          # host tensors
     with pytest.raises(ValueError):
         dg.dg_moe_sort_contiguous(i.reshape(-1), 8, i, i.reshape(-1), i.reshape(-1))    # ids must be [T, topk]
+
+
+@pytest.mark.parametrize("T", [1 << 26, 1 << 28])
+def test_more_tokens_than_one_launch_holds(T):
+    """A launch has fewer than 2^32 work items: one wave a token and piece (combine's gradient: four waves a token)."""
+    f = P(FAKE)
+    assert lib.dg_moe_dispatch_bf16(f, f, None, f, T, 1, 256, 8, None) == UNSUPPORTED
+    assert lib.dg_moe_dispatch_fp8(f, f, None, f, f, T, 1, 256, 256, 128, 0, None) == UNSUPPORTED
+    assert lib.dg_moe_combine(f, f, None, None, f, T, 1, 256, 8, None) == UNSUPPORTED
+    assert lib.dg_moe_combine_backward(f, f, f, None, None, f, f, T >> 2, 1, 256, 8, None) == UNSUPPORTED
+
+
+def test_rows_of_m_indices_count_to_the_launch():
+    """... and the padding rows' waves, 16 rows each, with every row count an int holds."""
+    f = P(FAKE)
+    R = (1 << 31) - 128
+    assert lib.dg_moe_dispatch_bf16(f, f, f, f, 0, 1, R, 8, None) == UNSUPPORTED
+    assert lib.dg_moe_dispatch_bf16(f, f, f, f, 0, 1, (1 << 31) - 1, 8, None) == UNSUPPORTED
+    assert lib.dg_moe_combine_backward(f, f, f, None, f, f, f, 0, 1, (1 << 31) - 1, 8, None) == UNSUPPORTED
