@@ -252,7 +252,8 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
                  const EpilogueArgs& ep = {}) {
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     const bool rewrite = !p.direct && (p.kind == kKGrouped || p.a_k_outer || p.b_k_outer);
-    const int extra = p.ep.code() * 2 + p.direct;      // what the sizes do not say about the kernels
+    // what the sizes do not say about the kernels
+    const int extra = p.ep.code() * 2 + p.direct + (p.sf == 3 && p.kind == kKGrouped ? k_share(p.kt) << 12 : 0);
     // ---- warm call: the previous call of this thread had the same key
     int dev_now = 0;
     if (hipGetDevice(&dev_now) != hipSuccess) dev_now = -1;

@@ -110,6 +110,17 @@ struct Problem {
     Epilogue ep;
 };
 
+// The K of a K-grouped problem as its plan sees it: plans are chosen and kept per eighth of
+// an octave of the K blocks, so that a token count that changes with every call neither
+// makes a new plan each time nor runs with the plan of another size.
+inline int k_share(int kt) {
+    const int blocks = (kt + 63) / 64;
+    int shift = 0;
+    while ((blocks >> shift) >= 16) ++shift;
+    return shift * 16 + (blocks >> shift);
+}
+inline int k_share_blocks(int share) { return (share % 16) << (share / 16); }
+
 // Tile heuristics (heuristics.cpp): the launches of one call, in order (one,
 // or two over disjoint column ranges).
 std::vector<KernelConfig> select_plan(const Problem& p, int num_cus);

@@ -122,7 +122,9 @@ bool valid(const KernelConfig& c, const Problem& p) {
     auto kout_tile = [](int t, int w) { return (t == 64 || t == 128 || t == 256) && ((t / w) & (t / w - 1)) == 0; };
     if (c.b_kout && (!kout_tile(c.bn, c.wn) || p.n % 8 || (c.variant != 0 && c.variant != 6) || c.kstep != 1)) return false;
     if (c.a_kout && (!kout_tile(c.bm, c.wm) || p.rows % 8)) return false;
-    if (c.splitk < 1 || (c.splitk > 1 && p.kind != kDense)) return false;   // split-K: dense only
+    // split-K: not where a row block makes two passes, and K-grouped in BF16 only
+    if (c.splitk < 1 || (c.splitk > 1 && ((p.kind == kContiguous && c.bm > 128) || (p.kind == kKGrouped && p.sf != 3))))
+        return false;
     if (c.sf != p.sf) return false;
     // variant 4: variant 0 with A requested a K block ahead of B (two B slots, three A
     // slots), for FP8 operands with FP32 or UE8M0 scales and the M forms
@@ -175,7 +177,7 @@ bool valid(const KernelConfig& c, const Problem& p) {
     // more than 32 sub-tiles per wave: only 4-wave groups without promotion (accumulators in AGPRs)
     const bool agpr_acc = (c.sf == 1 || c.sf == 3 || c.sf == 5) && c.wm * c.wn == 4;
     if (tm < 1 || tn < 1 || tm > 8 || tn > 8 || tm * tn > (agpr_acc ? 64 : 32)) return false;
-    if ((p.k / 128) % (c.splitk * c.kstep)) return false;
+    if (p.kind != kKGrouped && (p.k / 128) % (c.splitk * c.kstep)) return false;
     return true;
 }
 
@@ -282,34 +284,41 @@ std::vector<KernelConfig> tuned(const Problem& p, int num_cus, const KernelConfi
 }
 
 // The products with a fused epilogue and the BF16 NN and TN products choose among
-// these structures by a short cost sum fitted to sweeps of them on an MI355X (31
-// shapes of 1 to 17408 rows, BF16 and FP8, every form, 4100 configurations):
+// these structures by the time that a sum of measured parts gives them.  A CU
+// that gets t tiles (splits of K included) in b batches of at most per_cu takes
 //
-//   rounds * K blocks * us  (+ what a split of K costs)
+//   one tile at a time:   b * (start + K blocks * us)
+//   several at a time:    start * (1 + 1.5 (b - 1)) + K blocks * max(b * us, t * us_full)
 //
-// with rounds = ceil(tiles / 256 CUs) and us the measured time a CU takes
-// for one 128-byte K block of the tile.  Structures that several workgroups of a CU
-// share have their smaller time with the CU full.  What decides, measured (the
-// general model's choice in brackets): 517 x 2112 x 1536 BF16 14.4 us (17.3); 64 x
-// 4096 x 7168 16.8 (28.6); 1024 x 4096 x 4096 39.7 (48.2); 5 experts' 2176 x 2048 x
-// 2048 36.6 as 128 x 256 and 32.6 as 128 x 192 (53.8); 3000 x 2048 x 2048 33.9 as
-// 128 x 256 and 30.0 as 192 x 128; masked 8 x 256 x 2048 x 4096
-// FP8 33.0 (53.5); 4 experts' 8704 x 4096 x 7168 FP8 261 as 128 x 128, whose 2176
-// tiles leave 6 % of the last round idle, against 348 as 256 x 256 (544 tiles, 29 %
-// idle), where 8192 x 4096 x 7168 BF16 (512 tiles) runs 348 as 256 x 256 and over
-// 430 as 128 x 128.
+// with us the time of one 128-byte K block while a tile has the CU to itself, us_full
+// that per tile with the CU full, and start = 1.1 + 2.3 * (tile area / 128^2) us for
+// the first loads and the epilogue.  A split of K adds its hand-off, 0.6 us, and 2.7 us
+// per 10^6 FP32 partials.  The figures are fitted to 1420 launches of 59 shapes (1 to
+// 17408 rows, BF16 and FP8, every form) on an MI355X; over these and 11 more the choice takes
+// 2.0 % longer than the fastest structure in the geometric mean (a sum without start,
+// without split-K for the grouped and TN forms and with one tile a CU: 7.7 %).  What decides,
+// measured (the general model's choice in brackets): 64 x 4096 x 7168 BF16 16.8 us
+// (28.6); 1024 x 4096 x 4096 39.7 (48.2); masked 8 x 256 x 2048 x 4096 FP8 33.0 (53.5);
+// 4 experts' 8704 x 4096 x 7168 FP8 250 as 128 x 128, whose 2176 tiles leave 6 % of the last
+// round idle, against 323 as 256 x 256 (544 tiles, 29 % idle), where 8192 x 4096 x 7168
+// BF16 (512 tiles) runs 348 as 256 x 256 and over 430 as 128 x 128.  Split against
+// unsplit: TN 512 x 512 over K 16384 21 us against 65, TN 1600 x 1408 over 6721 45 against
+// 56, masked 4 x 64 x 2048 x 7168 FP8 17.0 against 25.5, masked 2 x 447 x 1152 x 6528 BF16
+// 17.4 against 24.9, contiguous 2 experts' 256 x 1600 x 4352 FP8 11.7 against 13.9.
 struct Structure {
     int bm, bn, wm, wn, stages, variant;
-    int shares_cu;                 // only with more than one round: two workgroups a CU
+    int per_cu;                    // tiles a CU works on at a time
     double us_bf16, us_fp8;        // (FP8: a block is 128 K values, and its scales are applied)
+    double us_full_bf16, us_full_fp8;
 };
 const Structure kStructures[] = {
-    {256, 256, 4, 2, 2, 6, 0, 1.55, 1.85}, {128, 256, 2, 4, 3, 0, 0, 0.89, 1.00},
-    {128, 192, 2, 4, 3, 0, 0, 0.76, 0.83}, {192, 128, 4, 2, 3, 0, 0, 0.72, 0.83},
-    {128, 128, 4, 2, 4, 0, 0, 0.58, 0.62}, {128, 128, 2, 2, 2, 6, 1, 0.50, 0.52},
-    {128, 64, 4, 2, 4, 0, 0, 0.39, 0.39},  {64, 128, 2, 4, 4, 0, 0, 0.40, 0.40},
-    {64, 64, 2, 2, 4, 0, 0, 0.23, 0.23},   {32, 64, 1, 4, 4, 0, 0, 0.22, 0.22},
-    {16, 64, 1, 4, 4, 0, 0, 0.20, 0.20},   {16, 32, 1, 2, 6, 0, 0, 0.14, 0.14},
+    {256, 256, 4, 2, 2, 6, 1, 1.37, 1.64, 0, 0},       {128, 256, 2, 4, 3, 0, 1, 0.80, 0.89, 0, 0},
+    {128, 192, 2, 4, 3, 0, 1, 0.75, 0.82, 0, 0},       {192, 128, 4, 2, 3, 0, 1, 0.64, 0.74, 0, 0},
+    {128, 128, 4, 2, 4, 0, 1, 0.51, 0.54, 0, 0},       {128, 128, 2, 2, 2, 6, 2, 0.64, 0.64, 0.49, 0.49},
+    {128, 64, 4, 2, 4, 0, 1, 0.33, 0.41, 0, 0},        {64, 128, 2, 4, 4, 0, 1, 0.34, 0.41, 0, 0},
+    {64, 128, 2, 2, 3, 0, 2, 0.45, 0.43, 0.38, 0.33},  {64, 64, 2, 2, 4, 0, 2, 0.23, 0.32, 0.23, 0.18},
+    {32, 64, 1, 4, 4, 0, 2, 0.20, 0.29, 0.15, 0.21},   {16, 64, 1, 4, 4, 0, 4, 0.13, 0.22, 0.11, 0.20},
+    {16, 32, 1, 2, 6, 0, 4, 0.16, 0.17, 0.11, 0.12},
 };
 
 bool uses_structures(const Problem& p) {
@@ -317,29 +326,53 @@ bool uses_structures(const Problem& p) {
 }
 
 std::vector<KernelConfig> choose_structure(const Problem& p, int num_cus, const KernelConfig& base) {
-    // row blocks of a masked group: half its rows valid on average, the last block part full
-    auto row_blocks = [&](int bm) {
-        if (p.kind == kMasked) return (0.5 * p.rows / bm + 0.5) * p.g;
+    // row blocks, with this share of a masked group's rows valid (the last block part full)
+    auto row_blocks = [&](int bm, double valid_rows) {
+        if (p.kind == kMasked)
+            return std::min((double)((p.rows + bm - 1) / bm), valid_rows * p.rows / bm + 0.5) * p.g;
+        // a 256-row block of two experts is computed for each: about half of the segments' ends
+        if (p.kind == kContiguous && bm > 128) return (double)((p.rows + bm - 1) / bm) + 0.5 * (p.g - 1);
         return (double)((p.rows + bm - 1) / bm) * (p.kind == kKGrouped ? p.g : 1);
     };
-    const int kb = p.k / 128;           // (K-grouped: no constant, and the same for every structure)
+    // rows of the output, for a split's partials
+    const double out_rows = p.kind == kMasked ? 0.5 * p.rows * p.g : p.kind == kKGrouped ? (double)p.rows * p.g : p.rows;
+    // K blocks of a tile; K-grouped: of a group on average, from the plan's share of K
+    const double kb = p.kind == kKGrouped ? std::max(1.0, (double)k_share_blocks(k_share(p.kt)) / p.g) : p.k / 128;
     double best = 1e30;
     std::vector<KernelConfig> out;
     for (const Structure& st : kStructures) {
-        const double tiles = row_blocks(st.bm) * ((p.n + st.bn - 1) / st.bn);
+        // (TN reads 128 x 64 tiles slowly: 512 x 512 over K 16384 28.8 us against 21.0 as 64 x 128)
+        if (p.kind == kKGrouped && st.bm > st.bn) continue;
+        // (many blocks of few rows read B again and again: 97 x 2616 x 448 NN 6.6 us as 16 x 64, 5.4 as
+        // 32 x 64; and blocks of many more rows than there are were not among the launches)
+        if (p.rows > (st.bm == 16 ? 64 : st.bm == 32 ? 1024 : p.rows)) continue;
+        if (p.kind != kKGrouped && p.rows <= (st.bm > 64 ? 64 : st.bm > 16 ? 16 : 0)) continue;
+        const int columns = (p.n + st.bn - 1) / st.bn;
+        const double tiles = row_blocks(st.bm, 0.5) * columns;
+        const double us = p.sf == 3 ? st.us_bf16 : st.us_fp8;
+        const double us_full = p.sf == 3 ? st.us_full_bf16 : st.us_full_fp8;
+        const double start = 1.1 + 2.3 * st.bm * st.bn / 16384.0;
         for (int sk = 1; sk <= 16; ++sk) {
-            if (sk > 1 && (p.kind != kDense || kb % sk || kb / sk < 4)) continue;
-            const double rounds = std::max(1.0, std::ceil(tiles * sk / num_cus));
-            if (sk > 1 && rounds > 1) break;
-            if (st.shares_cu && rounds < 2) continue;
-            double us = rounds * (kb / sk) * (p.sf == 3 ? st.us_bf16 : st.us_fp8);
-            // a split: the hand-off, and its FP32 partials out and back at about 4 TB/s
-            if (sk > 1) us += 1.5 + 8.0 * p.rows * p.n * sk / 4.0e6;
+            if (sk > 1 && (kb / sk < 4 || (p.kind != kKGrouped && (p.k / 128) % sk))) continue;
+            if (sk > 1 && tiles * sk > 2 * num_cus) break;     // (the tiles alone fill the device)
+            const double blocks = std::ceil(kb / sk);
+            auto time_of = [&](double items) {
+                double per_cu = std::max(1.0, std::ceil(items / num_cus - 1e-9));
+                if (p.kind == kContiguous && st.bm > 128 && p.g > 1) per_cu = std::max(per_cu, 2.0);   // (some CU has such a block)
+                const double batches = std::ceil(per_cu / st.per_cu);
+                if (st.per_cu == 1) return batches * (start + blocks * us);
+                return start * (1 + 1.5 * (batches - 1)) + blocks * std::max(batches * us, per_cu * us_full);
+            };
+            double t = time_of(tiles * sk);
+            // (half the rows, a quarter fewer and a quarter more: a choice must not need luck)
+            if (p.kind == kMasked)
+                t = (t + time_of(row_blocks(st.bm, 0.375) * columns * sk) + time_of(row_blocks(st.bm, 0.625) * columns * sk)) / 3;
+            if (sk > 1) t += 0.6 + 2.7e-6 * out_rows * p.n * sk;
             KernelConfig c = base;
             c.bm = st.bm; c.bn = st.bn; c.wm = st.wm; c.wn = st.wn;
             c.stages = st.stages; c.variant = st.variant; c.splitk = sk; c.kstep = 1;
-            if (us < best && valid(c, p)) {
-                best = us;
+            if (t < best && valid(c, p)) {
+                best = t;
                 out = {c};
             }
         }
@@ -401,8 +434,7 @@ bool valid_plan(const std::vector<KernelConfig>& plan, const Problem& p) {
 int64_t num_work_items(const KernelConfig& c, int rows) {
     const int64_t mt = (rows + c.bm - 1) / c.bm;
     const int64_t nt = (c.n_end() - c.n_begin() + c.bn - 1) / c.bn;
-    if (c.kind == kMasked || c.kind == kKGrouped) return mt * nt * c.g;
-    return mt * nt * c.splitk;
+    return mt * nt * c.splitk * (c.kind == kMasked || c.kind == kKGrouped ? c.g : 1);
 }
 
 std::vector<KernelConfig> select_plan(const Problem& p, int num_cus) {

@@ -133,6 +133,9 @@ typedef u16 v4u16 __attribute__((ext_vector_type(4)));
 #define DG_B_KOUT 0
 #endif
 #define DG_EPI (DG_BIAS || DG_ACT || DG_RES || DG_ZOUT)
+// Contiguous forms of these products (variant 0): work items are those of the row
+// blocks that are in use (used_row_blocks)
+#define DG_USED_ROWS (DG_KIND == 1 && (DG_EPI || DG_B_KOUT) && DG_VARIANT == 0)
 
 namespace dg {
 
@@ -173,12 +176,12 @@ constexpr bool KG = kKind == 3;                // K-grouped: per-column B scales
 constexpr bool SB_UNIFORM = (KBLK % WAVE_N) == 0 && (DG_NB % WAVE_N) == 0 && !FP4B && !KG && !BF16;
 static_assert(!BF16 || DG_KSTEP == 1, "BF16: one K block a stage");
 constexpr int KROWS = BF16 ? KBLK / 2 : KBLK;  // K indices of a 128-byte block (K-grouped counts)
-static_assert(!KG || (!SF_E8 && DG_SPLITK == 1 && DG_KSTEP == 1), "K-grouped: FP32 scales, no split-K, one K block a stage");
+static_assert(!KG || (!SF_E8 && (DG_SPLITK == 1 || BF16) && DG_KSTEP == 1), "K-grouped: FP32 scales, split-K in BF16 only, one K block a stage");
 
 static_assert(K % KBLK == 0, "K must be a multiple of 128");
 static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tiles must be 16-aligned");
 static_assert(KSTEP == 1 || KSTEP == 2, "one or two K blocks per stage");
-static_assert(KBLKS % (SPLITK * KSTEP) == 0, "split-K and stage depth must divide the K blocks");
+static_assert(KG || KBLKS % (SPLITK * KSTEP) == 0, "split-K and stage depth must divide the K blocks");
 static_assert(STAGES >= 2, "at least double buffering");
 
 // Register budget: 256 per lane, as for two waves per SIMD, whatever the wave
@@ -211,6 +214,9 @@ struct Params {
     const u8* bias;
     const u16* res;
     u16* z;
+#endif
+#if DG_USED_ROWS
+    int row_blocks = 0;    // of the rows that are in use
 #endif
 };
 
@@ -391,7 +397,11 @@ __device__ __forceinline__ int xcd_spread(int t, int num_items) {
 // Grouped order: walk 8 m-tiles per column sweep so that concurrently resident
 // workgroups share A and B tiles in L2.
 __device__ __forceinline__ void tile_position(const Params& p, int t, int& mn, int& split, int& mt, int& nt) {
+#if DG_USED_ROWS
+    const int num_mt = p.row_blocks;
+#else
     const int num_mt = (p.M + BM - 1) / BM;
+#endif
     t = xcd_spread(t, p.num_tiles);
     mn = t / SPLITK;
     split = t % SPLITK;
@@ -413,6 +423,24 @@ __device__ __forceinline__ void tile_experts(const Params& p, int t, int& g, int
     g2 = (BM > 128 && m0 + 128 < p.M) ? p.grp[m0 + 128] : -1;
 }
 
+#if DG_USED_ROWS
+// Row blocks up to the last that names an expert.  A caller who does not wait for the device
+// gives M as a capacity that this call's experts seldom fill; dealt out with the others, the
+// row blocks past the last segment would leave some CUs nothing and others two tiles (8 of 14
+// row blocks in use, NN 5440 x 1344 in 128 x 256 tiles: 33.6 us, 30.3 without them; all
+// in use: no difference).  One load of 64 blocks' first rows, from the end.
+__device__ __forceinline__ int used_row_blocks(const Params& p) {
+    for (int end = (p.M + BM - 1) / BM; end > 0; end -= 64) {
+        const int m0 = (end - 1 - (int)(threadIdx.x & 63)) * BM;
+        bool used = m0 >= 0 && (u32)p.grp[m0 < 0 ? 0 : m0] < (u32)G;
+        if (BM > 128 && m0 >= 0 && m0 + 128 < p.M) used = used || (u32)p.grp[m0 + 128] < (u32)G;
+        const u64 mask = __ballot(used);
+        if (mask) return end - __builtin_ctzll(mask);
+    }
+    return 0;
+}
+#endif
+
 // PRE: the contiguous form's experts come from tile_experts() (g_pre, g2_pre)
 // instead of being read here.
 template <bool PRE = false>
@@ -425,6 +453,10 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
     tl.kb1 = KBLKS;
     if constexpr (kKind == 2) {
         // Masked: enumerate only the active row blocks, group by group.
+        tl.mn = t / SPLITK;
+        tl.split = t % SPLITK;
+        tl.kb0 = tl.split * (KBLKS / SPLITK);
+        tl.kb1 = tl.kb0 + KBLKS / SPLITK;
         const int nmt_max = (p.M + BM - 1) / BM;
         int g = 0, base = 0;
         int mb = 0, nt = 0, valid = 0;
@@ -435,8 +467,8 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
             int nmt = (v + BM - 1) / BM;
             if (nmt > nmt_max) nmt = nmt_max;
             int cnt = nmt * NUM_NT;
-            if (t < base + cnt) {
-                int local = t - base;
+            if (tl.mn < base + cnt) {
+                int local = tl.mn - base;
                 mb = local % nmt;                 // row blocks fastest: they share B
                 nt = local / nmt;
                 valid = v;
@@ -450,7 +482,6 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         tl.n0 = N_BEGIN + nt * BN;
         tl.rows = p.M - tl.m0 < BM ? p.M - tl.m0 : BM;
         tl.row_limit = valid - tl.m0;
-        tl.mn = 0;
     } else if constexpr (kKind == 3) {
         // K-grouped: every group has the same output tiles; its K range is the
         // prefix sum of ks (negative counts taken as 0, cut at kt; a count that
@@ -459,8 +490,10 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         const int num_mt = (p.M + BM - 1) / BM;
         const int per_g = num_mt * NUM_NT;
         t = xcd_spread(t, p.num_tiles);
-        const int g = t / per_g;
-        const int local = t % per_g;
+        tl.mn = t / SPLITK;
+        tl.split = t % SPLITK;
+        const int g = tl.mn / per_g;
+        const int local = tl.mn % per_g;
         int off = 0;
         int len = p.kt;
         if (!BF16 || p.grp) {
@@ -483,9 +516,12 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         tl.n0 = N_BEGIN + nt * BN;
         tl.rows = p.M - tl.m0 < BM ? p.M - tl.m0 : BM;
         tl.row_limit = tl.rows;
-        tl.kb0 = kb0;
-        tl.kb1 = kb1 > kb0 ? kb1 : kb0;
-        tl.mn = 0;
+        kb1 = kb1 > kb0 ? kb1 : kb0;
+        // split s of a group of nk K blocks takes [nk s / SPLITK, nk (s + 1) / SPLITK) of them
+        // (a group of fewer blocks than splits leaves some of its splits empty)
+        const int nk = kb1 - kb0;
+        tl.kb0 = SPLITK > 1 ? kb0 + (int)((u64)nk * (u32)tl.split / SPLITK) : kb0;
+        tl.kb1 = SPLITK > 1 ? kb0 + (int)((u64)nk * (u32)(tl.split + 1) / SPLITK) : kb1;
     } else {
         int mn, mt, nt;
         tile_position(p, t, mn, tl.split, mt, nt);
@@ -1071,11 +1107,18 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
     u32* __restrict__ counters = (u32*)ka.counters;
     const int M = ka.M, num_tiles = ka.num_tiles, kt = ka.kt;
     u32* __restrict__ status = (u32*)ka.status;
-    const Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status DG_EPI_ARGS};
+#if !DG_USED_ROWS
+    const
+#endif
+    Params p{A, sfa, B, sfb, C, D, grp, ws, counters, M, num_tiles, kt, status DG_EPI_ARGS};
     // Every argument in one round trip of scalar loads: otherwise the loop bound
     // is fetched first and the pointers only after it arrives (~0.5 us each).
     asm volatile("" :: "s"(A), "s"(sfa), "s"(B), "s"(sfb), "s"(C), "s"(D), "s"(grp), "s"(ws), "s"(counters), "s"(M),
                  "s"(num_tiles), "s"(gridDim.x));
+#if DG_USED_ROWS
+    p.row_blocks = __builtin_amdgcn_readfirstlane(used_row_blocks(p));
+    p.num_tiles = p.row_blocks * NUM_NT * SPLITK;
+#endif
     __shared__ __attribute__((aligned(1024))) u8 smem[LDS_BYTES];
 
     const int tid = threadIdx.x;

@@ -446,3 +446,117 @@ def test_tn_operand_around_four_gigabytes(N):
     rest = torch.ones(N, dtype=torch.bool, device="cuda")
     rest[cols] = False
     assert not D[:, rest].any()
+
+
+# ------------------------------------------------------------------ split-K of the grouped and TN forms
+SPLITS = ["64,64,2,2,4,4,1,0", "64,128,2,2,3,3,1,0", "128,128,2,2,2,2,1,6", "32,64,1,4,4,6,1,0", "16,32,1,2,6,4,1,0"]
+
+
+def _same_twice(call, out):
+    """The splits' partials are added in split order whichever arrives last: the same bits on every run (rows that are not computed keep the NaN)."""
+    out.fill_(float("nan"))
+    call()
+    first = out.cpu().view(torch.int16)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        call()
+        assert torch.equal(out.cpu().view(torch.int16), first)
+
+
+@pytest.mark.parametrize("forced", SPLITS)
+@pytest.mark.parametrize("bf16", [True, False])
+def test_split_k_of_grouped_products(monkeypatch, forced, bf16):
+    """Empty experts, padding rows, masks that leave a tile part full or empty; K of 24 (FP8: 12) blocks."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    K = 1536
+    for N in (256, 333):
+        for rows in ([128, 0, 200, 100], [1, 1]):
+            p = gen.make_bf16("contiguous", seed=13, N=N, K=K, group_rows=rows, pad_rows=128) if bf16 else \
+                gen.make_contiguous(rows, N, K, seed=13, pad_rows=128)
+            if bf16:
+                p.A[p.m_indices < 0] = float("nan")
+            _check(p, True, "gelu", True, True, 14, what=f"contiguous {forced} {N} {rows}")
+        for counts in ([60, 0, 33], [0, 0, 0], [1, 130, 128]):
+            p = gen.make_bf16("masked", seed=14, N=N, K=K, G=3, M_max=130, masked_m=counts) if bf16 else \
+                gen.make_masked(3, 130, N, K, seed=14, masked_m=counts)
+            _check(p, True, "silu", True, True, 15, what=f"masked {forced} {N} {counts}")
+
+
+@pytest.mark.parametrize("forced", SPLITS[:2] + ["16,32,1,2,6,6,1,0"])
+def test_split_k_of_packed_scales(monkeypatch, forced):
+    """Splits that begin inside a word of four scales."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    p = gen.make_masked(2, 70, 200, 18 * 128 if "6,6" in forced or ",3,1" in forced else 20 * 128, seed=6, masked_m=[70, 9], ue8m0=True)
+    _check(p, True, "relu", False, True, 10, what="ue8m0 masked")
+
+
+@pytest.mark.parametrize("forced", SPLITS[:3] + ["64,64,2,2,4,16,1,0"])
+@pytest.mark.parametrize("ks,M,N", [([128], 40, 72), ([128, 0, 256, 1152], 264, 520), ([0, 0], 16, 16), ([640, 128], 33, 515)])
+def test_split_k_of_tn(monkeypatch, forced, ks, M, N):
+    """Groups of fewer K blocks than splits, empty ones, operands read as stored and rewritten; C added once."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    for with_c in (False, True):
+        test_bf16_k_grouped(ks, M, N, with_c)
+    if len(ks) == 1:
+        for K in (1, 63, 200, 1000):
+            test_bf16_tn(M, N, K, True)
+
+
+@pytest.mark.parametrize("K", [16384, 12345, 3000])
+def test_split_k_is_chosen_for_few_tn_tiles(K):
+    M = N = 256
+    key = dg.describe_config(3 | dg.KIND_BF16, M, N, K, 1)
+    assert int(key.split("_sk")[1].split("_")[0]) > 1, key
+    A, B = _bf((K, M), 1), _bf((K, N), 2)
+    a, b = A.cuda(), B.cuda()
+    D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _same_twice(lambda: dg.dg_bf16_gemm_tn(a, b, None, D), D)
+    _close(D, A.double().numpy().T @ B.double().numpy(), f"tn {K}")
+
+
+def test_split_k_is_chosen_for_few_masked_tiles():
+    G, M, N, K = 2, 64, 1024, 7168
+    key = dg.describe_config(2 | dg.EPI_BIAS_F32, M, N, K, G)
+    assert int(key.split("_sk")[1].split("_")[0]) > 1, key
+    p = gen.make_masked(G, M, N, K, seed=3, masked_m=[64, 5])
+    _check(p, True, "silu", True, True, 4, what="masked")
+    c = [t.cuda() for t in (p.A, p.sfa, p.B, p.sfb, p.masked_m)]
+    D = torch.zeros((G, M, N), dtype=torch.bfloat16, device="cuda")
+    bias = torch.randn((G, N), device="cuda")
+    _same_twice(lambda: dg.dg_m_grouped_fp8_gemm_nt_masked_epilogue(*c, D, bias=bias, activation="gelu"), D)
+
+
+def test_token_counts_that_change_share_few_plans():
+    """A TN plan is chosen per eighth of an octave of K, so the same K gives the same bits whatever ran before."""
+    M, N = 192, 200
+    A, B = _bf((9000, M), 1).cuda(), _bf((9000, N), 2).cuda()
+    out = lambda: torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    first = {}
+    for K in (700, 8999, 8000, 64, 700, 5000, 8999, 64, 8000, 5000):
+        D = out()
+        dg.dg_bf16_gemm_tn(A[:K], B[:K], None, D)
+        assert torch.equal(first.setdefault(K, D).view(torch.int16), D.view(torch.int16)), K
+        _close(D.cpu(), A[:K].double().cpu().numpy().T @ B[:K].double().cpu().numpy(), f"tn {K}")
+
+
+def test_split_k_replays_from_a_graph():
+    K, M, N = 6000, 128, 192
+    a, b = _bf((K, M), 1).cuda(), _bf((K, N), 2).cuda()
+    D, E = (torch.zeros((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        dg.dg_bf16_gemm_tn(a, b, None, D)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dg.dg_bf16_gemm_tn(a, b, None, D)
+    for seed in range(4):
+        a.copy_(_bf((K, M), 20 + seed))
+        D.zero_()
+        torch.cuda.synchronize()
+        dg.dg_bf16_gemm_tn(a, b, None, E)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(D.view(torch.int16), E.view(torch.int16)), seed
