@@ -329,7 +329,7 @@ dg_moe_dispatch_bf16_kernel(const DispatchArgs a) {
         } else {
             u16 v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = c0 + lane + 64 * i < H ? src[c0 + lane + 64 * i] : (u16)0;
+            for (int i = 0; i < 16; ++i) v[i] = src[c0 + lane + 64 * i < H ? c0 + lane + 64 * i : H - 1];   // (dropped past H)
             for (int j = 0; j < k; ++j) {
                 const int r = pos[(u64)t * k + j];
                 if ((u32)r >= (u32)rows) continue;
@@ -506,9 +506,7 @@ __global__ void __launch_bounds__(256) dg_moe_combine_kernel(const CombineArgs a
         if constexpr (VEC) {
             if (in_range) w = load16<STREAM>(p + col(0));
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col(i) < N) w[i >> 1] |= (u32)p[col(i)] << (16 * (i & 1));
+            w = load_spread(p, c0 + lane, N);
         }
         return w;
     };
@@ -578,17 +576,16 @@ __global__ void __launch_bounds__(256) dg_moe_combine_backward_kernel(const Comb
     const int t = blockIdx.x;
     auto col = [&](int c0, int i) { return VEC ? c0 + lane * 8 + i : c0 + lane + 64 * i; };
     auto load = [&](const u16* p, int c0, float (&v)[8]) {
+        u32x4 w = {0u, 0u, 0u, 0u};
         if constexpr (VEC) {
-            u32x4 w = {0u, 0u, 0u, 0u};
             if (col(c0, 0) < N) w = load16<STREAM>(p + col(c0, 0));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = bf16_lo(w[i]);
-                v[2 * i + 1] = bf16_hi(w[i]);
-            }
         } else {
+            w = load_spread(p, c0 + lane, N);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = col(c0, i) < N ? __builtin_bit_cast(float, (u32)p[col(c0, i)] << 16) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(w[i]);
+            v[2 * i + 1] = bf16_hi(w[i]);
         }
     };
     auto store = [&](u16* p, int c0, const float (&v)[8]) {

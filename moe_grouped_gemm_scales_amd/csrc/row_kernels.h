@@ -25,6 +25,22 @@ __device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(floa
 __device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
 __device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
 
+// Eight BF16 of a row whose width N is no multiple of 8, 64 apart from column c, two a word;
+// zeros past N.  Past the end the last element is read instead and dropped, so that the
+// eight loads are issued together: with a branch round each they were waited for one by one
+// (epilogue backward, 300 x 515: 13.3 us against 8.5; combine of 86 x 5 rows of 1977: 7.8
+// against 4.4).
+__device__ __forceinline__ u32x4 load_spread(const u16* p, int c, int N) {
+    u32 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[c + 64 * i < N ? c + 64 * i : N - 1];
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (c + 128 * i < N ? v[2 * i] : 0u) | (c + 128 * i + 64 < N ? v[2 * i + 1] << 16 : 0u);
+    return w;
+}
+
 inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // A launch has fewer than 2^32 work items along each axis: workgroups of 256 or 1024
