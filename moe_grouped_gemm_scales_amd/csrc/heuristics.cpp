@@ -177,8 +177,9 @@ bool valid(const KernelConfig& c, const Problem& p) {
     // more than 32 sub-tiles per wave: only 4-wave groups without promotion (accumulators in AGPRs)
     const bool agpr_acc = (c.sf == 1 || c.sf == 3 || c.sf == 5) && c.wm * c.wn == 4;
     if (tm < 1 || tn < 1 || tm > 8 || tn > 8 || tm * tn > (agpr_acc ? 64 : 32)) return false;
-    if (p.kind != kKGrouped && (p.k / 128) % (c.splitk * c.kstep)) return false;
-    return true;
+    // uneven splits: one K block a stage, variants 0 and 6
+    if (p.kind != kKGrouped && (c.kstep != 1 || c.variant == 4) && (p.k / 128) % (c.splitk * c.kstep)) return false;
+    return p.kind == kKGrouped || p.k / 128 >= c.splitk;
 }
 
 // Configurations measured fastest on an MI355X (graph-replayed back-to-back
@@ -353,7 +354,7 @@ std::vector<KernelConfig> choose_structure(const Problem& p, int num_cus, const 
         const double us_full = p.sf == 3 ? st.us_full_bf16 : st.us_full_fp8;
         const double start = 1.1 + 2.3 * st.bm * st.bn / 16384.0;
         for (int sk = 1; sk <= 16; ++sk) {
-            if (sk > 1 && (kb / sk < 4 || (p.kind != kKGrouped && (p.k / 128) % sk))) continue;
+            if (sk > 1 && kb / sk < 4) continue;
             if (sk > 1 && tiles * sk > 2 * num_cus) break;     // (the tiles alone fill the device)
             const double blocks = std::ceil(kb / sk);
             auto time_of = [&](double items) {

@@ -181,7 +181,12 @@ static_assert(!KG || (!SF_E8 && (DG_SPLITK == 1 || BF16) && DG_KSTEP == 1), "K-g
 static_assert(K % KBLK == 0, "K must be a multiple of 128");
 static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tiles must be 16-aligned");
 static_assert(KSTEP == 1 || KSTEP == 2, "one or two K blocks per stage");
-static_assert(KG || KBLKS % (SPLITK * KSTEP) == 0, "split-K and stage depth must divide the K blocks");
+static_assert(KG || KBLKS % (SPLITK * KSTEP) == 0 || (DG_VARIANT == 0 && KSTEP == 1),
+              "split-K and stage depth must divide the K blocks (variant 0 with one K block a stage: uneven splits)");
+// First K block of split s; with splits that do not divide the K blocks, some have one more.
+__device__ __forceinline__ constexpr int split_begin(int s) {
+    return KBLKS % SPLITK == 0 ? s * (KBLKS / SPLITK) : KBLKS * s / SPLITK;
+}
 static_assert(STAGES >= 2, "at least double buffering");
 
 // Register budget: 256 per lane, as for two waves per SIMD, whatever the wave
@@ -455,8 +460,8 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         // Masked: enumerate only the active row blocks, group by group.
         tl.mn = t / SPLITK;
         tl.split = t % SPLITK;
-        tl.kb0 = tl.split * (KBLKS / SPLITK);
-        tl.kb1 = tl.kb0 + KBLKS / SPLITK;
+        tl.kb0 = split_begin(tl.split);
+        tl.kb1 = KBLKS % SPLITK == 0 ? tl.kb0 + KBLKS / SPLITK : split_begin(tl.split + 1);
         const int nmt_max = (p.M + BM - 1) / BM;
         int g = 0, base = 0;
         int mb = 0, nt = 0, valid = 0;
@@ -530,8 +535,8 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         tl.n0 = N_BEGIN + nt * BN;
         tl.rows = p.M - tl.m0 < BM ? p.M - tl.m0 : BM;
         tl.row_limit = tl.rows;
-        tl.kb0 = tl.split * (KBLKS / SPLITK);
-        tl.kb1 = tl.kb0 + KBLKS / SPLITK;
+        tl.kb0 = split_begin(tl.split);
+        tl.kb1 = KBLKS % SPLITK == 0 ? tl.kb0 + KBLKS / SPLITK : split_begin(tl.split + 1);
         if constexpr (kKind == 1) {
             const int g = PRE ? g_pre : p.grp[tl.m0];
             tl.g = g;

@@ -560,3 +560,32 @@ def test_split_k_replays_from_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(D.view(torch.int16), E.view(torch.int16)), seed
+
+
+@pytest.mark.parametrize("forced", SPLITS + ["64,64,2,2,4,7,1,0", "16,64,1,4,4,13,1,0"])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_uneven_splits(monkeypatch, forced, bf16):
+    """13 K blocks, which no split but 13 divides: dense, contiguous and masked, operands of either layout."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    K, N = 13 * (64 if bf16 else 128), 200
+    dense = gen.make_bf16("dense", seed=3, M=70, N=N, K=K) if bf16 else gen.make_dense(70, N, K, seed=3)
+    _check(dense, True, "gelu", True, True, 4, what=f"dense {forced}")
+    rows, counts = [100, 0, 129], [40, 0, 1]
+    p = gen.make_bf16("contiguous", seed=5, N=N, K=K, group_rows=rows, pad_rows=128) if bf16 else \
+        gen.make_contiguous(rows, N, K, seed=5, pad_rows=128)
+    _check(p, True, "silu", True, False, 6, what=f"contiguous {forced}")
+    p = gen.make_bf16("masked", seed=7, N=N, K=K, G=3, M_max=40, masked_m=counts) if bf16 else \
+        gen.make_masked(3, 40, N, K, seed=7, masked_m=counts)
+    _check(p, True, "relu", True, True, 8, what=f"masked {forced}")
+    if bf16:
+        test_bf16_nn(70, N, K, True)
+    else:
+        _check(gen.make_dense(70, N, K, seed=9, ue8m0=True), True, "relu", False, True, 10, what=f"ue8m0 {forced}")
+
+
+@pytest.mark.parametrize("N", [72, 515])
+def test_split_is_chosen_for_a_prime_number_of_blocks(N):
+    M, K = 5, 107 * 64
+    key = dg.describe_config(0 | dg.KIND_BF16 | dg.EPI_BIAS_F32, M, N, K, 1)
+    assert int(key.split("_sk")[1].split("_")[0]) > 1, key
+    _check(gen.make_bf16("dense", seed=3, M=M, N=N, K=K), True, "silu", True, True, 4, what=f"prime {N}")
