@@ -616,12 +616,17 @@ __device__ __forceinline__ u32 cvt_pair(float x, float y) {
 
 // Four columns n .. n + 3 of a lane at element offset off, as BF16.
 __device__ __forceinline__ void store4(u16* base, u64 off, int n, v4f v) {
+    const v2u32 w{cvt_pair(v.x, v.y), cvt_pair(v.z, v.w)};
     if constexpr (VEC4) {
-        if (n < N_END) *(v2u32*)(base + off) = v2u32{cvt_pair(v.x, v.y), cvt_pair(v.z, v.w)};
+        if (n < N_END) *(v2u32*)(base + off) = w;
+    } else if (n + 3 < N_END) {
+        // (a row of any width: one store of whatever alignment, 4478 x 2139 x 448 with Z
+        // 32.7 us against 50.6 in four stores, with a residual too 40.5 against 66.4)
+        __builtin_memcpy(base + off, &w, 8);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (n + e < N_END) base[off + e] = (u16)cvt_pair(v[e], 0.f);
+            if (n + e < N_END) base[off + e] = (u16)(w[e >> 1] >> (16 * (e & 1)));
     }
 }
 // Two sub-tiles' columns (n and n + 16) of a lane as one 16-byte store: lanes 16
@@ -703,9 +708,15 @@ __device__ __forceinline__ void fused_epilogue(const Params& p, const Tile& tl, 
                 v += bf16x4(res[a & 1][b]);
             } else if constexpr (DG_RES != 0) {
                 const int n = tl.n0 + col0 + b * 16;
+                v2u32 w = {0u, 0u};
+                if (n + 3 < N_END) {
+                    __builtin_memcpy(&w, p.res + row_off + n, 8);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < N_END) v[e] += __builtin_bit_cast(float, (u32)p.res[row_off + n + e] << 16);
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < N_END) w[e >> 1] |= (u32)p.res[row_off + n + e] << (16 * (e & 1));
+                }
+                v += bf16x4(w);
             }
             return v;
         };
