@@ -589,3 +589,24 @@ def test_split_is_chosen_for_a_prime_number_of_blocks(N):
     key = dg.describe_config(0 | dg.KIND_BF16 | dg.EPI_BIAS_F32, M, N, K, 1)
     assert int(key.split("_sk")[1].split("_")[0]) > 1, key
     _check(gen.make_bf16("dense", seed=3, M=M, N=N, K=K), True, "silu", True, True, 4, what=f"prime {N}")
+
+
+@pytest.mark.parametrize("forced", ["16,32,1,2,6,1,1,0", "64,64,2,2,4,2,1,0", "128,128,2,2,2,1,1,6", "256,256,4,2,2,1,1,6"])
+def test_capacity_far_above_the_rows_in_use(monkeypatch, forced):
+    """M as a capacity: the row blocks past the last segment (more than one look at 64 of them covers), or all of
+    them, name no expert, and their rows stay untouched."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", forced)
+    for rows in ([100, 0, 130], [0, 0, 1], [0, 0, 0]):
+        p = gen.make_bf16("contiguous", seed=13, N=96, K=256, group_rows=rows, pad_rows=128 * 20)
+        p.A[p.m_indices < 0] = float("nan")
+        _check(p, True, "silu", True, True, 14, what=f"{forced} {rows}")
+    if forced.startswith("16,"):
+        return
+    m = torch.tensor([2] * 70 + [-1] * 58 + [1] * 128 + [-2] * 128 * 70, dtype=torch.int32)
+    A, B = _bf((len(m), 128), 1), _bf((3, 128, 64), 2)
+    A[m < 0] = float("nan")
+    D = torch.full((len(m), 64), float("inf"), dtype=torch.bfloat16, device="cuda")
+    dg.dg_m_grouped_bf16_gemm_nn_contiguous(A.cuda(), B.cuda(), m.cuda(), None, D)
+    keep = m >= 0
+    _close(D.cpu()[keep], np.stack([A[r].double().numpy() @ B[int(m[r])].double().numpy() for r in torch.nonzero(keep)[:, 0].tolist()]), "capacity")
+    assert torch.isinf(D.cpu()[~keep].float()).all()
