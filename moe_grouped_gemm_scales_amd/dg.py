@@ -1021,11 +1021,14 @@ def dg_m_grouped_fp8_gemm_nt_masked_epilogue(A, sfa, B, sfb, masked_m, D, bias=N
     return D
 
 
-def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=None):
+def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=None, num_experts=None):
     """dZ = dD * activation'(Z) and dbias = its column sums (either may be None).
 
     dD, Z, dZ bfloat16 [M,N] (Z None without an activation), dbias float32 [N]; with m_indices int32 [M]
-    (contiguous layout) dbias is [G,N], and dZ of padding rows is cleared."""
+    (contiguous layout) dbias is [G,N], dZ of rows with index -1 is cleared, and rows with another index
+    outside [0, G) are untouched.  G is num_experts, which dbias need not be given for; with neither, G is
+    not known here and every index that is not negative counts as an expert's: rows may then be marked as
+    padding by negative indices only (as dg_moe_sort_contiguous marks them)."""
     if dD.dim() != 2:
         raise ValueError("dD must be [M, N]")
     shape, act, dev = dD.shape, _activation(activation), _on(dD, "dD")
@@ -1038,8 +1041,8 @@ def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=No
         status = lib.dg_epilogue_backward(*args, dz, _opt(dbias, "dbias", _F32, (N,), dev), M, N,
                                           _raw_stream(stream, dev))
     else:
-        # without a bias any row that names an expert is one
-        G = 65535 if dbias is None else dbias.shape[0]
+        # (65535: the most that the library takes)
+        G = num_experts if num_experts is not None else 65535 if dbias is None else dbias.shape[0]
         status = lib.dg_m_grouped_epilogue_backward_contiguous(
             *args, _arg(m_indices, "m_indices", _I32, (M,), dev), dz, _opt(dbias, "dbias", _F32, (G, N), dev), M, N, G,
             _raw_stream(stream, dev))
