@@ -240,11 +240,12 @@ dg_moe_place_kernel(const SortArgs a) {
     const int share = rows / blocks + 1;
     const int r0 = b * share < rows ? b * share : rows;
     const int r1 = rows - r0 < share ? rows : r0 + share;
-    for (int r = r0 + tid; r < r1; r += kSortThreads) {
+    // (unsigned: rows may be up to 2^31 - 128, and a thread's last step passes 2^31)
+    for (u32 r = (u32)r0 + (u32)tid; r < (u32)r1; r += kSortThreads) {
         int lo = 0;
         for (int half = 1 << bits >> 1; half > 0; half >>= 1)
-            if (lo + half < G && base[lo + half] <= (u32)r) lo += half;
-        const u32 in = (u32)r - base[lo], cnt = total[lo];
+            if (lo + half < G && base[lo + half] <= r) lo += half;
+        const u32 in = r - base[lo], cnt = total[lo];
         m_indices[r] = in < cnt ? lo : in < (cnt + kAlign - 1) / kAlign * kAlign ? kPadding : kUnused;
     }
 }
