@@ -9,8 +9,11 @@
 // The calls of a decode step run for a few microseconds on the GPU, and the same
 // attribute reads in Python take about 0.5 us a tensor (here about 0.1), so that
 // a call with five tensors waited for its checks.  Nothing is kept of a tensor.
+// torch_version names the torch that it was compiled against: the binding makes the
+// checks in Python where that is not the running one, or where this is not built.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <Python.h>
 
@@ -83,4 +86,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycheck", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pycheck() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__pycheck() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}
