@@ -43,18 +43,23 @@ class MoELayer:
         self.b1 = torch.randn((experts, inner), generator=g, device=device) * 0.1
         self.b2 = torch.randn((experts, hidden), generator=g, device=device) * 0.1
         rows = dg.moe_sorted_rows(tokens, topk, experts)
-        # cleared once: the products leave padding rows untouched, and the weight gradients read them
+        # the products leave rows that they do not compute as they are, so a new buffer is cleared
         buf = lambda width: torch.zeros((rows, width), dtype=BF16, device=device)
         self.rows, self.z1, self.h, self.out = buf(hidden), buf(inner), buf(inner), buf(hidden)
         self.d_out, self.dh, self.d_rows = buf(hidden), buf(inner), buf(hidden)
         self.m_indices = torch.empty(rows, dtype=torch.int32, device=device)
         self.ks = torch.empty(experts, dtype=torch.int32, device=device)
+        self.no_tokens = torch.empty((0, inner), dtype=BF16, device=device)
+        self.no_places = torch.empty((0, topk), dtype=torch.int32, device=device)
 
     def forward(self, x, ids, weights):
         self.x, self.weights = x, weights
         self.pos = torch.empty_like(ids)
         dg.dg_moe_sort_contiguous(ids, self.experts, self.pos, self.m_indices, self.ks)
         dg.dg_moe_dispatch_bf16(x, self.pos, self.m_indices, self.rows)
+        # a dispatch of no tokens clears the padding rows.  The gradient of w2 multiplies those of h by zeros, and
+        # an infinity or NaN that an earlier step left in one would come through that.
+        dg.dg_moe_dispatch_bf16(self.no_tokens, self.no_places, self.m_indices, self.h)
         dg.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(self.rows, self.w1, self.m_indices, self.h, bias=self.b1,
                                                          activation=self.act, Z=self.z1)
         dg.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(self.h, self.w2, self.m_indices, self.out, bias=self.b2)

@@ -407,8 +407,11 @@ dg_status dg_m_grouped_epilogue_backward_contiguous(const void *dD, const void *
  *       [G][M][N], an empty group gets C or zeros; K a multiple of 128.  A
  *       segment's padding rows are part of its sum: they must be zero in one
  *       operand (dispatch and the epilogue's backward pass clear them) and
- *       finite in the other (a product leaves them untouched, so clear a new
- *       buffer once); rows past the segments are not read
+ *       finite in the other.  A product leaves them untouched, so a buffer that
+ *       is used again holds what earlier calls with other segments wrote there,
+ *       an infinity or NaN of theirs too: clear them for each call
+ *       (dg_moe_dispatch_bf16 with T = 0 does that and no more).  Rows past the
+ *       segments are not read
  * The K-outermost operands are read as they are stored where their rows are
  * 16-byte aligned (N, for tn also M, a multiple of 8) and under 4 GiB (a group
  * of them); otherwise they are first rewritten K-contiguous into the stream's
@@ -444,7 +447,8 @@ dg_status dg_k_grouped_bf16_gemm_tn_contiguous(const void *A, const void *B, con
  * dg_moe_dispatch_*: rows_out[pos[t][j]] = X[t].  m_indices (contiguous layout;
  *   NULL for masked) names the rows: those with -1 are cleared (zeros, scale
  *   1), as a weight gradient over whole segments needs; all others that no
- *   token goes to are untouched.  pos outside [0, rows) is skipped.
+ *   token goes to are untouched.  pos outside [0, rows) is skipped.  T = 0:
+ *   the rows with -1 are cleared, in a buffer of any product's output too.
  *   bf16: rows_out BF16 [rows][H], any H.
  *   fp8: rows_out E4M3 [rows][H], H a multiple of 128, quantised with one scale
  *     per 1x128 block: s = amax / 448 (at least 2^-126; 1 for a block of zeros),
