@@ -1454,9 +1454,12 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
                     issue_one_aa(j, tl.kb0 + min(1, nst - 1), 1, nst > 1, tl.kb0, 0, false);
             } else if constexpr (SPLIT) {
                 // K blocks 0 .. STAGES-1 without the end group of the last (issued in the
-                // first steps of block 0); placeholders past the tile keep the counts fixed
+                // first steps of block 0); placeholders past the tile keep the counts fixed.
+                // An empty group (or split of one) has no K block that a placeholder could
+                // name: block kb0 - 1 may lie before the operand, kb0 past its end.
 #pragma unroll
                 for (int s = 0; s < STAGES; ++s) {
+                    if (KG && nst == 0) break;
 #pragma unroll
                     for (int j = 0; j < G_MID; ++j) issue_mid(j, tl.kb0 + min(s, nst - 1), s, s < nst);
                     if (s + 1 < STAGES) {
