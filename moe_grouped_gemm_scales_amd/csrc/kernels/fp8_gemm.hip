@@ -502,8 +502,13 @@ __device__ __forceinline__ Tile decode_tile(const Params& p, int t, int g_pre = 
         int off = 0;
         int len = p.kt;
         if (!BF16 || p.grp) {
-            for (int h = 0; h < g; ++h) off += p.grp[h] > 0 ? p.grp[h] : 0;
-            len = p.grp[g] > 0 ? p.grp[g] : 0;
+            // (a count is cut at the K rows that are left as it is added, so no sum passes 32 bits)
+            auto rows_of = [&](int h) {
+                const int k = p.grp[h], left = p.kt - off;
+                return k < 0 ? 0 : k < left ? k : left;
+            };
+            for (int h = 0; h < g; ++h) off += rows_of(h);
+            len = rows_of(g);
         }
         // (one BF16 group may end inside a K block: its rows past kt read as zeros)
         const int kbt = (p.kt + KROWS - 1) / KROWS;
