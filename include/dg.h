@@ -32,6 +32,7 @@
  *   - Calls are asynchronous on `stream` (a hipStream_t; NULL = default
  *     stream).  They never synchronise the host and never read device data
  *     (group indices, masks) on the host.
+ *   - M, M_max or T may be 0; an array without elements may then be NULL.
  *   - The library owns its compiled-kernel cache and a per-stream device
  *     workspace (split-K partials and arrival counters; the K-contiguous copies
  *     of K-outermost operands, a sort's counts, a bias gradient's partial sums),

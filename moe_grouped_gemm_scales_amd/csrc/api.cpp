@@ -227,9 +227,11 @@ dg_status ensure_kmajor(DeviceState& st, hipStream_t stream, size_t need, uint8_
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// (the row arrays of a call without rows have no elements and may be NULL, as torch's empty tensors are)
 dg_status check_common(const void* A, const void* sfa, const void* B, const void* sfb, const float* C,
                        const void* D, int rows, int N, int K, size_t sf_align = 4) {
-    if (!A || !sfa || !B || !sfb || !D) return set_error(DG_ERR_INVALID_ARG, "A, sfa, B, sfb and D must be non-NULL");
+    if ((rows != 0 && (!A || !sfa || !D)) || !B || !sfb)
+        return set_error(DG_ERR_INVALID_ARG, "A, sfa, B, sfb and D must be non-NULL");
     if (rows < 0 || N <= 0 || K <= 0)
         return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M may be 0)");
     if (K % 128 != 0) return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (the scale block)");
@@ -482,7 +484,7 @@ dg_status contiguous(const void* A, const void* sfa, const void* B, const void* 
                      int b_k_outer = 0, const Epilogue& ep = {}, const EpilogueArgs& args = {}) {
     dg_status s = check_common(A, sfa, B, sfb, C, D, M, N, K, sf == 5 ? 2 : 4);
     if (s != DG_OK) return s;
-    if (!m_indices) return set_error(DG_ERR_INVALID_ARG, "m_indices must be non-NULL");
+    if (!m_indices && M != 0) return set_error(DG_ERR_INVALID_ARG, "m_indices must be non-NULL");
     if (num_groups <= 0) return set_error(DG_ERR_INVALID_ARG, "num_groups must be positive");
     if (!aligned(m_indices, 4)) return set_error(DG_ERR_ALIGNMENT, "m_indices must be 4-byte aligned");
     if (M % dg_get_mk_alignment_for_contiguous_layout() != 0)
@@ -535,14 +537,15 @@ bool reads_k_outermost(int64_t cols, int64_t K) {
 dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, const float* C, void* D, int rows,
                     int N, int K, int num_groups, void* stream, int b_k_outer = 0, const Epilogue& ep = {},
                     const EpilogueArgs& args = {}) {
-    if (!A || !B || !D) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
+    if ((rows != 0 && (!A || !D)) || !B) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
     if (rows < 0 || N <= 0 || K <= 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M may be 0)");
     if (K % 64 != 0) return set_error(DG_ERR_UNSUPPORTED, "BF16: K must be a multiple of 64 (one 128-byte block)");
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || (C && !aligned(C, 16)))
         return set_error(DG_ERR_ALIGNMENT, "A, B, C and D must be 16-byte aligned");
     if ((uint64_t)K * 2u * 256u >= (1ull << 32)) return set_error(DG_ERR_UNSUPPORTED, "sizes exceed 32-bit buffer offsets");
     if (kind != kDense) {
-        if (!grp) return set_error(DG_ERR_INVALID_ARG, "m_indices / masked_m must be non-NULL");
+        if (!grp && (rows != 0 || kind == kMasked))
+            return set_error(DG_ERR_INVALID_ARG, "m_indices / masked_m must be non-NULL");
         if (num_groups <= 0) return set_error(DG_ERR_INVALID_ARG, "num_groups must be positive");
         if (!aligned(grp, 4)) return set_error(DG_ERR_ALIGNMENT, "m_indices / masked_m must be 4-byte aligned");
     }
@@ -569,7 +572,8 @@ Problem tn_problem(int M, int N, int K, int num_groups, int has_c) {
 // BF16 TN (A [K][M], B [K][N]): K-grouped, or one group of any K (ks NULL)
 dg_status bf16_gemm_tn(const void* A, const void* B, const int32_t* ks, const float* C, void* D, int M, int N, int K,
                        int num_groups, void* stream) {
-    if ((K != 0 && (!A || !B)) || !D) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
+    if ((K != 0 && ((M != 0 && !A) || !B)) || (M != 0 && !D))
+        return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
     if (M < 0 || N <= 0 || K < 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M and K may be 0)");
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || (C && !aligned(C, 16)))
         return set_error(DG_ERR_ALIGNMENT, "A, B, C and D must be 16-byte aligned");
