@@ -389,6 +389,7 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue(const void *A, const in
  * cleared, as the weight gradient over whole segments needs, other rows that
  * name no expert are untouched.  Then, with A and B as in the forward call,
  *   dA = dZ . B        dg_bf16_gemm_nn            dg_m_grouped_bf16_gemm_nn_contiguous
+ *                      (N not a multiple of 64, which is their K: the same names with _k_tail)
  *   dB = dZ^T . A      dg_bf16_gemm_tn            dg_k_grouped_bf16_gemm_tn_contiguous
  * The partial sums of dbias use the stream's workspace.
  */
@@ -401,7 +402,9 @@ dg_status dg_m_grouped_epilogue_backward_contiguous(const void *dD, const void *
 /*
  * BF16 products of the other storage layouts, D = C + (logical) A . B^T as for
  * the FP8 calls of the same letters, C float or NULL, D BF16:
- *   nn  A [M][K], B [K][N] (grouped [G][K][N]); K a multiple of 64
+ *   nn  A [M][K], B [K][N] (grouped [G][K][N]); K a multiple of 64, or with
+ *       _k_tail any K: where it is no multiple of 64, A and B are first copied
+ *       and rewritten with K filled up by zeros
  *   tn  A [K][M], B [K][N]; any K, 0 included (D = C, or zeros)
  *   k_grouped tn  A [K][M], B [K][N], ks int32 [G] (device): consecutive K
  *       segments of the groups, multiples of 128, as for the FP8 form; C, D
@@ -416,11 +419,17 @@ dg_status dg_m_grouped_epilogue_backward_contiguous(const void *dD, const void *
  * The K-outermost operands are read as they are stored where their rows are
  * 16-byte aligned (N, for tn also M, a multiple of 8) and under 4 GiB (a group
  * of them); otherwise they are first rewritten K-contiguous into the stream's
- * workspace: G * N * K * 2 bytes for nn, (M + N) * ceil(K/512) * 1024 for tn.
+ * workspace: G * N * K * 2 bytes for nn (a K tail: (M + G * N) * ceil(K/64) *
+ * 128), (M + N) * ceil(K/512) * 1024 for tn.
  */
 dg_status dg_bf16_gemm_nn(const void *A, const void *B, const float *C, void *D, int M, int N, int K, void *stream);
 dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void *A, const void *B, const int32_t *m_indices, const float *C,
                                                void *D, int M, int N, int K, int num_groups, void *stream);
+dg_status dg_bf16_gemm_nn_k_tail(const void *A, const void *B, const float *C, void *D, int M, int N, int K,
+                                 void *stream);
+dg_status dg_m_grouped_bf16_gemm_nn_contiguous_k_tail(const void *A, const void *B, const int32_t *m_indices,
+                                                      const float *C, void *D, int M, int N, int K, int num_groups,
+                                                      void *stream);
 dg_status dg_bf16_gemm_tn(const void *A, const void *B, const float *C, void *D, int M, int N, int K, void *stream);
 dg_status dg_k_grouped_bf16_gemm_tn_contiguous(const void *A, const void *B, const int32_t *ks, const float *C, void *D,
                                                int M, int N, int K, int num_groups, void *stream);

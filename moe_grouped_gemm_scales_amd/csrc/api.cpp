@@ -354,7 +354,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     auto rewrite_k_major = [&](const void* x, void* xt, int rows_k, int cols, int groups) -> dg_status {
         if (p.sf == 3) {       // BF16: K in elements; K-grouped K is padded with zeros to whole K blocks
             const bool kg = p.kind == kKGrouped;
-            const int k = kg ? p.kt : rows_k / 2;
+            const int k = kg ? p.kt : p.k_tail ? p.k_tail : rows_k / 2;
             return transpose_bf16(x, xt, groups, k, cols, (k + 63) / 64 * 64, p.k / 2, stream_ptr);
         }
         const uint64_t blocks = (uint64_t)(rows_k / 64) * (uint64_t)((cols + 63) / 64);
@@ -367,15 +367,21 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
         return e == hipSuccess ? DG_OK : hip_fail(e, "hipModuleLaunchKernel(transpose)");
     };
     // TN / NN / TT layouts: the K-outermost operand(s) rewritten K-contiguous in the
-    // stream's workspace, then the NT kernels run on them
+    // stream's workspace, then the NT kernels run on them (an A whose rows end inside a
+    // K block is copied there too, its last block filled up with zeros)
     if (rewrite && p.kind != kKGrouped) {
-        const size_t a_bytes = p.a_k_outer ? (size_t)p.rows * (size_t)p.k : 0;
+        const size_t a_bytes = p.a_k_outer || p.k_tail ? (size_t)p.rows * (size_t)p.k : 0;
         const size_t b_bytes = p.b_k_outer ? (size_t)p.g * (size_t)p.n * (size_t)p.k : 0;
         uint8_t* buf = nullptr;
         s = ensure_kmajor(*st, stream, a_bytes + b_bytes, &buf);
         if (s != DG_OK) return s;
         if (p.a_k_outer) {
             s = rewrite_k_major(A, buf, p.k, p.rows, 1);
+            if (s != DG_OK) return s;
+            A = buf;
+        }
+        if (p.k_tail) {
+            s = pad_rows_bf16(A, buf, p.rows, p.k_tail, p.k / 2, stream_ptr);
             if (s != DG_OK) return s;
             A = buf;
         }
@@ -536,13 +542,15 @@ bool reads_k_outermost(int64_t cols, int64_t K) {
 // BF16 x BF16, the three M forms: no scales; the kernels count K in bytes
 dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, const float* C, void* D, int rows,
                     int N, int K, int num_groups, void* stream, int b_k_outer = 0, const Epilogue& ep = {},
-                    const EpilogueArgs& args = {}) {
+                    const EpilogueArgs& args = {}, bool any_k = false) {
     if ((rows != 0 && (!A || !D)) || !B) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
     if (rows < 0 || N <= 0 || K <= 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M may be 0)");
-    if (K % 64 != 0) return set_error(DG_ERR_UNSUPPORTED, "BF16: K must be a multiple of 64 (one 128-byte block)");
+    if (K % 64 != 0 && !any_k)
+        return set_error(DG_ERR_UNSUPPORTED, "BF16: K must be a multiple of 64 (one 128-byte block)");
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || (C && !aligned(C, 16)))
         return set_error(DG_ERR_ALIGNMENT, "A, B, C and D must be 16-byte aligned");
-    if ((uint64_t)K * 2u * 256u >= (1ull << 32)) return set_error(DG_ERR_UNSUPPORTED, "sizes exceed 32-bit buffer offsets");
+    const int64_t whole = ((int64_t)K + 63) / 64 * 64;
+    if ((uint64_t)whole * 2u * 256u >= (1ull << 32)) return set_error(DG_ERR_UNSUPPORTED, "sizes exceed 32-bit buffer offsets");
     if (kind != kDense) {
         if (!grp && (rows != 0 || kind == kMasked))
             return set_error(DG_ERR_INVALID_ARG, "m_indices / masked_m must be non-NULL");
@@ -552,9 +560,10 @@ dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, 
     if (kind == kContiguous && rows % dg_get_mk_alignment_for_contiguous_layout() != 0)
         return set_error(DG_ERR_ALIGNMENT, "contiguous M must be a multiple of the M alignment (128)");
     if (rows == 0) return DG_OK;
-    Problem p{kind, rows, N, 2 * K, kind == kDense ? 1 : num_groups, C ? 1 : 0, 3};
+    Problem p{kind, rows, N, 2 * (int)whole, kind == kDense ? 1 : num_groups, C ? 1 : 0, 3};
     p.b_k_outer = b_k_outer;
-    p.direct = b_k_outer && reads_k_outermost(N, K);
+    p.k_tail = K % 64 ? K : 0;
+    p.direct = b_k_outer && !p.k_tail && reads_k_outermost(N, K);
     p.ep = ep;
     return launch(p, A, nullptr, B, nullptr, grp, C, D, stream, false, args);
 }
@@ -676,7 +685,7 @@ Epilogue epilogue_flags(int* kind) {
 
 // the kernels' K: BF16 rows are counted in bytes; K-grouped operands use the padded pitch
 int kernel_k(int kind, int sf, int K) {
-    if (sf == 3) return 2 * K;
+    if (sf == 3) return 2 * ((K + 63) / 64 * 64);
     return kind == kKGrouped ? k_grouped_pitch(K) : K;
 }
 
@@ -689,13 +698,14 @@ dg_status described_problem(int kind, int rows, int N, int K, int num_groups, in
     if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH ||
         (nn && sf != 3))
         return set_error(DG_ERR_INVALID_ARG, "bad arguments");
-    if (K % (sf != 3 ? 128 : kind == kKGrouped ? 1 : 64))
+    if (K % (sf != 3 ? 128 : kind == kKGrouped || nn ? 1 : 64))
         return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
     if (kind == kKGrouped && sf == 3) *p = tn_problem(rows, N, K, num_groups, has_c ? 1 : 0);
     else *p = Problem{kind, rows, N, kernel_k(kind, sf, K), kind == kDense ? 1 : num_groups, has_c ? 1 : 0, sf};
     if (nn) {
         p->b_k_outer = 1;
-        p->direct = reads_k_outermost(N, K);
+        p->k_tail = K % 64 ? K : 0;
+        p->direct = !p->k_tail && reads_k_outermost(N, K);
     }
     p->ep = ep;
     return DG_OK;
@@ -982,6 +992,20 @@ dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void* A, const void* B, con
                                                void* D, int M, int N, int K, int num_groups, void* stream) {
     return guarded([&]() -> dg_status {
         return bf16_gemm(kContiguous, A, B, m_indices, C, D, M, N, K, num_groups, stream, 1);
+    });
+}
+
+dg_status dg_bf16_gemm_nn_k_tail(const void* A, const void* B, const float* C, void* D, int M, int N, int K, void* stream) {
+    return guarded([&]() -> dg_status {
+        return bf16_gemm(kDense, A, B, nullptr, C, D, M, N, K, 1, stream, 1, {}, {}, true);
+    });
+}
+
+dg_status dg_m_grouped_bf16_gemm_nn_contiguous_k_tail(const void* A, const void* B, const int32_t* m_indices,
+                                                      const float* C, void* D, int M, int N, int K, int num_groups,
+                                                      void* stream) {
+    return guarded([&]() -> dg_status {
+        return bf16_gemm(kContiguous, A, B, m_indices, C, D, M, N, K, num_groups, stream, 1, {}, {}, true);
     });
 }
 

@@ -107,6 +107,7 @@ struct Problem {
     int kt = 0;    // K-grouped: K rows of the operands (n, k above: N and the padded pitch)
     int a_k_outer = 0, b_k_outer = 0;   // A stored [K][rows] (T), B stored [(G)][K][N] (N)
     int direct = 0;   // BF16: the K-outermost operands are read as stored, without a rewrite
+    int k_tail = 0;   // BF16 NN whose K ends inside a 128-byte block: that K (k above: padded to whole blocks)
     Epilogue ep;
 };
 
@@ -144,6 +145,8 @@ inline int k_grouped_pitch(int k) { return (k + 1023) / 1024 * 1024; }
 // (elements); columns [rows_k, k_end) of Xt are zeros (linear.hip)
 dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int cols, int k_end, int64_t pitch,
                          void* stream);
+// BF16 X [rows][cols] copied to rows of `pitch` elements (a multiple of 8), the rest zeros (linear.hip)
+dg_status pad_rows_bf16(const void* x, void* xp, int rows, int cols, int pitch, void* stream);
 std::string cache_dir();
 
 // Device address of the library's status words on the current device

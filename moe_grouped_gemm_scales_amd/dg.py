@@ -130,6 +130,8 @@ def _load():
                        ("dg_epilogue_backward", [vp, vp, i32, vp, vp, i32, i32, vp]),
                        ("dg_m_grouped_epilogue_backward_contiguous", [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp]),
                        ("dg_bf16_gemm_nn", [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_bf16_gemm_nn_k_tail", [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_m_grouped_bf16_gemm_nn_contiguous_k_tail", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_bf16_gemm_tn", [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_m_grouped_bf16_gemm_nn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_k_grouped_bf16_gemm_tn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
@@ -1071,24 +1073,24 @@ def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=No
 
 # ---------------------------------------------------------------- BF16 products of the backward pass
 def dg_bf16_gemm_nn(A, B, C, D, stream=None):
-    """D = C + A @ B with A [M,K], B [K,N] bfloat16, C None or float32 [M,N]."""
+    """D = C + A @ B with A [M,K], B [K,N] bfloat16 (any K), C None or float32 [M,N]."""
     M, K = A.shape
     N = B.shape[1]
     dev = _on(A, "A")
-    status = lib.dg_bf16_gemm_nn(_arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (K, N), dev),
-                                 _opt(C, "C", _F32, (M, N), dev), _arg(D, "D", _BF, (M, N), dev), M, N, K,
-                                 _raw_stream(stream, dev))
+    status = (lib.dg_bf16_gemm_nn_k_tail if K % 64 else lib.dg_bf16_gemm_nn)(
+        _arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (K, N), dev), _opt(C, "C", _F32, (M, N), dev),
+        _arg(D, "D", _BF, (M, N), dev), M, N, K, _raw_stream(stream, dev))
     if status:
         _check(status)
     return D
 
 
 def dg_m_grouped_bf16_gemm_nn_contiguous(A, B, m_indices, C, D, stream=None):
-    """Contiguous M-grouped: row m of D is C[m] + A[m] @ B[m_indices[m]], B [G,K,N]."""
+    """Contiguous M-grouped: row m of D is C[m] + A[m] @ B[m_indices[m]], B [G,K,N], any K."""
     M, K = A.shape
     G, N = B.shape[0], B.shape[2]
     dev = _on(A, "A")
-    status = lib.dg_m_grouped_bf16_gemm_nn_contiguous(
+    status = (lib.dg_m_grouped_bf16_gemm_nn_contiguous_k_tail if K % 64 else lib.dg_m_grouped_bf16_gemm_nn_contiguous)(
         _arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (G, K, N), dev), _arg(m_indices, "m_indices", _I32, (M,), dev),
         _opt(C, "C", _F32, (M, N), dev), _arg(D, "D", _BF, (M, N), dev), M, N, K, G, _raw_stream(stream, dev))
     if status:
