@@ -255,7 +255,9 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     const bool rewrite = !p.direct && (p.kind == kKGrouped || p.a_k_outer || p.b_k_outer);
     // what the sizes do not say about the kernels
-    const int extra = p.ep.code() * 2 + p.direct + (p.sf == 3 && p.kind == kKGrouped ? k_share(p.kt) << 12 : 0);
+    // (a BF16 B that is rewritten first runs on the kernels of the NT form, but chooses them otherwise)
+    const int extra = p.ep.code() * 2 + p.direct + (p.sf == 3 && p.b_k_outer ? 1 << 11 : 0) +
+                      (p.sf == 3 && p.kind == kKGrouped ? k_share(p.kt) << 12 : 0);
     // ---- warm call: the previous call of this thread had the same key
     int dev_now = 0;
     if (hipGetDevice(&dev_now) != hipSuccess) dev_now = -1;
