@@ -122,8 +122,10 @@ bool valid(const KernelConfig& c, const Problem& p) {
     auto kout_tile = [](int t, int w) { return (t == 64 || t == 128 || t == 256) && ((t / w) & (t / w - 1)) == 0; };
     if (c.b_kout && (!kout_tile(c.bn, c.wn) || p.n % 8 || (c.variant != 0 && c.variant != 6) || c.kstep != 1)) return false;
     if (c.a_kout && (!kout_tile(c.bm, c.wm) || p.rows % 8)) return false;
-    // split-K: not where a row block makes two passes, and K-grouped in BF16 only
-    if (c.splitk < 1 || (c.splitk > 1 && ((p.kind == kContiguous && c.bm > 128) || (p.kind == kKGrouped && p.sf != 3))))
+    // split-K: not where a row block makes two passes, K-grouped in BF16 only, and of the grouped
+    // forms in variants 0 and 6 only
+    if (c.splitk < 1 || (c.splitk > 1 && ((p.kind == kContiguous && c.bm > 128) || (p.kind == kKGrouped && p.sf != 3) ||
+                                          (p.kind != kDense && c.variant != 0 && c.variant != 6))))
         return false;
     if (c.sf != p.sf) return false;
     // variant 4: variant 0 with A requested a K block ahead of B (two B slots, three A
