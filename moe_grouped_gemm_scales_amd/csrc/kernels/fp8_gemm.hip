@@ -886,8 +886,9 @@ __device__ __forceinline__ void finish_tile(const Params& p, const Tile& tl, v4f
         const int r = row0 + a * 16;            // row inside the tile
         bool row_ok = r < tl.row_limit;
         if constexpr (kKind == 1) {
+            // (the last 256-row block may have 128 rows: its lanes past them read no index of their own)
             const int gr = GRP_LDS ? *(__attribute__((address_space(3))) const int*)(grp_lds + a * 64)
-                                   : p.grp[tl.m0 + r];
+                                   : p.grp[tl.m0 + (row_ok ? r : 0)];
             row_ok = row_ok && gr == tl.g;
         }
         if (!row_ok) continue;
