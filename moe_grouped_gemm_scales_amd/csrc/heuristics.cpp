@@ -302,12 +302,21 @@ std::vector<KernelConfig> tuned(const Problem& p, int num_cus, const KernelConfi
 // without split-K for the grouped and TN forms and with one tile a CU: 7.7 %).  What decides,
 // measured (the general model's choice in brackets): 64 x 4096 x 7168 BF16 16.8 us
 // (28.6); 1024 x 4096 x 4096 39.7 (48.2); masked 8 x 256 x 2048 x 4096 FP8 33.0 (53.5);
-// 4 experts' 8704 x 4096 x 7168 FP8 250 as 128 x 128, whose 2176 tiles leave 6 % of the last
-// round idle, against 323 as 256 x 256 (544 tiles, 29 % idle), where 8192 x 4096 x 7168
+// 4 experts' 8704 x 4096 x 7168 FP8 267 as 128 x 128, whose 2176 tiles leave 6 % of the last
+// round idle, against 343 as 256 x 256 (544 tiles, 29 % idle), where 8192 x 4096 x 7168
 // BF16 (512 tiles) runs 348 as 256 x 256 and over 430 as 128 x 128.  Split against
 // unsplit: TN 512 x 512 over K 16384 21 us against 65, TN 1600 x 1408 over 6721 45 against
 // 56, masked 4 x 64 x 2048 x 7168 FP8 17.0 against 25.5, masked 2 x 447 x 1152 x 6528 BF16
 // 17.4 against 24.9, contiguous 2 experts' 256 x 1600 x 4352 FP8 11.7 against 13.9.
+//
+// Contiguous rows in 256-row tiles: an expert that ends inside a tile (every second one does, of
+// random lengths) has it computed twice, which lengthens that CU's round.  It adds 0.25 + 0.065
+// (experts - 1) rounds, whatever the rows and columns: measured over 40 shapes of 8192 to 65536
+// rows in 4 to 32 experts of random lengths, where a choice with it takes 0.3 % longer than the best of
+// 256 x 256, 128 x 256 and 128 x 128 (half a row block an expert, rounded up to whole rounds: 1.1 %).
+// us, 256 x 256 and 128 x 256: FP8 32768 x 4096 x 7168 in 4 experts 862 and 977 (ending at
+// multiples of 256 rows 823 and 996), in 8 891 and 987, in 32 1060 and 1022; 8192 rows in 4
+// 241 and 226; BF16 32768 x 4096 x 4096 in 8 877 and 929, in 32 1058 and 974.
 struct Structure {
     int bm, bn, wm, wn, stages, variant;
     int per_cu;                    // tiles a CU works on at a time
@@ -315,7 +324,7 @@ struct Structure {
     double us_full_bf16, us_full_fp8;
 };
 const Structure kStructures[] = {
-    {256, 256, 4, 2, 2, 6, 1, 1.37, 1.64, 0, 0},       {128, 256, 2, 4, 3, 0, 1, 0.80, 0.89, 0, 0},
+    {256, 256, 4, 2, 2, 6, 1, 1.37, 1.64, 0, 0},       {128, 256, 2, 4, 3, 0, 1, 0.80, 0.92, 0, 0},
     {128, 192, 2, 4, 3, 0, 1, 0.75, 0.82, 0, 0},       {192, 128, 4, 2, 3, 0, 1, 0.64, 0.74, 0, 0},
     {128, 128, 4, 2, 4, 0, 1, 0.51, 0.54, 0, 0},       {128, 128, 2, 2, 2, 6, 2, 0.64, 0.64, 0.49, 0.49},
     {128, 64, 4, 2, 4, 0, 1, 0.33, 0.41, 0, 0},        {64, 128, 2, 4, 4, 0, 1, 0.34, 0.41, 0, 0},
@@ -333,8 +342,6 @@ std::vector<KernelConfig> choose_structure(const Problem& p, int num_cus, const 
     auto row_blocks = [&](int bm, double valid_rows) {
         if (p.kind == kMasked)
             return std::min((double)((p.rows + bm - 1) / bm), valid_rows * p.rows / bm + 0.5) * p.g;
-        // a 256-row block of two experts is computed for each: about half of the segments' ends
-        if (p.kind == kContiguous && bm > 128) return (double)((p.rows + bm - 1) / bm) + 0.5 * (p.g - 1);
         return (double)((p.rows + bm - 1) / bm) * (p.kind == kKGrouped ? p.g : 1);
     };
     // rows of the output, for a split's partials
@@ -361,8 +368,8 @@ std::vector<KernelConfig> choose_structure(const Problem& p, int num_cus, const 
             const double blocks = std::ceil(kb / sk);
             auto time_of = [&](double items) {
                 double per_cu = std::max(1.0, std::ceil(items / num_cus - 1e-9));
-                if (p.kind == kContiguous && st.bm > 128 && p.g > 1) per_cu = std::max(per_cu, 2.0);   // (some CU has such a block)
-                const double batches = std::ceil(per_cu / st.per_cu);
+                double batches = std::ceil(per_cu / st.per_cu);
+                if (p.kind == kContiguous && st.bm > 128 && p.g > 1) batches += 0.25 + 0.065 * (p.g - 1);
                 if (st.per_cu == 1) return batches * (start + blocks * us);
                 return start * (1 + 1.5 * (batches - 1)) + blocks * std::max(batches * us, per_cu * us_full);
             };
