@@ -287,7 +287,7 @@ dg_status dg_k_grouped_fp8_gemm_tn_contiguous(const void *A, const float *sfa, c
  * contiguous A [M][K], B [G][N][K], m_indices [M]; masked A [G][M_max][K],
  * B [G][N][K], masked_m [G]; C float like D or NULL.  K must be a multiple of
  * 64 (one 128-byte block; reading, the pages give no rule), M of the
- * contiguous form a multiple of 128.  Ownership, streams, group and mask rules
+ * contiguous form a multiple of 128 below 2^30.  Ownership, streams, group and mask rules
  * and errors as for the FP8 forms.
  */
 dg_status dg_bf16_gemm_nt(const void *A, const void *B, const float *C, void *D, int M, int N, int K,

@@ -561,6 +561,9 @@ dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, 
     }
     if (kind == kContiguous && rows % dg_get_mk_alignment_for_contiguous_layout() != 0)
         return set_error(DG_ERR_ALIGNMENT, "contiguous M must be a multiple of the M alignment (128)");
+    // (m_indices is one buffer of 32-bit offsets)
+    if (kind == kContiguous && (uint64_t)rows * 4u >= (1ull << 32))
+        return set_error(DG_ERR_UNSUPPORTED, "contiguous M must be below 2^30");
     if (rows == 0) return DG_OK;
     Problem p{kind, rows, N, 2 * (int)whole, kind == kDense ? 1 : num_groups, C ? 1 : 0, 3};
     p.b_k_outer = b_k_outer;
