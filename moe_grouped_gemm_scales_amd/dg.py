@@ -774,10 +774,18 @@ def _raw_stream(stream, dev: int) -> int:
 
 
 _BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_INT_MAX = 2 ** 31 - 1
+
+
+def _too_many(name: str, n: int):
+    # (ctypes would pass such a size on modulo 2^32)
+    raise ValueError(f"{name}: {n} is more than the library's sizes hold (2^31 - 1)")
 
 
 def moe_sorted_rows(T: int, topk: int, num_experts: int) -> int:
     """Rows of the contiguous layout that hold T tokens' topk assignments whatever experts they choose."""
+    if max(T, topk, num_experts) > _INT_MAX:
+        _too_many("T, topk and num_experts", max(T, topk, num_experts))
     n = int(lib.dg_moe_sorted_rows(T, topk, num_experts))
     if n < 0:
         raise ValueError("T must not be negative, topk and num_experts must be positive")
@@ -789,6 +797,8 @@ def _ids(expert_ids):
         raise TypeError(f"expert_ids must be int32, got {expert_ids.dtype}")
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be int32 [T, topk]")
+    if expert_ids.numel() > _INT_MAX:
+        _too_many("expert_ids", expert_ids.numel())
     return expert_ids.shape
 
 
@@ -801,6 +811,8 @@ def dg_moe_sort_contiguous(expert_ids, num_experts, pos, m_indices, ks, stream=N
     shape = _ids(expert_ids)
     dev = _on(expert_ids, "expert_ids")
     rows = m_indices.numel()
+    if rows > _INT_MAX:
+        _too_many("rows of m_indices", rows)
     status = lib.dg_moe_sort_contiguous(
         _arg(expert_ids, "expert_ids", _I32, shape, dev), _arg(pos, "pos", _I32, shape, dev),
         _arg(m_indices, "m_indices", _I32, (rows,), dev), _arg(ks, "ks", _I32, (num_experts,), dev), shape[0], shape[1],
@@ -813,6 +825,8 @@ def dg_moe_sort_contiguous(expert_ids, num_experts, pos, m_indices, ks, stream=N
 def dg_moe_sort_masked(expert_ids, num_experts, M_max, pos, masked_m, stream=None):
     """Sort the assignments by expert into the masked layout: expert g's rows start at g * M_max."""
     shape = _ids(expert_ids)
+    if M_max > _INT_MAX:
+        _too_many("M_max", M_max)
     dev = _on(expert_ids, "expert_ids")
     status = lib.dg_moe_sort_masked(
         _arg(expert_ids, "expert_ids", _I32, shape, dev), _arg(pos, "pos", _I32, shape, dev),
@@ -831,7 +845,10 @@ def _token_rows(X, name, pos, rows, rows_name="rows"):
     T, width = X.shape
     if shape[-1] != width:
         raise ValueError(f"{rows_name} must be {width} wide like {name}, got {tuple(shape)}")
-    return T, pos.shape[1], shape[0] if len(shape) == 2 else shape[0] * shape[1], width, shape
+    n = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    if n > _INT_MAX or T > _INT_MAX or width > _INT_MAX:
+        _too_many(f"rows of {name} or {rows_name}", max(T, n, width))
+    return T, pos.shape[1], n, width, shape
 
 
 def dg_moe_dispatch_bf16(X, pos, m_indices, rows, stream=None):
@@ -1051,8 +1068,10 @@ def dg_epilogue_backward(dD, Z, activation, dZ, dbias, m_indices=None, stream=No
     padding by negative indices only (as dg_moe_sort_contiguous marks them)."""
     if dD.dim() != 2:
         raise ValueError("dD must be [M, N]")
-    shape, act, dev = dD.shape, _activation(activation), _on(dD, "dD")
-    M, N = shape
+    shape = M, N = dD.shape
+    if M > _INT_MAX or N > _INT_MAX:
+        _too_many("rows of dD", max(M, N))
+    act, dev = _activation(activation), _on(dD, "dD")
     if act and Z is None:
         raise ValueError("Z is needed with an activation")
     args = (_arg(dD, "dD", _BF, shape, dev), _arg(Z, "Z", _BF, shape, dev) if act else None, act)
