@@ -421,6 +421,13 @@ dg_status dg_m_grouped_epilogue_backward_contiguous(const void *dD, const void *
  * of them); otherwise they are first rewritten K-contiguous into the stream's
  * workspace: G * N * K * 2 bytes for nn (a K tail: (M + G * N) * ceil(K/64) *
  * 128), (M + N) * ceil(K/512) * 1024 for tn.
+ * K of the tn forms is the number of tokens, which changes from call to call.
+ * The kernel is chosen by K (per eighth of an octave; where the operands are
+ * rewritten first also per 512 of K, their row pitch): the first call in a range
+ * of K compiles or loads its kernel, and may allocate split-K workspace, in a
+ * few tenths of a second.  A caller that times or captures such calls first runs
+ * one of each K range that it will meet on that stream (dg_describe_config names
+ * the kernel of each K; dg_precompile moves the compile out of the run).
  */
 dg_status dg_bf16_gemm_nn(const void *A, const void *B, const float *C, void *D, int M, int N, int K, void *stream);
 dg_status dg_m_grouped_bf16_gemm_nn_contiguous(const void *A, const void *B, const int32_t *m_indices, const float *C,

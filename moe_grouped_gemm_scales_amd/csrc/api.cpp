@@ -574,7 +574,9 @@ dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, 
 }
 
 // The problem of a BF16 TN product.  Read as stored, K is no constant of the
-// kernel: one serves every token count.
+// kernel, but the tile and the split of K are chosen by K's share (k_share), so a range of
+// token counts runs on a few kernels: 512 x 512 over K 128 to 32768 on five (64 x 64 tiles
+// split 1 to 4 times, 64 x 128 eight times), 4096 x 7168 on two.
 Problem tn_problem(int M, int N, int K, int num_groups, int has_c) {
     const bool direct = reads_k_outermost(M, K) && reads_k_outermost(N, K);
     Problem p{kKGrouped, M, N, direct ? 1024 : std::max(1024, k_grouped_pitch(2 * K)), num_groups, has_c, 3};
