@@ -35,7 +35,7 @@
  *   - M, M_max or T may be 0; an array without elements may then be NULL.
  *   - The library owns its compiled-kernel cache and a per-stream device
  *     workspace (split-K partials and arrival counters; the K-contiguous copies
- *     of K-outermost operands, a sort's counts, a bias gradient's partial sums),
+ *     of K-outermost operands, a sort's counts, a bias or weight gradient's partial sums),
  *     created on first use (or by dg_init) and kept until process exit.  The
  *     first call for a new shape compiles a kernel (hipRTC) and may allocate;
  *     later calls with the same shape neither compile nor allocate.  Host
@@ -46,7 +46,7 @@
  *     Two graphs that captured calls on the same stream share its workspace
  *     too, so they must not be replayed concurrently (on other streams) when
  *     their calls use it: split-K (few rows, long K), a K-contiguous rewrite, a
- *     sort of more than 4096 assignments, a bias gradient.  That races on what
+ *     sort of more than 4096 assignments, a bias gradient, a norm's weight gradient.  That races on what
  *     they keep there and is unsupported.
  *     A call that compiles or allocates cannot run under stream capture: make
  *     the first call of each shape on each stream eagerly, then capture.
@@ -505,6 +505,50 @@ dg_status dg_moe_combine(const void *rows_in, const int32_t *pos, const float *w
 dg_status dg_moe_combine_backward(const void *dY, const void *rows_in, const int32_t *pos, const float *weights,
                                   const int32_t *m_indices, void *d_rows, float *d_weights, int T, int topk,
                                   int rows, int N, void *stream);
+
+/*
+ * Root-mean-square norm of BF16 rows X [T][H], with the residual's addition in
+ * front of it and the operand of an FP8 product behind it:
+ *
+ *     s = X + residual,  y = s * weight / sqrt(mean over H of s^2 + eps)
+ *
+ * in FP32 from the sum s on (y does not see S's rounding), each output rounded
+ * once.  residual, weight (1) and each output may be NULL, at least one output given:
+ *   weight  [H], FP32 or BF16 (weight_type)
+ *   S       BF16 [T][H]: s, the residual stream of the next layer; may be X or
+ *           residual itself
+ *   Y       BF16 [T][H]; may be X or residual where S is not the same
+ *   Q, sf   E4M3 [T][H], H a multiple of 128, with one scale per 1x128 block as
+ *           dg_moe_dispatch_fp8 makes them: A and sfa of the dense FP8 forms.
+ *           sf float [H/128][T]; ue8m0 != 0: int32 words [ceil(H/512)][T] of four
+ *           power-of-two scales
+ * A row that holds an infinity or NaN gives NaN in places of that row alone.
+ * The sum of squares is an FP32 number: rows with |s| of 1e19 and more
+ * overflow it and give zeros.  Any H up to 65536.
+ *
+ * dg_rms_norm_backward, with S the norm's input (X without a residual) and dY
+ * the gradient of y:
+ *   dX = gradient of s through the norm + dS    BF16 [T][H] (dX, and the residual's
+ *        gradient too; may be dY or dS itself, or NULL).  dS BF16 [T][H] or NULL: the
+ *        gradient that reaches S past the norm
+ *   dweight = sum over rows of dY * s / sqrt(...)   FP32 [H] or NULL, summed in an
+ *        order that does not change from run to run; 0 for T = 0
+ * The partial sums of dweight use the stream's workspace.
+ * X, residual, weight, S, Y, Q, dY, dS and dX must be 16-byte aligned, sf and
+ * dweight 4-byte.
+ */
+typedef struct {
+    const void *residual;   /* or NULL */
+    const void *weight;     /* or NULL */
+    int weight_type;        /* dg_type */
+    float eps;
+    void *S, *Y;            /* or NULL */
+    void *Q, *sf;           /* or NULL */
+    int ue8m0;
+} dg_norm;
+dg_status dg_rms_norm(const void *X, const dg_norm *norm, int T, int H, void *stream);
+dg_status dg_rms_norm_backward(const void *dY, const void *S, const void *weight, int weight_type, float eps,
+                               const void *dS, void *dX, float *dweight, int T, int H, void *stream);
 
 /*
  * Health of the current device's kernels.  The producer/consumer kernel

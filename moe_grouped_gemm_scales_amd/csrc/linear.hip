@@ -339,6 +339,13 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
 
 }  // namespace
 
+dg_status column_sums(const char* what, const float* partial, int chunks, int N, float* out, void* stream) {
+    if (!fits_launch((N + kSumCols - 1) / kSumCols, 64 * kSumWaves))
+        return set_error(DG_ERR_UNSUPPORTED, std::string(what) + ": too many columns for one launch");
+    return launch_rows(what, dg_bias_sum_kernel, dim3((N + kSumCols - 1) / kSumCols), 64 * kSumWaves, stream,
+                       BiasSumArgs{partial, nullptr, out, chunks, 1, N});
+}
+
 dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int cols, int k_end, int64_t pitch,
                          void* stream) {
     const int k_blocks = k_end / 64;

@@ -135,6 +135,8 @@ def _load():
                        ("dg_bf16_gemm_tn", [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_m_grouped_bf16_gemm_nn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_k_grouped_bf16_gemm_tn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
+                       ("dg_rms_norm", [vp] * 2 + [i32] * 2 + [vp]),
+                       ("dg_rms_norm_backward", [vp] * 3 + [i32, ctypes.c_float] + [vp] * 3 + [i32] * 2 + [vp]),
                        ("dg_moe_combine", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_moe_combine_backward", [vp] * 7 + [i32] * 4 + [vp])):
         getattr(lib, name).argtypes = args
@@ -1141,3 +1143,68 @@ def dg_k_grouped_bf16_gemm_tn_contiguous(A, B, ks, C, D, stream=None):
     if status:
         _check(status)
     return D
+
+
+# ---------------------------------------------------------------- norm
+class _Norm(ctypes.Structure):      # dg_norm
+    _fields_ = [("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("weight_type", ctypes.c_int),
+                ("eps", ctypes.c_float), ("S", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("Q", ctypes.c_void_p),
+                ("sf", ctypes.c_void_p), ("ue8m0", ctypes.c_int)]
+
+
+def _rows_of(t, name):
+    """(T, H) of the call's BF16 rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T, H]")
+    if max(t.shape) > _INT_MAX:
+        _too_many(f"rows of {name}", max(t.shape))
+    return t.shape
+
+
+def _weight(weight, H, dev):
+    """(address, dg_type) of a norm's weight."""
+    if weight is None:
+        return None, 0
+    wide = weight.dtype is not _F32
+    if wide and weight.dtype is not _BF:
+        raise TypeError(f"weight must be float32 or bfloat16, got {weight.dtype}")
+    return _arg(weight, "weight", _BF if wide else _F32, (H,), dev), wide
+
+
+def dg_rms_norm(X, weight, eps, Y=None, residual=None, S=None, Q=None, sf=None, stream=None):
+    """s = X + residual; y = s * weight / sqrt(mean(s * s) + eps), over the rows of X [T,H] bfloat16.
+
+    Outputs, each optional: S bfloat16 (s; may be X or residual itself), Y bfloat16 (y), Q (y in E4M3, one scale per 1x128
+    block in sf: float32 [H/128,T], or int32 [ceil(H/512),T] for packed UE8M0), which are A and sfa of the dense FP8
+    products.  weight [H] bfloat16, float32 or None.  Returns Y, Q or S, the first that is given."""
+    shape = T, H = _rows_of(X, "X")
+    dev = _on(X, "X")
+    if (Q is None) != (sf is None):
+        raise ValueError("Q and sf go together")
+    w, wide = _weight(weight, H, dev)
+    ue8m0 = sf is not None and sf.dtype is _I32
+    x = _arg(X, "X", _BF, shape, dev)
+    norm = _Norm(_opt(residual, "residual", _BF, shape, dev), w, wide, eps, _opt(S, "S", _BF, shape, dev),
+                 _opt(Y, "Y", _BF, shape, dev), None if Q is None else _fp8_arg(Q, "Q", shape, dev),
+                 _opt(sf, "sf", _I32 if ue8m0 else _F32, ((H + 511) // 512 if ue8m0 else H // 128, T), dev), ue8m0)
+    if norm.S and norm.S == norm.Y:
+        raise ValueError("S and Y must not be the same tensor")
+    status = lib.dg_rms_norm(x, ctypes.byref(norm), T, H, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return Y if Y is not None else Q if Q is not None else S
+
+
+def dg_rms_norm_backward(dY, S, weight, eps, dX, dweight, dS=None, stream=None):
+    """Gradients of dg_rms_norm: dX = d loss / d s through y, plus dS (what reaches S past the norm), and dweight.
+
+    dY, S (the norm's input), dS, dX bfloat16 [T,H] (dX may be dY or dS itself, or None), dweight float32 [H] or None."""
+    shape = T, H = _rows_of(dY, "dY")
+    dev = _on(dY, "dY")
+    w, wide = _weight(weight, H, dev)
+    status = lib.dg_rms_norm_backward(
+        _arg(dY, "dY", _BF, shape, dev), _arg(S, "S", _BF, shape, dev), w, wide, eps, _opt(dS, "dS", _BF, shape, dev),
+        _opt(dX, "dX", _BF, shape, dev), _opt(dweight, "dweight", _F32, (H,), dev), T, H, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return dX
