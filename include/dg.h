@@ -551,6 +551,49 @@ dg_status dg_rms_norm_backward(const void *dY, const void *S, const void *weight
                                const void *dS, void *dX, float *dweight, int T, int H, void *stream);
 
 /*
+ * Routing: the topk experts of each token and their weights, as dg_moe_sort_*
+ * and dg_moe_combine take them, from a router's logits [T][num_experts] (FP32 or
+ * BF16, logits_type).
+ *
+ *   p = softmax of the row, or of each logit 1 / (1 + e^-l)      (score)
+ *   v = p + bias[expert]     bias FP32 [num_experts] or NULL: what keeps the experts' loads
+ *                            balanced; it takes part in the choice alone
+ *   The experts are groups runs of the same number of experts; a group is worth the sum of
+ *   its group_best (1 or 2) largest v, and only experts of the topk_groups most worthy
+ *   groups can be chosen (groups 1: of all).
+ *   expert_ids [T][topk]: the experts of the topk largest v, largest first; of equals (groups
+ *   too) the one of the lowest index first
+ *   weights [T][topk] FP32: scale * p, or with renormalise scale * p / (sum of the chosen p)
+ *
+ * p, v and the weights are computed in 64 bits, so that a choice does not hang
+ * on FP32's roundings.  An expert whose logit or v is -infinity is not available:
+ * where fewer than topk are, the remaining ids are -1 and their weights 0 (as the
+ * sort drops them), and a row without any has no other; weights whose sum is 0 stay 0.
+ * A NaN logit, of which a softmax makes a row of NaN, ranks below every number.
+ * At most 1024 experts, topk 64 and groups 64.
+ *
+ * dg_moe_route_backward: d_logits [T][num_experts] (the logits' type, or the
+ * logits' array itself) from d_weights FP32 [T][topk], the gradient of the weights
+ * (dg_moe_combine_backward gives it), with the ids of the forward call; of routing
+ * it takes score, renormalise and scale.  The choice itself and the bias have no
+ * gradient.  Ids outside [0, num_experts) add nothing; one that a token names twice
+ * gets both terms.
+ * Arrays must be aligned to their elements (BF16 2 bytes, the others 4).
+ */
+typedef enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
+typedef struct {
+    int score;              /* dg_score */
+    int groups, topk_groups, group_best;
+    int renormalise;
+    float scale;
+} dg_routing;
+dg_status dg_moe_route(const void *logits, int logits_type, const float *bias, const dg_routing *routing,
+                       int32_t *expert_ids, float *weights, int T, int num_experts, int topk, void *stream);
+dg_status dg_moe_route_backward(const void *logits, int logits_type, const int32_t *expert_ids, const float *d_weights,
+                                const dg_routing *routing, void *d_logits, int T, int num_experts, int topk,
+                                void *stream);
+
+/*
  * Health of the current device's kernels.  The producer/consumer kernel
  * variant (one wave streams the A tiles into an LDS ring, the others wait on
  * per-slot LDS flags; chosen for few rows, e.g. M <= 128) bounds every such

@@ -29,3 +29,4 @@ from .dg import (ACTIVATIONS, EPI_BIAS_BF16, EPI_BIAS_F32, EPI_RESIDUAL, EPI_Z, 
                  dg_m_grouped_bf16_gemm_nt_masked_epilogue, dg_m_grouped_fp8_gemm_nt_contiguous_epilogue,
                  dg_m_grouped_fp8_gemm_nt_masked_epilogue)
 from .dg import dg_rms_norm, dg_rms_norm_backward  # noqa: F401
+from .dg import SCORES, dg_moe_route, dg_moe_route_backward  # noqa: F401

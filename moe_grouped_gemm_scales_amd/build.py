@@ -4,7 +4,8 @@ The host library (C++, HIP runtime + hipRTC) is compiled with the host C++
 compiler against the ROCm headers, plus HIP sources compiled for gfx950 by hipcc
 (csrc/device.hip: the library's status words and its measurement probes;
 csrc/moe.hip: tokens to expert rows and back; csrc/linear.hip: the backward
-side of the products with a fused epilogue; csrc/norm.hip: the norm in front of them); the GEMM kernel source is embedded into the library as text and
+side of the products with a fused epilogue; csrc/norm.hip: the norm in front of them;
+csrc/route.hip: the router's choice); the GEMM kernel source is embedded into the library as text and
 compiled for gfx950 by hipRTC at run time, once per shape.  ``precompile()`` runs that hipRTC step ahead of time
 (no GPU needed) so that the code objects of the standard workloads sit in the
 in-tree cache and the device source is known to compile for gfx950.
@@ -25,7 +26,7 @@ PYCHECK = os.path.join(PKG, "_pycheck.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["api.cpp", "jit.cpp", "heuristics.cpp"]
-DEVICE_SOURCES = ["device.hip", "moe.hip", "linear.hip", "norm.hip"]
+DEVICE_SOURCES = ["device.hip", "moe.hip", "linear.hip", "norm.hip", "route.hip"]
 BUILD_DIR = os.path.join(PKG, "_build")
 # every HIP source is compiled for gfx950 with packed FP32 instructions off
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -1,0 +1,383 @@
+// Routing of tokens to experts (hipcc, gfx950): the topk experts of each token
+// and their weights from a router's logits, and the gradient of the logits.  The
+// operations are specified in include/dg.h.
+//
+//   score p = softmax(l) or 1 / (1 + e^-l),  choice value v = p + bias
+//   topk of v (among the best groups), w = scale p / (sum of the chosen p, or 1)
+//
+// One wave a token, expert e in lane e % 64: the logits are read once, coalesced,
+// and a choice is a few cross-lane steps.  A token's logits are at most 4 KB, so
+// the pass is bound by latency and by the wave's own instructions, not by HBM.
+#include <cmath>
+#include <type_traits>
+
+#include "row_kernels.h"
+
+namespace dg {
+namespace {
+
+constexpr int kMaxExperts = 1024;      // 16 a lane
+constexpr int kMaxTopk = 64;           // a chosen expert a lane
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    int* ids;
+    float* weights;
+    int E, k, groups, group_size, kept, best, renormalise;
+    float scale;
+};
+
+__device__ __forceinline__ float logit(const void* p, int wide, u64 at) {
+    return wide ? static_cast<const float*>(p)[at] : bf16_lo(static_cast<const u16*>(p)[at]);
+}
+
+// Sums and maxima over the wave, the same in every lane.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+template <int D>
+__device__ __forceinline__ u32 max_rotated(u32 v) {
+    const u32 o = (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + D, 0xf, 0xf, true);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ u32 wave_max(u32 v) {
+    v = max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(v))));
+    auto part = [&](int lane) { return (u32)__builtin_amdgcn_readlane((int)v, lane); };
+    const u32 a = part(0), b = part(16), c = part(32), d = part(48);
+    const u32 x = a > b ? a : b, y = c > d ? c : d;
+    return x > y ? x : y;
+}
+
+// A choice value as an integer of the same order; 0: the expert is not available.  A NaN (of
+// its logit, or of a softmax whose row holds one) ranks below every number.
+__device__ __forceinline__ u64 rank_of(double v) {
+    if (v != v) v = -1e300;
+    const u64 b = __builtin_bit_cast(u64, v);
+    return (b >> 63) ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ double value_of(u64 r) {
+    return __builtin_bit_cast(double, (r >> 63) ? r & ~(1ull << 63) : ~r);
+}
+
+// Choice values are 64-bit numbers: 256 scores of 8192 tokens hold pairs that FP32 scores
+// tell apart wrongly, and a choice is not rounded but made.
+template <int PER, bool WIDE, bool SIGMOID>
+__global__ void __launch_bounds__(64) dg_moe_route_kernel(const RouteArgs a) {
+    const int lane = threadIdx.x;
+    const u64 t = blockIdx.x;
+    const int E = a.E;
+    __shared__ double score[PER * 64];
+    __shared__ u64 shared_rank[PER * 64];
+    float l[PER];
+    double p[PER];
+    u64 rank[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        l[i] = lane + 64 * i < E ? logit(a.logits, WIDE, t * (u64)E + (lane + 64 * i)) : -INFINITY;
+    if constexpr (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) p[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+    } else {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
+        top = wave_max(top);
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            p[i] = l[i] == -INFINITY ? 0.0 : exp((double)l[i] - (double)top);
+            sum += p[i];
+        }
+        sum = 1.0 / wave_sum(sum);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) p[i] *= sum;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 64 * i;
+        const double v = a.bias && e < E ? p[i] + (double)a.bias[e] : p[i];
+        rank[i] = e >= E || l[i] == -INFINITY || v == -INFINITY ? 0ull : rank_of(v);
+        score[e] = p[i];
+    }
+    if (a.groups > 1) {
+        // L lanes a group: the sum of its best one or two values, then the group's place among all
+#pragma unroll
+        for (int i = 0; i < PER; ++i) shared_rank[lane + 64 * i] = rank[i];
+        __syncthreads();
+        int L = 64;
+        while (L * a.groups > 64) L /= 2;
+        const int g = lane / L, sub = lane % L;
+        u64 b1 = 0, b2 = 0;
+        if (g < a.groups)
+            for (int j = sub; j < a.group_size; j += L) {
+                const u64 r = shared_rank[g * a.group_size + j];
+                b2 = r > b1 ? b1 : r > b2 ? r : b2;
+                b1 = r > b1 ? r : b1;
+            }
+        for (int d = 1; d < L; d *= 2) {
+            const u64 o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+            const u64 lower = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
+            b1 = o1 > b1 ? o1 : b1;
+            b2 = lower > second ? lower : second;
+        }
+        double worth = -INFINITY;
+        if (b1) worth = value_of(b1) + (a.best > 1 && b2 ? value_of(b2) : 0.0);
+        int better = 0;
+        for (int h = 0; h < a.groups; ++h) {
+            const double o = __shfl(worth, h * L);
+            better += o > worth || (o == worth && h < g);
+        }
+        if (better >= a.kept && g < a.groups)
+            for (int j = sub; j < a.group_size; j += L) shared_rank[g * a.group_size + j] = 0ull;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) rank[i] = shared_rank[lane + 64 * i];
+    } else {
+        __syncthreads();
+    }
+    // the best of the wave, k times: the largest upper word, then among its lanes the largest
+    // lower word, then the lowest expert; the first step mostly leaves one lane
+    int id = -1;                                  // of choice `lane`
+    for (int j = 0; j < a.k; ++j) {
+        u64 best = rank[0];
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < PER; ++i) {
+            at = rank[i] > best ? lane + 64 * i : at;
+            best = rank[i] > best ? rank[i] : best;
+        }
+        const u32 hi = wave_max((u32)(best >> 32));
+        if (hi == 0u) break;                      // none is available
+        bool mine = (u32)(best >> 32) == hi;
+        u64 with = __ballot(mine);
+        if (with & (with - 1)) {
+            const u32 lo = wave_max(mine ? (u32)best : 0u);
+            mine = mine && (u32)best == lo;
+            with = __ballot(mine);
+            if (with & (with - 1)) {
+                const u32 first = kMaxExperts - wave_max(mine ? (u32)(kMaxExperts - at) : 0u);
+                with = __ballot(mine && (u32)at == first);
+            }
+        }
+        const int chosen = __builtin_amdgcn_readlane(at, __builtin_ctzll(with));
+        if (lane == j) id = chosen;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 64 * i == chosen) rank[i] = 0ull;
+    }
+    double w = id >= 0 ? score[id] : 0.0;
+    if (a.renormalise) {
+        const double sum = wave_sum(w);
+        w = sum == 0.0 ? 0.0 : w / sum;
+    }
+    if (lane < a.k) {
+        a.ids[t * (u64)a.k + lane] = id;
+        a.weights[t * (u64)a.k + lane] = (float)((double)a.scale * w);
+    }
+}
+
+// Gradient: from that of the weights, dp of the chosen experts, then through the scores' function.
+//   sigmoid: dl = dp p (1 - p);  softmax: dl_e = p_e (dp_e - sum_j dp_j p_j)
+//   dp_j = scale dw_j, or renormalised, with r_j = p_j / P, P the sum of the chosen p: dp_j p_j = scale r_j
+//   (dw_j - sum_i dw_i r_i), which add up to zero, so that a softmax's other experts get nothing
+// An expert that ids names twice gets both terms, in j order.
+struct RouteBackwardArgs {
+    const void* logits;
+    const int* ids;
+    const float* d_weights;
+    void* d_logits;
+    int E, k;
+    float scale;
+};
+template <int PER, bool WIDE, bool SIGMOID, bool RENORM>
+__global__ void __launch_bounds__(64) dg_moe_route_backward_kernel(const RouteBackwardArgs a) {
+    const int lane = threadIdx.x;
+    const u64 t = blockIdx.x;
+    const int E = a.E;
+    const u64 row = t * (u64)E;
+    int id = lane < a.k ? a.ids[t * (u64)a.k + lane] : -1;
+    if ((u32)id >= (u32)E) id = -1;
+    const float dw = id >= 0 ? a.scale * a.d_weights[t * (u64)a.k + lane] : 0.f;
+    const float lj = id >= 0 ? logit(a.logits, WIDE, row + (u32)id) : -INFINITY;
+    float p[PER];                              // softmax without renormalising: of every expert
+    float c;                                   // choice `lane`'s term
+    float every = 0.f;                         // ... and what every expert has subtracted, times its p
+    if constexpr (SIGMOID) {
+        // p = e^min(l,0) / (1 + e^-|l|), 1 - p that of -l; the ratios p_j / P from powers relative to the
+        // largest, which do not all vanish where every chosen logit is far below zero
+        const float small = 1.f / (1.f + expf(-fabsf(lj))), rest = (lj > 0.f ? expf(-lj) : 1.f) * small;
+        if constexpr (RENORM) {
+            const float top = fminf(wave_max(lj), 0.f);
+            const float s = lj == -INFINITY ? 0.f : expf(fminf(lj, 0.f) - top) * small;
+            const float P = wave_sum(s);
+            const float r = P > 0.f ? s / P : P != P ? P : 0.f;
+            c = r * rest * (dw - wave_sum(dw * r));
+        } else {
+            c = dw * (lj > 0.f ? 1.f : expf(lj)) * small * rest;
+        }
+    } else if constexpr (RENORM) {
+        const float top = wave_max(lj);
+        const float s = lj == -INFINITY ? 0.f : expf(lj - top);
+        const float P = wave_sum(s);
+        const float r = P > 0.f ? s / P : P != P ? P : 0.f;
+        c = r * (dw - wave_sum(dw * r));
+    } else {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            p[i] = lane + 64 * i < E ? logit(a.logits, WIDE, row + (lane + 64 * i)) : -INFINITY;
+            top = fmaxf(top, p[i]);
+        }
+        top = wave_max(top);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            p[i] = p[i] == -INFINITY ? 0.f : expf(p[i] - top);
+            sum += p[i];
+        }
+        sum = wave_sum(sum);
+        const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) p[i] *= inv;
+        c = dw;
+        every = wave_sum(lj == -INFINITY ? 0.f : dw * (expf(lj - top) * inv));
+    }
+    float out[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) out[i] = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+        const int e = __builtin_amdgcn_readlane(id, j);
+        const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, c), j));
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (e == lane + 64 * i) out[i] += v;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 64 * i;
+        if constexpr (!SIGMOID && !RENORM) out[i] = p[i] * (out[i] - every);
+        if (e >= E) continue;
+        if constexpr (WIDE) static_cast<float*>(a.d_logits)[row + e] = out[i];
+        else static_cast<u16*>(a.d_logits)[row + e] = to_bf16(out[i]);
+    }
+}
+
+template <int PER>
+dg_status launch_route(bool wide, bool sigmoid, unsigned T, void* stream, const RouteArgs& a) {
+    auto* kernel = wide ? (sigmoid ? dg_moe_route_kernel<PER, true, true> : dg_moe_route_kernel<PER, true, false>)
+                        : (sigmoid ? dg_moe_route_kernel<PER, false, true> : dg_moe_route_kernel<PER, false, false>);
+    return launch_rows("moe_route", kernel, dim3(T), 64, stream, a);
+}
+template <int PER, bool WIDE>
+dg_status launch_route_backward(bool sigmoid, bool renorm, unsigned T, void* stream, const RouteBackwardArgs& a) {
+    auto* kernel = sigmoid ? (renorm ? dg_moe_route_backward_kernel<PER, WIDE, true, true>
+                                     : dg_moe_route_backward_kernel<PER, WIDE, true, false>)
+                           : (renorm ? dg_moe_route_backward_kernel<PER, WIDE, false, true>
+                                     : dg_moe_route_backward_kernel<PER, WIDE, false, false>);
+    return launch_rows("moe_route_backward", kernel, dim3(T), 64, stream, a);
+}
+
+dg_status check_route(const char* what, bool null, const dg_routing* r, int logits_type, int T, int E, int k) {
+    const std::string name(what);
+    if (!r || null) return set_error(DG_ERR_INVALID_ARG, name + ": NULL pointer");
+    if (T < 0 || E <= 0 || k <= 0)
+        return set_error(DG_ERR_INVALID_ARG, name + ": sizes must be positive (T may be 0)");
+    if (logits_type != DG_TYPE_F32 && logits_type != DG_TYPE_BF16)
+        return set_error(DG_ERR_INVALID_ARG, name + ": unknown type of the logits");
+    if (r->score != DG_SCORE_SOFTMAX && r->score != DG_SCORE_SIGMOID)
+        return set_error(DG_ERR_INVALID_ARG, name + ": unknown score");
+    if (E > kMaxExperts) return set_error(DG_ERR_UNSUPPORTED, name + ": at most 1024 experts");
+    if (k > E) return set_error(DG_ERR_INVALID_ARG, name + ": topk is larger than the number of experts");
+    if (k > kMaxTopk) return set_error(DG_ERR_UNSUPPORTED, name + ": topk is at most 64");
+    if (!fits_launch(T, 64)) return set_error(DG_ERR_UNSUPPORTED, name + ": too many tokens for one launch");
+    return DG_OK;
+}
+
+// experts a lane
+int per_lane(int E) {
+    int per = 1;
+    while (per * 64 < E) per *= 2;
+    return per;
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dg_status dg_moe_route(const void* logits, int logits_type, const float* bias, const dg_routing* routing,
+                       int32_t* expert_ids, float* weights, int T, int num_experts, int topk, void* stream) {
+    return guarded([&]() -> dg_status {
+        const bool null = T > 0 && (!logits || !expert_ids || !weights);
+        dg_status s = check_route("moe_route", null, routing, logits_type, T, num_experts, topk);
+        if (s != DG_OK) return s;
+        const dg_routing r = *routing;
+        if (r.groups <= 0 || num_experts % r.groups || r.topk_groups <= 0 || r.topk_groups > r.groups)
+            return set_error(DG_ERR_INVALID_ARG, "moe_route: groups must divide the experts, topk_groups be 1 to groups");
+        if (r.groups > 64) return set_error(DG_ERR_UNSUPPORTED, "moe_route: at most 64 groups");
+        if (r.group_best != 1 && r.group_best != 2)
+            return set_error(DG_ERR_INVALID_ARG, "moe_route: group_best must be 1 or 2");
+        const int size = num_experts / r.groups;
+        if (topk > r.topk_groups * size)
+            return set_error(DG_ERR_INVALID_ARG, "moe_route: topk is larger than the experts of topk_groups groups");
+        const bool wide = logits_type == DG_TYPE_F32;
+        if (!aligned(logits, wide ? 4 : 2) || !aligned(bias, 4) || !aligned(expert_ids, 4) || !aligned(weights, 4))
+            return set_error(DG_ERR_ALIGNMENT, "moe_route: arrays must be aligned to their elements");
+        if (T == 0) return DG_OK;
+        const RouteArgs a{logits, bias, expert_ids, weights, num_experts, topk,
+                          r.topk_groups < r.groups ? r.groups : 1, size, r.topk_groups, r.group_best, r.renormalise != 0, r.scale};
+        const bool sigmoid = r.score == DG_SCORE_SIGMOID;
+        switch (per_lane(num_experts)) {
+            case 1: return launch_route<1>(wide, sigmoid, (unsigned)T, stream, a);
+            case 2: return launch_route<2>(wide, sigmoid, (unsigned)T, stream, a);
+            case 4: return launch_route<4>(wide, sigmoid, (unsigned)T, stream, a);
+            case 8: return launch_route<8>(wide, sigmoid, (unsigned)T, stream, a);
+            default: return launch_route<16>(wide, sigmoid, (unsigned)T, stream, a);
+        }
+    });
+}
+
+dg_status dg_moe_route_backward(const void* logits, int logits_type, const int32_t* expert_ids, const float* d_weights,
+                                const dg_routing* routing, void* d_logits, int T, int num_experts, int topk,
+                                void* stream) {
+    return guarded([&]() -> dg_status {
+        const bool null = T > 0 && (!logits || !expert_ids || !d_weights || !d_logits);
+        dg_status s = check_route("moe_route_backward", null, routing, logits_type, T, num_experts, topk);
+        if (s != DG_OK) return s;
+        const bool wide = logits_type == DG_TYPE_F32;
+        if (!aligned(logits, wide ? 4 : 2) || !aligned(d_logits, wide ? 4 : 2) || !aligned(expert_ids, 4) ||
+            !aligned(d_weights, 4))
+            return set_error(DG_ERR_ALIGNMENT, "moe_route_backward: arrays must be aligned to their elements");
+        if (T == 0) return DG_OK;
+        const RouteBackwardArgs a{logits, expert_ids, d_weights, d_logits, num_experts, topk, routing->scale};
+        const bool sigmoid = routing->score == DG_SCORE_SIGMOID, renorm = routing->renormalise != 0;
+        auto launch = [&](auto per) {
+            constexpr int PER = decltype(per)::value;
+            return wide ? launch_route_backward<PER, true>(sigmoid, renorm, (unsigned)T, stream, a)
+                        : launch_route_backward<PER, false>(sigmoid, renorm, (unsigned)T, stream, a);
+        };
+        switch (per_lane(num_experts)) {
+            case 1: return launch(std::integral_constant<int, 1>{});
+            case 2: return launch(std::integral_constant<int, 2>{});
+            case 4: return launch(std::integral_constant<int, 4>{});
+            case 8: return launch(std::integral_constant<int, 8>{});
+            default: return launch(std::integral_constant<int, 16>{});
+        }
+    });
+}
+
+}  // extern "C"

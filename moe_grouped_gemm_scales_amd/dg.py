@@ -135,6 +135,8 @@ def _load():
                        ("dg_bf16_gemm_tn", [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_m_grouped_bf16_gemm_nn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_k_grouped_bf16_gemm_tn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
+                       ("dg_moe_route", [vp, i32] + [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_moe_route_backward", [vp, i32] + [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_rms_norm", [vp] * 2 + [i32] * 2 + [vp]),
                        ("dg_rms_norm_backward", [vp] * 3 + [i32, ctypes.c_float] + [vp] * 3 + [i32] * 2 + [vp]),
                        ("dg_moe_combine", [vp] * 5 + [i32] * 4 + [vp]),
@@ -1208,3 +1210,75 @@ def dg_rms_norm_backward(dY, S, weight, eps, dX, dweight, dS=None, stream=None):
     if status:
         _check(status)
     return dX
+
+
+# ---------------------------------------------------------------- routing
+SCORES = {"softmax": 0, "sigmoid": 1}   # dg_score
+
+
+class _Routing(ctypes.Structure):       # dg_routing
+    _fields_ = [("score", ctypes.c_int), ("groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("group_best", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+def _logits(logits, others):
+    """((T, E), dtype, topk) of a router's logits [T,E] and an array [T,topk]."""
+    if logits.dtype is not _F32 and logits.dtype is not _BF:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2 or others.dim() != 2:
+        raise ValueError("logits must be [T, num_experts], ids and weights [T, topk]")
+    if max(*logits.shape, others.shape[1]) > _INT_MAX:
+        _too_many("logits", max(*logits.shape, others.shape[1]))
+    return logits.shape, logits.dtype, others.shape[1]
+
+
+def _score(name) -> int:
+    score = SCORES.get(name)
+    if score is None:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, got {name!r}")
+    return score
+
+
+def _routed_on(logits) -> int:
+    """The device of the logits, which has to be the current one."""
+    d = logits.get_device()
+    if d < 0 or d != _cur_device():
+        _dev(logits, "logits")
+    return d
+
+
+def dg_moe_route(logits, bias, expert_ids, weights, score="softmax", groups=1, topk_groups=1, group_best=1,
+                 renormalise=True, scale=1.0, stream=None):
+    """The topk experts of each token and their weights, from a router's logits [T,num_experts] (float32 or bfloat16).
+
+    p = softmax(logits) or sigmoid(logits) (score); the experts of the topk largest p + bias, largest first, the lowest
+    index first among equals, into expert_ids int32 [T,topk]; their p, divided by its sum if renormalise, times scale
+    into weights float32 [T,topk].  bias float32 [num_experts] or None.  With groups > 1 only experts of the topk_groups
+    groups with the largest sum of their group_best (1, 2) largest p + bias are chosen from.  Experts at -inf are not
+    available: id -1 and weight 0 where too few are."""
+    (T, E), dtype, k = _logits(logits, expert_ids)
+    dev = _routed_on(logits)
+    routing = _Routing(_score(score), groups, topk_groups, group_best, bool(renormalise), scale)
+    status = lib.dg_moe_route(
+        _arg(logits, "logits", dtype, (T, E), dev), dtype is _BF, _opt(bias, "bias", _F32, (E,), dev),
+        ctypes.byref(routing), _arg(expert_ids, "expert_ids", _I32, (T, k), dev),
+        _arg(weights, "weights", _F32, (T, k), dev), T, E, k, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return expert_ids
+
+
+def dg_moe_route_backward(logits, expert_ids, d_weights, d_logits, score="softmax", renormalise=True, scale=1.0,
+                          stream=None):
+    """d_logits [T,num_experts] (the logits' type; may be logits itself) from d_weights float32 [T,topk], with the ids,
+    score, renormalise and scale of the forward call."""
+    (T, E), dtype, k = _logits(logits, expert_ids)
+    dev = _routed_on(logits)
+    routing = _Routing(_score(score), 1, 1, 1, bool(renormalise), scale)
+    status = lib.dg_moe_route_backward(
+        _arg(logits, "logits", dtype, (T, E), dev), dtype is _BF, _arg(expert_ids, "expert_ids", _I32, (T, k), dev),
+        _arg(d_weights, "d_weights", _F32, (T, k), dev), ctypes.byref(routing),
+        _arg(d_logits, "d_logits", dtype, (T, E), dev), T, E, k, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return d_logits

@@ -41,3 +41,71 @@ def e4m3_values(codes, scales):
     """Values of codes [T, K] with scales [T, K/128]."""
     v = codes.view(torch.float8_e4m3fn).double()
     return (v.reshape(v.shape[0], -1, 128) * scales.double()[..., None]).reshape(v.shape)
+
+
+# ------------------------------------------------------------------ routing
+def scores(logits, score):
+    """p of rows of logits; a row of nothing but -inf has zeros."""
+    l = logits.double()
+    if score == "sigmoid":
+        return torch.sigmoid(l)
+    p = torch.softmax(l, 1)
+    return torch.where((l == -math.inf).all(1, keepdim=True), torch.zeros_like(p), p)
+
+
+def route(logits, bias, k, score, groups=1, topk_groups=1, group_best=1, renormalise=True, scale=1.0):
+    """(ids, weights) token by token, by sorting (value, lowest index) pairs."""
+    T, E = logits.shape
+    p = scores(logits, score)
+    v = p if bias is None else p + bias.double()
+    ids, weights = torch.full((T, k), -1, dtype=torch.int32), torch.zeros((T, k), dtype=torch.float64)
+    size = E // groups
+    for t in range(T):
+        row = []                                     # (-value, expert) of the available ones
+        for e in range(E):
+            x = float(v[t, e])
+            if float(logits[t, e]) == -math.inf or x == -math.inf:
+                continue
+            row.append((1e300 if math.isnan(x) else -x, e))
+        if groups > 1:
+            worth = []
+            for g in range(groups):
+                mine = sorted(r for r in row if r[1] // size == g)[:group_best]
+                if mine:
+                    worth.append((sum(r[0] for r in mine), g))
+            keep = {g for _, g in sorted(worth)[:topk_groups]}
+            row = [r for r in row if r[1] // size in keep]
+        for j, (_, e) in enumerate(sorted(row)[:k]):
+            ids[t, j], weights[t, j] = e, p[t, e]
+    if renormalise:
+        total = weights.sum(1, keepdim=True)
+        weights = torch.where(total == 0, torch.zeros_like(weights), weights / total)
+    return ids, scale * weights
+
+
+def route_backward(logits, ids, d_weights, score, renormalise, scale):
+    """(d_logits, magnitude of its terms)."""
+    l = logits.double()
+    T, E = l.shape
+    p = scores(logits, score)
+    out, mag = torch.zeros_like(p), torch.zeros_like(p)
+    for t in range(T):
+        mine = [(int(e), scale * float(d)) for e, d in zip(ids[t], d_weights[t]) if 0 <= int(e) < E]
+        total = sum(float(p[t, e]) for e, _ in mine)
+        mean = sum(d * float(p[t, e]) for e, d in mine) / total if renormalise and total else 0.0
+        size = sum(abs(d) * float(p[t, e]) for e, d in mine) / total if renormalise and total else 0.0
+        dp, dm = torch.zeros(E, dtype=torch.float64), torch.zeros(E, dtype=torch.float64)
+        for e, d in mine:
+            if renormalise and not total:
+                continue
+            dp[e] += (d - mean) / total if renormalise else d
+            dm[e] += (abs(d) + size) / total if renormalise else abs(d)
+        if score == "sigmoid":
+            slope = p[t] * torch.sigmoid(-l[t])
+            out[t], mag[t] = dp * slope, dm * slope
+        else:
+            out[t] = p[t] * (dp - (dp * p[t]).sum())
+            mag[t] = p[t] * (dm + (0 if renormalise else (dm * p[t]).sum()))
+            if renormalise:                          # the sum is zero: only the chosen get a gradient
+                out[t] = p[t] * dp
+    return out, mag
