@@ -594,6 +594,42 @@ dg_status dg_moe_route_backward(const void *logits, int logits_type, const int32
                                 void *stream);
 
 /*
+ * Activations kept for the backward pass in 8 bits: BF16 rows X [M][N] (the Z of
+ * a fused epilogue, a product's A operand) as
+ *   codes   E4M3 [M][N]
+ *   scales  E8M0 bytes [M][ceil(N/128)], one per 1x128 block (the last of a row may be
+ *           shorter): 2^(byte - 127), the least power of two (from 2^-126) that brings the
+ *           block within 448; 127 for a block of zeros; 255 (NaN, all of the block with
+ *           it) where it holds an infinity or NaN
+ * code = E4M3(x / scale), round-to-nearest-even: half the bytes of BF16, 2^-4 relative
+ * per element (2^-10 of the scale where that is larger); under the largest scale,
+ * 2^120, codes end at 240, since 256 * 2^120 is no BF16 number.  Any N.
+ * dg_checkpoint_restore: X = code * scale in BF16, which holds it without rounding
+ * (below 2^-126 it may round).
+ * m_indices int32 [M] or NULL: rows that name an expert (0 and more) are passed;
+ * those with -1 (a segment's padding rows) are written as zeros, scale 1; all other
+ * rows are neither read nor written.
+ *
+ * dg_epilogue_backward_fp8, dg_m_grouped_epilogue_backward_fp8_contiguous: as
+ * dg_epilogue_backward and its grouped form with Z = code * scale, and
+ *   H = activation(Z)    BF16 [M][N] or NULL: the epilogue's output again (without its
+ *                        residual), the operand of the next product's weight gradient; an
+ *                        array of its own.  Padding rows are cleared as in dZ
+ * dZ may be dD itself.  With activation none, dZ is dD's copy and H is Z.
+ * X, codes, dD, dZ and H must be 16-byte aligned, m_indices and dbias 4-byte.  The
+ * partial sums of dbias use the stream's workspace.
+ */
+dg_status dg_checkpoint_fp8(const void *X, const int32_t *m_indices, void *codes, void *scales, int M, int N,
+                            void *stream);
+dg_status dg_checkpoint_restore(const void *codes, const void *scales, const int32_t *m_indices, void *X, int M, int N,
+                                void *stream);
+dg_status dg_epilogue_backward_fp8(const void *dD, const void *codes, const void *scales, int activation, void *dZ,
+                                   void *H, float *dbias, int M, int N, void *stream);
+dg_status dg_m_grouped_epilogue_backward_fp8_contiguous(const void *dD, const void *codes, const void *scales,
+                                                        int activation, const int32_t *m_indices, void *dZ, void *H,
+                                                        float *dbias, int M, int N, int num_groups, void *stream);
+
+/*
  * Health of the current device's kernels.  The producer/consumer kernel
  * variant (one wave streams the A tiles into an LDS ring, the others wait on
  * per-slot LDS flags; chosen for few rows, e.g. M <= 128) bounds every such

@@ -147,8 +147,13 @@ dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int co
                          void* stream);
 // BF16 X [rows][cols] copied to rows of `pitch` elements (a multiple of 8), the rest zeros (linear.hip)
 dg_status pad_rows_bf16(const void* x, void* xp, int rows, int cols, int pitch, void* stream);
-// out[n] = the sum over `chunks` rows of partial [chunks][N], in a fixed order (linear.hip)
-dg_status column_sums(const char* what, const float* partial, int chunks, int N, float* out, void* stream);
+// out[g][n] = the sum of the rows of partial [chunks][N] that belong to group g (m_indices of row c * chunk;
+// NULL: all), in a fixed order (linear.hip)
+dg_status column_sums(const char* what, const float* partial, const int32_t* m_indices, int chunks, int chunk, int N,
+                      int G, float* out, void* stream);
+bool column_sums_fit(int N, int G);
+// rows a workgroup of an epilogue's backward pass takes
+int backward_chunk(int rows, int N);
 std::string cache_dir();
 
 // Device address of the library's status words on the current device

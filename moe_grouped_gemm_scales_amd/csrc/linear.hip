@@ -2,6 +2,7 @@
 // activation's gradient with the bias gradient in the same pass, and the
 // K-contiguous rewrite of BF16 operands for the NN and TN products.  The
 // operations are specified in include/dg.h.
+#include "activation.h"
 #include "row_kernels.h"
 
 namespace dg {
@@ -92,49 +93,6 @@ __global__ void __launch_bounds__(256) dg_pad_rows_bf16_kernel(const PadArgs a) 
 }
 
 // ---------------------------------------------------------------- activation and bias gradient
-// d act / d z in FP32.  exp2 and the reciprocal are the hardware's (1 ulp), Phi's tail is the
-// rational fit of the forward epilogue (relative error 7e-8 before FP32's roundings, its
-// e^(-z^2/2) shared with the density): errors of FP32's own size, which the bias
-// gradient's sum averages.  With the device library's expf, erff and division the
-// pass was bound by its arithmetic (8192 x 4096, GELU: 55 us against 45; 2304 x
-// 2112, tanh form: 12.4 against 9.2).  A fit that keeps only the absolute error
-// small (1.5e-7 of erf) has three terms fewer and is off by 1 % at z = -8: 43.7 us
-// against 44.5.
-// Past |z| = 16 the slopes are 0 or 1 to the last bit (SiLU: past 200 its tail is
-// below FP32); z is cut there, so that no infinity meets a zero.  A NaN stays a NaN.
-__device__ __forceinline__ float cut(float z, float far) { return z > far ? far : z < -far ? -far : z; }
-__device__ __forceinline__ float logistic2(float x) {      // 1 / (1 + 2^-x)
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x));
-}
-template <int ACT>
-__device__ __forceinline__ float slope(float z) {
-    if constexpr (ACT == DG_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
-    if constexpr (ACT == DG_ACT_SILU) {
-        z = cut(z, 200.f);
-        const float s = logistic2(1.44269504f * z);
-        return s * __builtin_fmaf(z, 1.f - s, 1.f);
-    }
-    if constexpr (ACT == DG_ACT_GELU) {
-        z = cut(z, 16.f);
-        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.30405593f, __builtin_fabsf(z), 1.f));
-        const float e = __builtin_amdgcn_exp2f(-0.72134752f * z * z);
-        float y = __builtin_fmaf(t, 0.036534112f, -0.15392894f);
-        y = __builtin_fmaf(t, y, 0.18981865f);
-        y = __builtin_fmaf(t, y, -0.041117497f);
-        y = __builtin_fmaf(t, y, 0.12256832f);
-        y = __builtin_fmaf(t, y, 0.10271288f);
-        y = __builtin_fmaf(t, y, 0.12215308f);
-        const float tail = __builtin_fmaf(t, y, 0.12125936f) * t * e;       // Phi(-|z|)
-        return __builtin_fmaf(0.39894228f * z, e, z < 0.f ? tail : 1.f - tail);
-    }
-    if constexpr (ACT == DG_ACT_GELU_TANH) {
-        z = cut(z, 16.f);
-        const float s = logistic2(2.30220820f * z * __builtin_fmaf(0.044715f * z, z, 1.f));
-        return __builtin_fmaf(z * s * (1.f - s), __builtin_fmaf(0.21406445f * z, z, 1.59576912f), s);
-    }
-    return 1.f;
-}
-
 // dZ = dD slope(Z), and the column sums of dZ (FP32, before its rounding) of the
 // workgroup's rows.  A workgroup takes 512 columns of `chunk` rows, 16 at a time:
 // 8 columns a lane, its four waves every fourth row.  A wave's loads of the 16
@@ -311,10 +269,9 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
         return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: sizes must be positive (M may be 0)");
     if (!aligned(dD, 16) || !aligned(Z, 16) || !aligned(dZ, 16) || !aligned(dbias, 4) || !aligned(m_indices, 4))
         return set_error(DG_ERR_ALIGNMENT, "epilogue_backward: dD, Z and dZ must be 16-byte, the rest 4-byte aligned");
-    int chunk = 128;
-    while (chunk > kStep && ((int64_t)rows + chunk - 1) / chunk * ((N + 511) / 512) < kBackwardGroups) chunk /= 2;
+    const int chunk = backward_chunk(rows, N);
     const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
-    if (G > 65535 || N > 65535 * 512 || !fits_launch(chunks) || !fits_launch((N + kSumCols - 1) / kSumCols, 64 * kSumWaves))
+    if (N > 65535 * 512 || !fits_launch(chunks) || !column_sums_fit(N, G))
         return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many rows, groups or columns for one launch");
     float* partial = nullptr;
     StreamScratch scratch;               // held until both kernels are launched
@@ -333,17 +290,23 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
         if (s != DG_OK) return s;
     }
     if (!dbias) return DG_OK;
-    return launch_rows("epilogue_backward (bias)", dg_bias_sum_kernel, dim3((N + kSumCols - 1) / kSumCols, G), 64 * kSumWaves, stream,
-                       BiasSumArgs{partial, m_indices, dbias, chunks, chunk, N});
+    return column_sums("epilogue_backward (bias)", partial, m_indices, chunks, chunk, N, G, dbias, stream);
 }
 
 }  // namespace
 
-dg_status column_sums(const char* what, const float* partial, int chunks, int N, float* out, void* stream) {
-    if (!fits_launch((N + kSumCols - 1) / kSumCols, 64 * kSumWaves))
-        return set_error(DG_ERR_UNSUPPORTED, std::string(what) + ": too many columns for one launch");
-    return launch_rows(what, dg_bias_sum_kernel, dim3((N + kSumCols - 1) / kSumCols), 64 * kSumWaves, stream,
-                       BiasSumArgs{partial, nullptr, out, chunks, 1, N});
+int backward_chunk(int rows, int N) {
+    int chunk = 128;
+    while (chunk > kStep && ((int64_t)rows + chunk - 1) / chunk * ((N + 511) / 512) < kBackwardGroups) chunk /= 2;
+    return chunk;
+}
+
+bool column_sums_fit(int N, int G) { return G <= 65535 && fits_launch((N + kSumCols - 1) / kSumCols, 64 * kSumWaves); }
+
+dg_status column_sums(const char* what, const float* partial, const int32_t* m_indices, int chunks, int chunk, int N,
+                      int G, float* out, void* stream) {
+    return launch_rows(what, dg_bias_sum_kernel, dim3((N + kSumCols - 1) / kSumCols, G), 64 * kSumWaves, stream,
+                       BiasSumArgs{partial, m_indices, out, chunks, chunk, N});
 }
 
 dg_status transpose_bf16(const void* x, void* xt, int groups, int rows_k, int cols, int k_end, int64_t pitch,

@@ -18,41 +18,7 @@ namespace {
 // The largest row: 1024 lanes of 8 chunks.
 constexpr int kMaxWidth = 65536;
 
-// Eight BF16 from column c of a row of H; zeros past H.  Rows of any width: with H no
-// multiple of 8 a row starts at any even address, which 16-byte loads and stores take.
-__device__ __forceinline__ u32x4 load8(const u16* row, int c, int H) {
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if (c + 8 <= H) {
-        __builtin_memcpy(&w, row + c, 16);
-    } else if (c < H) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i) {
-            const u32 v = c + i < H ? row[c + i] : (u16)0;
-            w[i >> 1] |= v << (16 * (i & 1));
-        }
-    }
-    return w;
-}
-__device__ __forceinline__ void store8(u16* row, int c, int H, u32x4 w) {
-    if (c + 8 <= H) {
-        __builtin_memcpy(row + c, &w, 16);
-    } else if (c < H) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (c + i < H) row[c + i] = (u16)(w[i >> 1] >> (16 * (i & 1)));
-    }
-}
-__device__ __forceinline__ void unpack8(u32x4 w, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
-__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
-    return u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]), to_bf16x2(v[6], v[7])};
-}
-// ... of the weight, FP32 or BF16 (4- or 2-byte aligned)
+// Eight elements of the weight, FP32 or BF16
 __device__ __forceinline__ void load_weight(const void* weight, int wide, int c, int H, float (&w)[8]) {
     if (!weight) {
 #pragma unroll
@@ -70,11 +36,6 @@ __device__ __forceinline__ void load_weight(const void* weight, int wide, int c,
     }
 }
 
-// Rotation by D lanes within each 16: four of them bring a 16-lane sum or maximum to all 16.
-template <int D>
-__device__ __forceinline__ u32 rotate16(u32 v) {
-    return (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + D, 0xf, 0xf, true);
-}
 template <int D>
 __device__ __forceinline__ float add_rotated(float v) {
     return v + __builtin_bit_cast(float, rotate16<D>(__builtin_bit_cast(u32, v)));
@@ -85,14 +46,6 @@ __device__ __forceinline__ float wave_sum(float v) {
         return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
     };
     return (part(0) + part(16)) + (part(32) + part(48));
-}
-template <int D>
-__device__ __forceinline__ u32 max_rotated(u32 v) {
-    const u32 o = rotate16<D>(v);
-    return o > v ? o : v;
-}
-__device__ __forceinline__ u32 max16(u32 v) {
-    return max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(v))));
 }
 
 // Workgroups go to the 8 XCDs in turn.  Here XCD x takes the x-th eighth of the rows, so that
@@ -413,7 +366,7 @@ dg_status dg_rms_norm_backward(const void* dY, const void* S, const void* weight
                                                         weight_type == DG_TYPE_F32, T, H});
             if (s != DG_OK) return s;
         }
-        return dweight ? column_sums("rms_norm_backward (weight)", partial, (int)grid, H, dweight, stream) : DG_OK;
+        return dweight ? column_sums("rms_norm_backward (weight)", partial, nullptr, (int)grid, 1, H, 1, dweight, stream) : DG_OK;
     });
 }
 

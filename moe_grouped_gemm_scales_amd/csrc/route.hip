@@ -48,13 +48,8 @@ __device__ __forceinline__ float wave_max(float v) {
     for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
     return v;
 }
-template <int D>
-__device__ __forceinline__ u32 max_rotated(u32 v) {
-    const u32 o = (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + D, 0xf, 0xf, true);
-    return o > v ? o : v;
-}
 __device__ __forceinline__ u32 wave_max(u32 v) {
-    v = max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(v))));
+    v = max16(v);
     auto part = [&](int lane) { return (u32)__builtin_amdgcn_readlane((int)v, lane); };
     const u32 a = part(0), b = part(16), c = part(32), d = part(48);
     const u32 x = a > b ? a : b, y = c > d ? c : d;

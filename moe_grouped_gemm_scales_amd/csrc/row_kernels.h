@@ -1,5 +1,5 @@
-// What the kernels over BF16 rows share (moe.hip, linear.hip): conversions, and
-// the launch of a kernel that takes one by-value struct.
+// What the kernels over rows share: conversions, loads and stores of eight elements,
+// steps across lanes, and the launch of a kernel that takes one by-value struct.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -39,6 +39,55 @@ __device__ __forceinline__ u32x4 load_spread(const u16* p, int c, int N) {
     for (int i = 0; i < 4; ++i)
         w[i] = (c + 128 * i < N ? v[2 * i] : 0u) | (c + 128 * i + 64 < N ? v[2 * i + 1] << 16 : 0u);
     return w;
+}
+
+// Eight BF16 from column c of a row of H; zeros past H.  Rows of any width: with H no
+// multiple of 8 a row starts at any even address, which 16-byte loads and stores take.
+__device__ __forceinline__ u32x4 load8(const u16* row, int c, int H) {
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (c + 8 <= H) {
+        __builtin_memcpy(&w, row + c, 16);
+    } else if (c < H) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i) {
+            const u32 v = c + i < H ? row[c + i] : (u16)0;
+            w[i >> 1] |= v << (16 * (i & 1));
+        }
+    }
+    return w;
+}
+__device__ __forceinline__ void store8(u16* row, int c, int H, u32x4 w) {
+    if (c + 8 <= H) {
+        __builtin_memcpy(row + c, &w, 16);
+    } else if (c < H) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (c + i < H) row[c + i] = (u16)(w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+__device__ __forceinline__ void unpack8(u32x4 w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+    return u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]), to_bf16x2(v[6], v[7])};
+}
+
+// Rotation by D lanes within each 16: four of them bring a 16-lane sum or maximum to all 16.
+template <int D>
+__device__ __forceinline__ u32 rotate16(u32 v) {
+    return (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + D, 0xf, 0xf, true);
+}
+template <int D>
+__device__ __forceinline__ u32 max_rotated(u32 v) {
+    const u32 o = rotate16<D>(v);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ u32 max16(u32 v) {
+    return max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(v))));
 }
 
 inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

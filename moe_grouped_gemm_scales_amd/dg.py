@@ -137,6 +137,10 @@ def _load():
                        ("dg_k_grouped_bf16_gemm_tn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_moe_route", [vp, i32] + [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_moe_route_backward", [vp, i32] + [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_checkpoint_fp8", [vp] * 4 + [i32] * 2 + [vp]),
+                       ("dg_checkpoint_restore", [vp] * 4 + [i32] * 2 + [vp]),
+                       ("dg_epilogue_backward_fp8", [vp] * 3 + [i32] + [vp] * 3 + [i32] * 2 + [vp]),
+                       ("dg_m_grouped_epilogue_backward_fp8_contiguous", [vp] * 3 + [i32] + [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_rms_norm", [vp] * 2 + [i32] * 2 + [vp]),
                        ("dg_rms_norm_backward", [vp] * 3 + [i32, ctypes.c_float] + [vp] * 3 + [i32] * 2 + [vp]),
                        ("dg_moe_combine", [vp] * 5 + [i32] * 4 + [vp]),
@@ -1282,3 +1286,58 @@ def dg_moe_route_backward(logits, expert_ids, d_weights, d_logits, score="softma
     if status:
         _check(status)
     return d_logits
+
+
+# ---------------------------------------------------------------- 8-bit checkpoints
+def _kept_args(x, name, codes, scales, dev):
+    """(address of x [M,N], codes, scales)."""
+    M, N = x.shape
+    return (_arg(x, name, _BF, (M, N), dev), _fp8_arg(codes, "codes", (M, N), dev),
+            _arg(scales, "scales", torch.uint8, (M, _cdiv(N, 128)), dev))
+
+
+def dg_checkpoint_fp8(X, codes, scales, m_indices=None, stream=None):
+    """Keep X [M,N] bfloat16 in 8 bits: codes [M,N] E4M3, scales uint8 [M,ceil(N/128)] (E8M0, one per 1x128 block).
+
+    m_indices int32 [M] (contiguous layout): rows with -1 are kept as zeros, other negative ones are left alone."""
+    M, N = _rows_of(X, "X")
+    dev = _on(X, "X")
+    x, c, s = _kept_args(X, "X", codes, scales, dev)
+    status = lib.dg_checkpoint_fp8(x, _opt(m_indices, "m_indices", _I32, (M,), dev), c, s, M, N, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return codes
+
+
+def dg_checkpoint_restore(codes, scales, X, m_indices=None, stream=None):
+    """X [M,N] bfloat16 from what dg_checkpoint_fp8 kept of it."""
+    M, N = _rows_of(X, "X")
+    dev = _on(X, "X")
+    x, c, s = _kept_args(X, "X", codes, scales, dev)
+    status = lib.dg_checkpoint_restore(c, s, _opt(m_indices, "m_indices", _I32, (M,), dev), x, M, N,
+                                       _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return X
+
+
+def dg_epilogue_backward_fp8(dD, codes, scales, activation, dZ, dbias, H=None, m_indices=None, stream=None,
+                             num_experts=None):
+    """dg_epilogue_backward on a Z kept by dg_checkpoint_fp8: dZ = dD * activation'(Z), dbias = its column sums, and
+    H = activation(Z) bfloat16 [M,N]; each may be None.  num_experts as there."""
+    M, N = _rows_of(dD, "dD")
+    act, dev = _activation(activation), _on(dD, "dD")
+    args = (*_kept_args(dD, "dD", codes, scales, dev), act)
+    out = (_opt(dZ, "dZ", _BF, (M, N), dev), _opt(H, "H", _BF, (M, N), dev))
+    if m_indices is None:
+        status = lib.dg_epilogue_backward_fp8(*args, *out, _opt(dbias, "dbias", _F32, (N,), dev), M, N,
+                                              _raw_stream(stream, dev))
+    else:
+        # (65535: the most that the library takes)
+        G = num_experts if num_experts is not None else 65535 if dbias is None else dbias.shape[0]
+        status = lib.dg_m_grouped_epilogue_backward_fp8_contiguous(
+            *args, _arg(m_indices, "m_indices", _I32, (M,), dev), *out, _opt(dbias, "dbias", _F32, (G, N), dev), M, N, G,
+            _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return dZ

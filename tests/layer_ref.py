@@ -109,3 +109,54 @@ def route_backward(logits, ids, d_weights, score, renormalise, scale):
             if renormalise:                          # the sum is zero: only the chosen get a gradient
                 out[t] = p[t] * dp
     return out, mag
+
+
+# ------------------------------------------------------------------ 8-bit checkpoints
+def keep(x, m_indices=None):
+    """(values x 2^-e [M,N] before the code's rounding, exponent bytes [M,ceil(N/128)]) of BF16 rows."""
+    M, N = x.shape
+    x = x.double()
+    if m_indices is not None:
+        x = torch.where((m_indices >= 0)[:, None], x, torch.zeros_like(x))
+    B = -(-N // 128)
+    e = torch.empty((M, B), dtype=torch.uint8)
+    v = torch.empty_like(x)
+    for t in range(M):
+        for b in range(B):
+            block = x[t, 128 * b:128 * b + 128]
+            top = float(block.abs().max())
+            if not bool(torch.isfinite(block).all()):
+                e[t, b], v[t, 128 * b:128 * b + 128] = 255, math.nan
+                continue
+            k = 0 if top == 0 else -126
+            while top > 448 * 2.0 ** k:
+                k += 1
+            block = block * 2.0 ** -k
+            if k == 120:                     # 256 2^120 is past BF16's largest number
+                block = block.clamp(-240, 240)
+            e[t, b], v[t, 128 * b:128 * b + 128] = k + 127, block
+    return v, e
+
+
+def kept_values(codes, scales):
+    """Values of codes [M,N] (uint8) with exponent bytes."""
+    s = torch.where(scales == 255, torch.full((), math.nan, dtype=torch.float64), torch.exp2(scales.double() - 127))
+    v = codes.view(torch.float8_e4m3fn).double()
+    return v * s.repeat_interleave(128, 1)[:, :v.shape[1]]
+
+
+def activation(z, name):
+    """(activation, slope) of 64-bit z."""
+    if name == "relu":
+        return torch.relu(z), (z > 0).double()
+    if name == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * torch.sigmoid(-z)
+    if name == "gelu":
+        phi = 0.5 * torch.erfc(-z / math.sqrt(2))
+        return z * phi, phi + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if name == "gelu_tanh":
+        u = 2 * math.sqrt(2 / math.pi)
+        s = torch.sigmoid(u * (z + 0.044715 * z ** 3))
+        return z * s, s + z * s * (1 - s) * u * (1 + 0.134145 * z * z)
+    return z, torch.ones_like(z)
