@@ -35,7 +35,7 @@
  *   - M, M_max or T may be 0; an array without elements may then be NULL.
  *   - The library owns its compiled-kernel cache and a per-stream device
  *     workspace (split-K partials and arrival counters; the K-contiguous copies
- *     of K-outermost operands, a sort's counts, a bias or weight gradient's partial sums),
+ *     of K-outermost operands, a sort's counts, a bias or weight gradient's partial sums, a low-rank product),
  *     created on first use (or by dg_init) and kept until process exit.  The
  *     first call for a new shape compiles a kernel (hipRTC) and may allocate;
  *     later calls with the same shape neither compile nor allocate.  Host
@@ -46,7 +46,8 @@
  *     Two graphs that captured calls on the same stream share its workspace
  *     too, so they must not be replayed concurrently (on other streams) when
  *     their calls use it: split-K (few rows, long K), a K-contiguous rewrite, a
- *     sort of more than 4096 assignments, a bias gradient, a norm's weight gradient.  That races on what
+ *     sort of more than 4096 assignments, a bias gradient, a norm's weight
+ *     gradient, low-rank adapters.  That races on what
  *     they keep there and is unsupported.
  *     A call that compiles or allocates cannot run under stream capture: make
  *     the first call of each shape on each stream eagerly, then capture.
@@ -378,6 +379,33 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue(const void *A, const in
                                                          int num_groups, void *stream);
 
 /*
+ * Low-rank adapters of many requests at once beside a shared product, for
+ * serving: row m of a batch belongs to a request with adapter a = adapter[m],
+ *
+ *     Z[m] = A[m] . B^T + scale[a] (A[m] . down[a]^T) . up[a]^T + bias,   D = activation(Z) + residual
+ *
+ * and D and Z as for dg_bf16_gemm_nt_epilogue (epilogue NULL: D = Z).
+ *   down  BF16 [num_adapters][rank][K], up BF16 [num_adapters][N][rank]; rank a multiple of 8
+ *         up to 256 (an adapter of a smaller rank: zeros behind it)
+ *   adapter int32 [M]: in any order, one a row; outside [0, num_adapters): none, the row's
+ *         plain product
+ *   scale FP32 [num_adapters] or NULL (1)
+ * FP32 throughout up to the one rounding of D and of Z; the inner product, low =
+ * scale (A down^T), stays FP32 (as two BF16 where matrix instructions take it, 2^-17).
+ * Rows of other adapters see nothing of one that holds an infinity or NaN.
+ * down and up must be 16-byte, adapter and scale 4-byte aligned; M at most 2^24.
+ * low stands in the stream's workspace, M * rank (rounded up to 32) * 4 bytes.
+ */
+typedef struct {
+    const void *down, *up;
+    const int32_t *adapter;
+    const float *scale;     /* or NULL */
+    int num_adapters, rank;
+} dg_lora;
+dg_status dg_bf16_gemm_nt_lora(const void *A, const void *B, const dg_lora *lora, const dg_epilogue *epilogue, void *D,
+                               int M, int N, int K, void *stream);
+
+/*
  * Backward pass of the fused epilogue.  With dD the gradient of D [M][N] and Z
  * as the forward call stored it:
  *   dZ = dD * activation'(Z)             BF16 [M][N] (the one rounding; may be dD itself, or NULL)
@@ -680,6 +708,7 @@ dg_status dg_init(void);
 #define DG_EPI_BIAS_BF16 0x200
 #define DG_EPI_RESIDUAL 0x400
 #define DG_EPI_Z 0x800
+#define DG_EPI_LORA 0x8000   /* the rows' low-rank adapters (dense BF16) */
 #define DG_EPI_ACT(a) ((a) << 12)
 
 /*

@@ -31,3 +31,4 @@ from .dg import (ACTIVATIONS, EPI_BIAS_BF16, EPI_BIAS_F32, EPI_RESIDUAL, EPI_Z, 
 from .dg import dg_rms_norm, dg_rms_norm_backward  # noqa: F401
 from .dg import SCORES, dg_moe_route, dg_moe_route_backward  # noqa: F401
 from .dg import dg_checkpoint_fp8, dg_checkpoint_restore, dg_epilogue_backward_fp8  # noqa: F401
+from .dg import EPI_LORA, dg_bf16_gemm_nt_lora  # noqa: F401

@@ -5,7 +5,8 @@ compiler against the ROCm headers, plus HIP sources compiled for gfx950 by hipcc
 (csrc/device.hip: the library's status words and its measurement probes;
 csrc/moe.hip: tokens to expert rows and back; csrc/linear.hip: the backward
 side of the products with a fused epilogue; csrc/norm.hip: the norm in front of them;
-csrc/route.hip: the router's choice; csrc/checkpoint.hip: activations kept in 8 bits); the GEMM kernel source is embedded into the library as text and
+csrc/route.hip: the router's choice; csrc/checkpoint.hip: activations kept in 8 bits;
+csrc/lora.hip: the first product of low-rank adapters); the GEMM kernel source is embedded into the library as text and
 compiled for gfx950 by hipRTC at run time, once per shape.  ``precompile()`` runs that hipRTC step ahead of time
 (no GPU needed) so that the code objects of the standard workloads sit in the
 in-tree cache and the device source is known to compile for gfx950.
@@ -27,7 +28,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 HOST_SOURCES = ["api.cpp", "jit.cpp", "heuristics.cpp"]
 DEVICE_SOURCES = ["device.hip", "moe.hip", "linear.hip", "norm.hip", "route.hip",
-                  "checkpoint.hip"]
+                  "checkpoint.hip", "lora.hip"]
 BUILD_DIR = os.path.join(PKG, "_build")
 # every HIP source is compiled for gfx950 with packed FP32 instructions off
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -49,7 +49,9 @@ struct LaunchParamsEpilogue {
     LaunchParams lp;
     EpilogueArgs ep;
 };
-static_assert(sizeof(LaunchParamsEpilogue) == 120 && offsetof(LaunchParamsEpilogue, ep) == 96, "the kernel reads this layout");
+static_assert(sizeof(LaunchParamsEpilogue) == 152 && offsetof(LaunchParamsEpilogue, ep) == 96 &&
+                  offsetof(EpilogueArgs, low) == 24 && offsetof(EpilogueArgs, adapters) == 48,
+              "the kernel reads this layout (without adapters its first 120 bytes)");
 
 struct Workspace {
     float* partials = nullptr;
@@ -251,7 +253,8 @@ dg_status check_common(const void* A, const void* sfa, const void* B, const void
 // instead of the stream's workspace, and nothing is allocated.
 dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B, const void* sfb,
                  const int32_t* grp, const float* C, void* D, void* stream_ptr, bool noalloc = false,
-                 const EpilogueArgs& ep = {}) {
+                 const EpilogueArgs& epilogue = {}, const LoraArgs* lora = nullptr) {
+    EpilogueArgs ep = epilogue;
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     const bool rewrite = !p.direct && (p.kind == kKGrouped || p.a_k_outer || p.b_k_outer);
     // what the sizes do not say about the kernels
@@ -265,7 +268,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
                                    fnv1a_str(std::getenv("DG_FORCE_CONFIG"), 14695981039346656037ull));
     const int limit = g_num_cus_limit.load(std::memory_order_relaxed);
     WarmCall& w = t_warm;
-    if (!noalloc && !rewrite && w.plan && w.kind == p.kind && w.rows == p.rows && w.n == p.n && w.k == p.k &&
+    if (!noalloc && !rewrite && !lora && w.plan && w.kind == p.kind && w.rows == p.rows && w.n == p.n && w.k == p.k &&
         w.g == p.g && w.has_c == p.has_c && w.sf == p.sf && w.extra == extra && w.dev == dev_now && w.stream == stream &&
         w.env == env && w.limit == limit)
         return launch_segments(*w.plan, p, A, sfa, B, sfb, grp, C, D, stream, w.partials, w.counters, w.status, ep);
@@ -424,6 +427,16 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
         partials = ws->partials;
         counters = ws->counters;
     }
+    // low-rank adapters: their first product's result in the stream's workspace
+    if (lora) {
+        uint8_t* buf = nullptr;
+        const size_t need = (size_t)p.rows * (size_t)lora_pitch(lora->rank) * sizeof(float);
+        s = ensure_kmajor(*st, stream, std::max(need, size_t(8) << 20), &buf);
+        if (s != DG_OK) return s;
+        ep.low = reinterpret_cast<const float*>(buf);
+        s = lora_down(*lora, A, reinterpret_cast<float*>(buf), p.rows, p.k / 2, stream_ptr);
+        if (s != DG_OK) return s;
+    }
     const bool print = env_flag("DG_PRINT_CONFIGS");
     if (print)
         for (const Segment& seg : it->second.segs)
@@ -431,7 +444,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
                          seg.grid, seg.cfg.threads(), (long long)seg.items, seg.cfg.lds_bytes());
     s = launch_segments(it->second, p, A, sfa, B, sfb, grp, C, D, stream, partials, counters, st->status, ep);
     if (s != DG_OK) return s;
-    if (!rewrite && !print) {
+    if (!rewrite && !lora && !print) {
         WarmCall& r = t_warm;
         r.kind = p.kind; r.rows = p.rows; r.n = p.n; r.k = p.k; r.g = p.g; r.has_c = p.has_c; r.sf = p.sf; r.extra = extra;
         r.dev = dev; r.limit = limit; r.env = env; r.stream = stream; r.plan = &it->second;
@@ -531,7 +544,10 @@ dg_status read_epilogue(const dg_epilogue* e, Epilogue* ep, EpilogueArgs* args) 
     ep->act = e->activation;
     ep->res = e->residual ? 1 : 0;
     ep->zout = e->Z ? 1 : 0;
-    *args = EpilogueArgs{e->bias, e->residual, e->Z};
+    *args = EpilogueArgs{};
+    args->bias = e->bias;
+    args->res = e->residual;
+    args->z = e->Z;
     return DG_OK;
 }
 
@@ -544,7 +560,7 @@ bool reads_k_outermost(int64_t cols, int64_t K) {
 // BF16 x BF16, the three M forms: no scales; the kernels count K in bytes
 dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, const float* C, void* D, int rows,
                     int N, int K, int num_groups, void* stream, int b_k_outer = 0, const Epilogue& ep = {},
-                    const EpilogueArgs& args = {}, bool any_k = false) {
+                    const EpilogueArgs& args = {}, bool any_k = false, const LoraArgs* lora = nullptr) {
     if ((rows != 0 && (!A || !D)) || !B) return set_error(DG_ERR_INVALID_ARG, "A, B and D must be non-NULL");
     if (rows < 0 || N <= 0 || K <= 0) return set_error(DG_ERR_INVALID_ARG, "sizes must be positive (M may be 0)");
     if (K % 64 != 0 && !any_k)
@@ -570,7 +586,7 @@ dg_status bf16_gemm(int kind, const void* A, const void* B, const int32_t* grp, 
     p.k_tail = K % 64 ? K : 0;
     p.direct = b_k_outer && !p.k_tail && reads_k_outermost(N, K);
     p.ep = ep;
-    return launch(p, A, nullptr, B, nullptr, grp, C, D, stream, false, args);
+    return launch(p, A, nullptr, B, nullptr, grp, C, D, stream, false, args, lora);
 }
 
 // The problem of a BF16 TN product.  Read as stored, K is no constant of the
@@ -685,8 +701,9 @@ Epilogue epilogue_flags(int* kind) {
     ep.bias = (*kind & DG_EPI_BIAS_BF16) ? 2 : (*kind & DG_EPI_BIAS_F32) ? 1 : 0;
     ep.res = (*kind & DG_EPI_RESIDUAL) ? 1 : 0;
     ep.zout = (*kind & DG_EPI_Z) ? 1 : 0;
+    ep.lora = (*kind & DG_EPI_LORA) ? 1 : 0;
     ep.act = (*kind >> 12) & 7;
-    *kind &= ~(DG_EPI_BIAS_F32 | DG_EPI_BIAS_BF16 | DG_EPI_RESIDUAL | DG_EPI_Z | DG_EPI_ACT(7));
+    *kind &= ~(DG_EPI_BIAS_F32 | DG_EPI_BIAS_BF16 | DG_EPI_RESIDUAL | DG_EPI_Z | DG_EPI_LORA | DG_EPI_ACT(7));
     return ep;
 }
 
@@ -703,7 +720,7 @@ dg_status described_problem(int kind, int rows, int N, int K, int num_groups, in
     const Epilogue ep = epilogue_flags(&kind);
     const int sf = scale_format(&kind);
     if (kind < 0 || kind > 3 || rows <= 0 || N <= 0 || K <= 0 || num_groups <= 0 || ep.act > DG_ACT_GELU_TANH ||
-        (nn && sf != 3))
+        (nn && sf != 3) || (ep.lora && (kind != kDense || sf != 3 || nn)))
         return set_error(DG_ERR_INVALID_ARG, "bad arguments");
     if (K % (sf != 3 ? 128 : kind == kKGrouped || nn ? 1 : 64))
         return set_error(DG_ERR_UNSUPPORTED, "K must be a multiple of 128 (BF16: 64)");
@@ -896,6 +913,33 @@ dg_status dg_bf16_gemm_nt_epilogue(const void* A, const void* B, const dg_epilog
         EpilogueArgs args;
         dg_status s = read_epilogue(epilogue, &ep, &args);
         return s != DG_OK ? s : bf16_gemm(kDense, A, B, nullptr, nullptr, D, M, N, K, 1, stream, 0, ep, args);
+    });
+}
+
+dg_status dg_bf16_gemm_nt_lora(const void* A, const void* B, const dg_lora* lora, const dg_epilogue* epilogue, void* D,
+                               int M, int N, int K, void* stream) {
+    return guarded([&]() -> dg_status {
+        if (!lora) return set_error(DG_ERR_INVALID_ARG, "lora must be non-NULL");
+        const dg_lora l = *lora;
+        if (l.num_adapters <= 0 || l.rank <= 0)
+            return set_error(DG_ERR_INVALID_ARG, "lora: num_adapters and rank must be positive");
+        if (!l.down || !l.up || (M != 0 && !l.adapter)) return set_error(DG_ERR_INVALID_ARG, "lora: NULL pointer");
+        if (l.rank % 8 || l.rank > 256) return set_error(DG_ERR_UNSUPPORTED, "lora: rank must be a multiple of 8 up to 256");
+        if (!aligned(l.down, 16) || !aligned(l.up, 16) || !aligned(l.adapter, 4) || !aligned(l.scale, 4))
+            return set_error(DG_ERR_ALIGNMENT, "lora: down and up must be 16-byte, adapter and scale 4-byte aligned");
+        if (M > (1 << 24)) return set_error(DG_ERR_UNSUPPORTED, "lora: more than 2^24 rows");
+        Epilogue ep;
+        EpilogueArgs args;
+        const dg_epilogue plain{};
+        dg_status s = read_epilogue(epilogue ? epilogue : &plain, &ep, &args);
+        if (s != DG_OK) return s;
+        ep.lora = 1;
+        args.up = l.up;
+        args.adapter = l.adapter;
+        args.adapters = l.num_adapters;
+        args.rank = l.rank;
+        const LoraArgs down{l.down, l.scale, l.adapter, l.num_adapters, l.rank};
+        return bf16_gemm(kDense, A, B, nullptr, nullptr, D, M, N, K, 1, stream, 0, ep, args, false, &down);
     });
 }
 

@@ -21,15 +21,31 @@ struct Epilogue {
     int act = 0;               // dg_activation
     int res = 0;               // residual added
     int zout = 0;              // pre-activation stored
-    bool any() const { return bias || act || res || zout; }
-    int code() const { return ((bias * 8 + act) * 2 + res) * 2 + zout; }
+    int lora = 0;              // the rows' low-rank adapters added
+    bool any() const { return bias || act || res || zout || lora; }
+    int code() const { return (((lora * 4 + bias) * 8 + act) * 2 + res) * 2 + zout; }
 };
 // ... and its tensors
 struct EpilogueArgs {
     const void* bias = nullptr;
     const void* res = nullptr;
     void* z = nullptr;
+    // low-rank adapters: scale (A down^T) of each row [M][lora_pitch(rank)], and the second factors
+    const float* low = nullptr;
+    const void* up = nullptr;
+    const int32_t* adapter = nullptr;
+    int adapters = 0, rank = 0;
 };
+// ... and what their first product takes
+struct LoraArgs {
+    const void* down = nullptr;
+    const float* scale = nullptr;
+    const int32_t* adapter = nullptr;
+    int adapters = 0, rank = 0;
+};
+inline int lora_pitch(int rank) { return (rank + 31) / 32 * 32; }
+// low [M][lora_pitch(rank)] = scale (A down[adapter]^T) of the rows that have an adapter (lora.hip)
+dg_status lora_down(const LoraArgs& l, const void* A, float* low, int M, int K, void* stream);
 
 // One compiled specialisation of the kernel.  Everything here becomes a -D
 // macro of the hipRTC compile; N and K are compile-time constants (the

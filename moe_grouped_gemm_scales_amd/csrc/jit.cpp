@@ -74,6 +74,7 @@ std::vector<std::string> compile_options(const KernelConfig& c) {
         def("DG_ACT", c.ep.act);
         def("DG_RES", c.ep.res);
         def("DG_ZOUT", c.ep.zout);
+        if (c.ep.lora) def("DG_LORA", 1);
     }
     if (c.a_kout) def("DG_A_KOUT", 1);
     if (c.b_kout) def("DG_B_KOUT", 1);
@@ -202,7 +203,7 @@ std::string KernelConfig::key() const {
     if (sf == 4) s << "_f4f4";
     if (sf == 5) s << "_e8m0x2";
     if (a_kout || b_kout) s << (a_kout ? "_tn" : "_nn");
-    if (ep.any()) s << "_ep" << ep.bias << ep.act << ep.res << ep.zout;
+    if (ep.any()) s << "_ep" << ep.bias << ep.act << ep.res << ep.zout << (ep.lora ? "_lora" : "");
     if (ne > 0) s << "_cols" << nb << "-" << ne;
     return s.str();
 }

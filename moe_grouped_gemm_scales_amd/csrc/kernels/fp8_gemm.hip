@@ -122,6 +122,11 @@ typedef u16 v4u16 __attribute__((ext_vector_type(4)));
 #ifndef DG_ZOUT
 #define DG_ZOUT 0
 #endif
+// DG_LORA (dense): the row's low-rank adapter is added in front of the bias,
+// Z = A . B^T + up[adapter] low^T + bias, with low [M][rank] from a kernel of its own
+#ifndef DG_LORA
+#define DG_LORA 0
+#endif
 // K-outermost operands read as they are stored (BF16, variant 0 and the split
 // refill): DG_B_KOUT: B [K][N] (grouped [G][K][N]); DG_A_KOUT: A [K][M] (K-grouped
 // only).  The matrix core wants each lane's K values side by side, so the
@@ -132,7 +137,7 @@ typedef u16 v4u16 __attribute__((ext_vector_type(4)));
 #ifndef DG_B_KOUT
 #define DG_B_KOUT 0
 #endif
-#define DG_EPI (DG_BIAS || DG_ACT || DG_RES || DG_ZOUT)
+#define DG_EPI (DG_BIAS || DG_ACT || DG_RES || DG_ZOUT || DG_LORA)
 // Contiguous forms of these products (variant 0): work items are those of the row
 // blocks that are in use (used_row_blocks)
 #define DG_USED_ROWS (DG_KIND == 1 && (DG_EPI || DG_B_KOUT) && DG_VARIANT == 0)
@@ -220,6 +225,12 @@ struct Params {
     const u16* res;
     u16* z;
 #endif
+#if DG_LORA
+    const float* low;      // [M][rank, rounded up to 32]
+    const u16* up;         // [adapters][N][rank]
+    const int* adapter;    // [M]
+    int adapters, rank;
+#endif
 #if DG_USED_ROWS
     int row_blocks = 0;    // of the rows that are in use
 #endif
@@ -248,12 +259,21 @@ struct KernArgs {
     const DG_GLOBAL u8* bias;
     const DG_GLOBAL u16* res;
     DG_GLOBAL u16* z;
+#if DG_LORA
+    const DG_GLOBAL float* low;
+    const DG_GLOBAL u16* up;
+    const DG_GLOBAL int* adapter;
+    int adapters, rank;
+#define DG_EPI_ARGS , (const u8*)ka.bias, (const u16*)ka.res, (u16*)ka.z, (const float*)ka.low, (const u16*)ka.up, \
+                    (const int*)ka.adapter, ka.adapters, ka.rank
+#else
 #define DG_EPI_ARGS , (const u8*)ka.bias, (const u16*)ka.res, (u16*)ka.z
+#endif
 #else
 #define DG_EPI_ARGS
 #endif
 };
-static_assert(sizeof(KernArgs) == (DG_EPI ? 120 : 96) && __builtin_offsetof(KernArgs, M) == 72 &&
+static_assert(sizeof(KernArgs) == (DG_LORA ? 152 : DG_EPI ? 120 : 96) && __builtin_offsetof(KernArgs, M) == 72 &&
               __builtin_offsetof(KernArgs, status) == 88, "the host fills this layout");
 
 // Promotion scale of one MFMA result: one FP32 per (row, 128-row block of B),
@@ -652,6 +672,120 @@ __device__ __forceinline__ void store_pair(u16* base, u64 row_off, int n, bool o
                                               : v4i{(int)lo0, (int)hi0, (int)r_lo, (int)r_hi};
 }
 
+#if DG_LORA
+// acc += up[adapter of the row] low^T over the rank, for the wave's rows.
+//   few different adapters among them (prompts): adapter after adapter, matrix instructions over 32 ranks at a time,
+//     low's FP32 as the sum of two BF16 (2^-17 of it left).  The product of another adapter's rows is dropped, not
+//     multiplied by zero: an adapter that holds an infinity must not reach other requests.
+//   many (decode, every row its own): each lane gathers the ranks of its four columns for its own rows.
+// A turn of the first way is a chain of loads, about 2000 clocks; the gather reads TM TN rank / 2 pieces of 16 bytes a
+// lane, which the CU takes in at about 64 a clock and wave of four: 32 TM TN rank clocks.
+template <int TM_, int TN_>
+__device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4f (&acc)[TM_][TN_], int row0, int col0) {
+    const int R = p.rank, pitch = (R + 31) & ~31;
+    const int l16 = row0 & 15, q = (col0 >> 2) & 3;
+    int ad[TM_];                            // of the lane's rows; -1: none
+#pragma unroll
+    for (int a = 0; a < TM_; ++a) {
+        const int r = row0 + 16 * a;
+        ad[a] = r < tl.row_limit ? p.adapter[tl.m0 + r] : -1;
+        if ((u32)ad[a] >= (u32)p.adapters) ad[a] = -1;
+    }
+    // the least adapter above `cur` among the wave's rows (the same in all lanes); -1 past the last
+    auto next_after = [&](int cur) {
+        u32 n = 0xffffffffu;
+#pragma unroll
+        for (int a = 0; a < TM_; ++a) n = ad[a] > cur && (u32)ad[a] < n ? (u32)ad[a] : n;
+        auto least = [&](u32 o) { n = o < n ? o : n; };
+        least((u32)__builtin_amdgcn_update_dpp(0, (int)n, 0x128, 0xf, 0xf, true));    // rotations within 16 lanes
+        least((u32)__builtin_amdgcn_update_dpp(0, (int)n, 0x124, 0xf, 0xf, true));
+        least((u32)__builtin_amdgcn_update_dpp(0, (int)n, 0x122, 0xf, 0xf, true));
+        least((u32)__builtin_amdgcn_update_dpp(0, (int)n, 0x121, 0xf, 0xf, true));
+        return __builtin_amdgcn_readfirstlane((int)n);
+    };
+    const int most = TM_ * TN_ * R / 64 + 1;
+    int turns = 0;
+    for (int cur = next_after(-1); cur >= 0 && turns <= most; cur = next_after(cur)) ++turns;
+    if (turns <= most) {
+        for (int cur = next_after(-1); cur >= 0; cur = next_after(cur)) {
+            for (int k0 = 0; k0 < R; k0 += 32) {
+                const int k = k0 + 8 * q;
+                v8bf up[TN_];
+#pragma unroll
+                for (int b = 0; b < TN_; ++b) {
+                    const int n = tl.n0 + col0 - 4 * q + 16 * b + l16;
+                    v4i w = {0, 0, 0, 0};
+                    if (k < R && n < N_END) w = *(const v4i*)(p.up + ((u64)cur * N + n) * R + k);
+                    up[b] = __builtin_bit_cast(v8bf, w);
+                }
+#pragma unroll
+                for (int a = 0; a < TM_; ++a) {
+                    const u64 mine = __ballot(ad[a] == cur);
+                    if (mine == 0) continue;                      // (the same for the whole wave)
+                    v4f h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
+                    if (ad[a] == cur) {
+                        const float* low = p.low + (u64)(tl.m0 + row0 + 16 * a) * pitch + k;
+                        h0 = *(const v4f*)low;
+                        h1 = *(const v4f*)(low + 4);
+                    }
+                    v8bf hi, lo;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        hi[e] = (__bf16)h0[e];
+                        lo[e] = (__bf16)(h0[e] - (float)hi[e]);
+                        hi[e + 4] = (__bf16)h1[e];
+                        lo[e + 4] = (__bf16)(h1[e] - (float)hi[e + 4]);
+                    }
+                    const bool all = mine == ~0ull;
+#pragma unroll
+                    for (int b = 0; b < TN_; ++b) {
+                        const v4f before = acc[a][b];
+                        v4f sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(up[b], lo, before, 0, 0, 0);
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(up[b], hi, sum, 0, 0, 0);
+                        acc[a][b] = all || ad[a] == cur ? sum : before;
+                    }
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int a = 0; a < TM_; ++a) {
+            if (ad[a] < 0) continue;
+            const float* low = p.low + (u64)(tl.m0 + row0 + 16 * a) * pitch;
+            const u16* up = p.up + (u64)ad[a] * N * R;
+            for (int k = 0; k < R; k += 8) {
+                const v4f h0 = *(const v4f*)(low + k), h1 = *(const v4f*)(low + k + 4);
+                v4i w[TN_][4];
+#pragma unroll
+                for (int b = 0; b < TN_; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int n = tl.n0 + col0 + 16 * b + e;
+                        w[b][e] = *(const v4i*)(up + (u64)(n < N_END ? n : N_END - 1) * R + k);     // (dropped past the end)
+                    }
+#pragma unroll
+                for (int b = 0; b < TN_; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const v4f u0 = bf16x4(v2u32{(u32)w[b][e].x, (u32)w[b][e].y});
+                        const v4f u1 = bf16x4(v2u32{(u32)w[b][e].z, (u32)w[b][e].w});
+                        float sum = acc[a][b][e];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum = __builtin_fmaf(u0[i], h0[i], sum);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum = __builtin_fmaf(u1[i], h1[i], sum);
+                        acc[a][b][e] = sum;
+                    }
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < TM_; ++a)
+#pragma unroll
+        for (int b = 0; b < TN_; ++b) asm volatile("" : "+v"(acc[a][b]));        // (as in finish_tile)
+}
+#endif
+
 // D = act(acc + bias) + residual of the rows that may be stored, and Z = acc +
 // bias where it is kept.  Everything stays in FP32 up to the one rounding of each
 // output.  The bias of the lane's columns is read once for all its rows, and a
@@ -878,6 +1012,9 @@ __device__ __forceinline__ void finish_tile(const Params& p, const Tile& tl, v4f
     if constexpr (kKind == 2 || kKind == 3) row_base = ((u64)tl.g * p.M + tl.m0) * N;
     else row_base = (u64)tl.m0 * N;
 #if DG_EPI
+#if DG_LORA
+    add_low_rank<TM_, TN_>(p, tl, acc, row0, col0);
+#endif
     fused_epilogue<TM_, TN_, GRP_LDS>(p, tl, acc, row0, col0, grp_lds, row_base);
     return;
 #endif

@@ -1,0 +1,117 @@
+// Low-rank adapters of many requests beside a shared product (hipcc, gfx950): the
+// first of their two products, low = scale (A down[adapter]^T).  The second is
+// added in the shared product's epilogue (kernels/fp8_gemm.hip).  The operation
+// is specified in include/dg.h.
+//
+// One workgroup takes 16 rows of A and up to 64 ranks; its eight waves take every
+// eighth 64 of K, on the matrix cores straight from global memory (an operand's 16
+// rows are 128 bytes each a step), and their sums meet in LDS.  What it reads
+// bounds it: A once, and an adapter once for each 16 rows that use it.
+#include "row_kernels.h"
+
+namespace dg {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kRows = 16;
+constexpr int kWaves = 8;
+
+struct DownArgs {
+    const u16* A;
+    const u16* down;
+    const int* adapter;
+    const float* scale;
+    float* low;
+    int M, K, adapters, rank, pitch;
+};
+
+// SUBS: 16-rank pieces of a workgroup.  EACH: grid z is a row of the 16, and the workgroup does
+// the adapter of that row if no earlier row has the same (decode: up to 16 adapters side by side);
+// otherwise one workgroup does all adapters of its rows in turn (prompts: mostly one).
+template <int SUBS, bool EACH>
+__global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, q = lane >> 4;
+    const int m = (int)blockIdx.x * kRows + l16;
+    const int r0 = (int)blockIdx.y * 64;
+    int ad = m < a.M ? a.adapter[m] : -1;
+    if ((u32)ad >= (u32)a.adapters) ad = -1;
+    u32 todo = (u32)__ballot(ad >= 0) & 0xffffu;
+    if constexpr (EACH) {
+        const u32 z = blockIdx.z;
+        const int of_z = __builtin_amdgcn_readlane(ad, (int)z);
+        const u32 same = (u32)__ballot(ad == of_z) & 0xffffu;
+        if (of_z < 0 || (u32)__builtin_ctz(same) != z) return;
+        todo = same;
+    }
+    if (todo == 0u) return;
+    f32x4 sum[SUBS];
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) sum[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bool done = false;                               // this lane's row
+    const u16* rows = a.A + (u64)(m < a.M ? m : a.M - 1) * (u64)a.K;
+    while (todo) {
+        const int mine = __builtin_amdgcn_readlane(ad, __builtin_ctz(todo));
+        todo &= ~((u32)__ballot(ad == mine) & 0xffffu);
+        const u16* down = a.down + (u64)mine * (u64)a.rank * (u64)a.K;
+        f32x4 acc[SUBS];
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int k0 = wave * 64; k0 < a.K; k0 += kWaves * 64) {
+            bf16x8 x[2], d[SUBS][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = k0 + 32 * h + 8 * q;
+                x[h] = *(const bf16x8*)(rows + k);
+#pragma unroll
+                for (int s = 0; s < SUBS; ++s) {
+                    // ranks past the last read the last one; their results are not kept
+                    const int r = r0 + 16 * s + l16;
+                    d[s][h] = *(const bf16x8*)(down + (u64)(r < a.rank ? r : a.rank - 1) * (u64)a.K + k);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < SUBS; ++s) acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[s][h], x[h], acc[s], 0, 0, 0);
+        }
+        // (a select: another adapter's rows keep their own sums, whatever this one made of them)
+        if (ad == mine) {
+            done = true;
+#pragma unroll
+            for (int s = 0; s < SUBS; ++s) sum[s] = acc[s];
+        }
+    }
+    __shared__ f32x4 parts[kWaves][SUBS][64];
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) parts[wave][s][lane] = sum[s];
+    __syncthreads();
+    // wave s adds piece s in wave order: lane (row l16, ranks 4 q ..)
+    if (wave >= SUBS || !done) return;
+    f32x4 t = parts[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) t += parts[w][wave][lane];
+    const int r = r0 + 16 * wave + 4 * q;
+    if (r >= a.pitch) return;
+    const float scale = a.scale ? a.scale[ad] : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = r + e < a.rank ? scale * t[e] : 0.f;
+    *(f32x4*)(a.low + (u64)m * (u64)a.pitch + r) = t;
+}
+
+}  // namespace
+
+dg_status lora_down(const LoraArgs& l, const void* A, float* low, int M, int K, void* stream) {
+    const int pitch = lora_pitch(l.rank);
+    const DownArgs args{static_cast<const u16*>(A), static_cast<const u16*>(l.down), l.adapter, l.scale, low, M, K,
+                        l.adapters, l.rank, pitch};
+    // side by side up to 512 rows: 16 times the workgroups, most of which end at once where prompts fill the tiles
+    const bool each = M <= 512;
+    const dim3 grid((M + kRows - 1) / kRows, (pitch + 63) / 64, each ? kRows : 1);
+    auto* kernel = pitch <= 32 ? (each ? dg_lora_down_kernel<2, true> : dg_lora_down_kernel<2, false>)
+                               : (each ? dg_lora_down_kernel<4, true> : dg_lora_down_kernel<4, false>);
+    return launch_rows("lora (down)", kernel, grid, 64 * kWaves, stream, args);
+}
+
+}  // namespace dg

@@ -137,6 +137,7 @@ def _load():
                        ("dg_k_grouped_bf16_gemm_tn_contiguous", [vp] * 5 + [i32] * 4 + [vp]),
                        ("dg_moe_route", [vp, i32] + [vp] * 4 + [i32] * 3 + [vp]),
                        ("dg_moe_route_backward", [vp, i32] + [vp] * 4 + [i32] * 3 + [vp]),
+                       ("dg_bf16_gemm_nt_lora", [vp] * 5 + [i32] * 3 + [vp]),
                        ("dg_checkpoint_fp8", [vp] * 4 + [i32] * 2 + [vp]),
                        ("dg_checkpoint_restore", [vp] * 4 + [i32] * 2 + [vp]),
                        ("dg_epilogue_backward_fp8", [vp] * 3 + [i32] + [vp] * 3 + [i32] * 2 + [vp]),
@@ -931,7 +932,7 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # d
 
 
 # OR into `kind` of precompile / describe_config, with activation << 12
-EPI_BIAS_F32, EPI_BIAS_BF16, EPI_RESIDUAL, EPI_Z = 0x100, 0x200, 0x400, 0x800
+EPI_BIAS_F32, EPI_BIAS_BF16, EPI_RESIDUAL, EPI_Z, EPI_LORA = 0x100, 0x200, 0x400, 0x800, 0x8000
 
 
 class _Epilogue(ctypes.Structure):      # dg_epilogue
@@ -1341,3 +1342,34 @@ def dg_epilogue_backward_fp8(dD, codes, scales, activation, dZ, dbias, H=None, m
     if status:
         _check(status)
     return dZ
+
+
+# ---------------------------------------------------------------- low-rank adapters
+class _Lora(ctypes.Structure):          # dg_lora
+    _fields_ = [("down", ctypes.c_void_p), ("up", ctypes.c_void_p), ("adapter", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("num_adapters", ctypes.c_int), ("rank", ctypes.c_int)]
+
+
+def dg_bf16_gemm_nt_lora(A, B, down, up, adapter, D, scale=None, bias=None, activation="none", residual=None, Z=None,
+                         stream=None):
+    """dg_bf16_gemm_nt_epilogue with each row's low-rank adapter added to the product:
+
+    Z = A @ B.T + scale[a] * (A @ down[a].T) @ up[a].T + bias with a = adapter[row]; D = activation(Z) + residual.
+    down [L,rank,K], up [L,N,rank] bfloat16 (rank a multiple of 8), adapter int32 [M] (outside [0, L): none),
+    scale float32 [L] or None (1)."""
+    M, K = A.shape
+    N = B.shape[0]
+    if down.dim() != 3 or up.dim() != 3:
+        raise ValueError("down must be [L, rank, K], up [L, N, rank]")
+    L, R = down.shape[0], down.shape[1]
+    if max(M, N, K, L, R) > _INT_MAX:
+        _too_many("sizes", max(M, N, K, L, R))
+    dev = _on(A, "A")
+    e = _epilogue(D, (N,), bias, activation, residual, Z, dev)
+    lora = _Lora(_arg(down, "down", _BF, (L, R, K), dev), _arg(up, "up", _BF, (L, N, R), dev),
+                 _arg(adapter, "adapter", _I32, (M,), dev), _opt(scale, "scale", _F32, (L,), dev), L, R)
+    status = lib.dg_bf16_gemm_nt_lora(_arg(A, "A", _BF, (M, K), dev), _arg(B, "B", _BF, (N, K), dev), ctypes.byref(lora), e,
+                                      _arg(D, "D", _BF, (M, N), dev), M, N, K, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return D

@@ -160,3 +160,21 @@ def activation(z, name):
         s = torch.sigmoid(u * (z + 0.044715 * z ** 3))
         return z * s, s + z * s * (1 - s) * u * (1 + 0.134145 * z * z)
     return z, torch.ones_like(z)
+
+
+# ------------------------------------------------------------------ low-rank adapters
+def lora(a, b, down, up, adapter, scale, bias):
+    """(Z, magnitudes of the shared product's and of the adapters' terms)."""
+    a = a.double()
+    z, base = a @ b.double().t(), a.abs() @ b.double().abs().t()
+    low = torch.zeros_like(z)
+    for i in range(down.shape[0]):
+        r = torch.nonzero(adapter == i)[:, 0]
+        if not len(r):
+            continue
+        s = 1.0 if scale is None else float(scale[i])
+        z[r] += s * (a[r] @ down[i].double().t()) @ up[i].double().t()
+        low[r] += abs(s) * (a[r].abs() @ down[i].double().abs().t()) @ up[i].double().abs().t()
+    if bias is not None:
+        z, base = z + bias.double(), base + bias.double().abs()
+    return z, base, low
