@@ -30,8 +30,9 @@ struct EpilogueArgs {
     const void* bias = nullptr;
     const void* res = nullptr;
     void* z = nullptr;
-    // low-rank adapters: scale (A down^T) of each row [M][lora_pitch(rank)], and the second factors
-    const float* low = nullptr;
+    // low-rank adapters: scale (A down^T) of each row, [M][2][lora_pitch(rank)] BF16 (the value, and what its
+    // rounding leaves), and the second factors
+    const void* low = nullptr;
     const void* up = nullptr;
     const int32_t* adapter = nullptr;
     int adapters = 0, rank = 0;
@@ -44,8 +45,8 @@ struct LoraArgs {
     int adapters = 0, rank = 0;
 };
 inline int lora_pitch(int rank) { return (rank + 31) / 32 * 32; }
-// low [M][lora_pitch(rank)] = scale (A down[adapter]^T) of the rows that have an adapter (lora.hip)
-dg_status lora_down(const LoraArgs& l, const void* A, float* low, int M, int K, void* stream);
+// low [M][2][lora_pitch(rank)] = scale (A down[adapter]^T) of the rows that have an adapter (lora.hip)
+dg_status lora_down(const LoraArgs& l, const void* A, void* low, int M, int K, void* stream);
 
 // One compiled specialisation of the kernel.  Everything here becomes a -D
 // macro of the hipRTC compile; N and K are compile-time constants (the

@@ -226,7 +226,7 @@ struct Params {
     u16* z;
 #endif
 #if DG_LORA
-    const float* low;      // [M][rank, rounded up to 32]
+    const u16* low;        // [M][2][rank, rounded up to 32]: BF16, and BF16 of what that leaves
     const u16* up;         // [adapters][N][rank]
     const int* adapter;    // [M]
     int adapters, rank;
@@ -260,11 +260,11 @@ struct KernArgs {
     const DG_GLOBAL u16* res;
     DG_GLOBAL u16* z;
 #if DG_LORA
-    const DG_GLOBAL float* low;
+    const DG_GLOBAL u16* low;
     const DG_GLOBAL u16* up;
     const DG_GLOBAL int* adapter;
     int adapters, rank;
-#define DG_EPI_ARGS , (const u8*)ka.bias, (const u16*)ka.res, (u16*)ka.z, (const float*)ka.low, (const u16*)ka.up, \
+#define DG_EPI_ARGS , (const u8*)ka.bias, (const u16*)ka.res, (u16*)ka.z, (const u16*)ka.low, (const u16*)ka.up, \
                     (const int*)ka.adapter, ka.adapters, ka.rank
 #else
 #define DG_EPI_ARGS , (const u8*)ka.bias, (const u16*)ka.res, (u16*)ka.z
@@ -675,7 +675,7 @@ __device__ __forceinline__ void store_pair(u16* base, u64 row_off, int n, bool o
 #if DG_LORA
 // acc += up[adapter of the row] low^T over the rank, for the wave's rows.
 //   few different adapters among them (prompts): adapter after adapter, matrix instructions over 32 ranks at a time,
-//     low's FP32 as the sum of two BF16 (2^-17 of it left).  The product of another adapter's rows is dropped, not
+//     low as the sum of two BF16 (2^-17 of it left).  The product of another adapter's rows is dropped, not
 //     multiplied by zero: an adapter that holds an infinity must not reach other requests.
 //   many (decode, every row its own): each lane gathers the ranks of its four columns for its own rows.
 // A turn of the first way is a chain of loads, about 2000 clocks; the gather reads TM TN rank / 2 pieces of 16 bytes a
@@ -703,72 +703,98 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
         least((u32)__builtin_amdgcn_update_dpp(0, (int)n, 0x121, 0xf, 0xf, true));
         return __builtin_amdgcn_readfirstlane((int)n);
     };
+    // low of row a's ranks k .. k + 7: BF16 and, `pitch` on, what it leaves of the FP32 value (a uniform base and
+    // 32-bit offsets, here and below: 64-bit addresses a lane spill)
+    const u16* const low_tile = p.low + (u64)(u32)tl.m0 * (u32)(2 * pitch);
+    auto low_of = [&](int a, int k) { return low_tile + (u32)((row0 + 16 * a) * 2 * pitch + k); };
+    // (a wave of more sub-tiles has no registers for the gather: 65 of them spilled, and up to 64 turns it is)
+    constexpr bool GATHER = TM_ * TN_ <= 16;
     const int most = TM_ * TN_ * R / 64 + 1;
     int turns = 0;
-    for (int cur = next_after(-1); cur >= 0 && turns <= most; cur = next_after(cur)) ++turns;
+    if constexpr (GATHER)
+        for (int cur = next_after(-1); cur >= 0 && turns <= most; cur = next_after(cur)) ++turns;
     if (turns <= most) {
-        for (int cur = next_after(-1); cur >= 0; cur = next_after(cur)) {
-            for (int k0 = 0; k0 < R; k0 += 32) {
-                const int k = k0 + 8 * q;
-                v8bf up[TN_];
+        // the factors of the next rows, in tiles with the registers for it of the next 32 ranks too, are on their way
+        // while one is multiplied
+        constexpr bool AHEAD = TM_ * TN_ <= 16;
+        v8bf up[TN_], up_next[TN_];
+        auto read_up = [&](int cur, int k) {
+            const u16* const of = p.up + (u64)(u32)cur * (u64)(u32)(N * R);
 #pragma unroll
-                for (int b = 0; b < TN_; ++b) {
-                    const int n = tl.n0 + col0 - 4 * q + 16 * b + l16;
-                    v4i w = {0, 0, 0, 0};
-                    if (k < R && n < N_END) w = *(const v4i*)(p.up + ((u64)cur * N + n) * R + k);
-                    up[b] = __builtin_bit_cast(v8bf, w);
+            for (int b = 0; b < TN_; ++b) {
+                const int n = tl.n0 + col0 - 4 * q + 16 * b + l16;
+                v4i w = {0, 0, 0, 0};
+                if (k < R && n < N_END) w = *(const v4i*)(of + (u32)(n * R + k));
+                up_next[b] = __builtin_bit_cast(v8bf, w);
+            }
+        };
+        for (int cur = next_after(-1); cur >= 0; cur = next_after(cur)) {
+            if constexpr (AHEAD) read_up(cur, 8 * q);
+            for (int k0 = 0; k0 < R; k0 += 32) {
+                if constexpr (!AHEAD) read_up(cur, k0 + 8 * q);
+                v4i hi[3], lo[3];
+                auto read_low = [&](int a) {
+                    hi[a % 3] = lo[a % 3] = v4i{0, 0, 0, 0};
+                    if (ad[a] == cur) {
+                        const u16* low = low_of(a, k0 + 8 * q);
+                        hi[a % 3] = *(const v4i*)low;
+                        lo[a % 3] = *(const v4i*)(low + pitch);
+                    }
+                };
+                read_low(0);
+                if constexpr (TM_ > 1) read_low(1);
+#pragma unroll
+                for (int b = 0; b < TN_; ++b) up[b] = up_next[b];
+                if constexpr (AHEAD) {
+                    if (k0 + 32 < R) read_up(cur, k0 + 32 + 8 * q);
                 }
 #pragma unroll
                 for (int a = 0; a < TM_; ++a) {
+                    if (a + 2 < TM_) read_low(a + 2);
                     const u64 mine = __ballot(ad[a] == cur);
                     if (mine == 0) continue;                      // (the same for the whole wave)
-                    v4f h0 = {0.f, 0.f, 0.f, 0.f}, h1 = h0;
-                    if (ad[a] == cur) {
-                        const float* low = p.low + (u64)(tl.m0 + row0 + 16 * a) * pitch + k;
-                        h0 = *(const v4f*)low;
-                        h1 = *(const v4f*)(low + 4);
-                    }
-                    v8bf hi, lo;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        hi[e] = (__bf16)h0[e];
-                        lo[e] = (__bf16)(h0[e] - (float)hi[e]);
-                        hi[e + 4] = (__bf16)h1[e];
-                        lo[e + 4] = (__bf16)(h1[e] - (float)hi[e + 4]);
-                    }
-                    const bool all = mine == ~0ull;
+                    const bool keep = mine == ~0ull || ad[a] == cur;
+                    const v8bf h = __builtin_bit_cast(v8bf, hi[a % 3]), l = __builtin_bit_cast(v8bf, lo[a % 3]);
 #pragma unroll
                     for (int b = 0; b < TN_; ++b) {
                         const v4f before = acc[a][b];
-                        v4f sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(up[b], lo, before, 0, 0, 0);
-                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(up[b], hi, sum, 0, 0, 0);
-                        acc[a][b] = all || ad[a] == cur ? sum : before;
+                        v4f sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(up[b], l, before, 0, 0, 0);
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(up[b], h, sum, 0, 0, 0);
+                        acc[a][b] = keep ? sum : before;
                     }
                 }
             }
         }
-    } else {
+    } else if constexpr (GATHER) {
 #pragma unroll
         for (int a = 0; a < TM_; ++a) {
             if (ad[a] < 0) continue;
-            const float* low = p.low + (u64)(tl.m0 + row0 + 16 * a) * pitch;
-            const u16* up = p.up + (u64)ad[a] * N * R;
+            // (columns past the end read the last one, and are dropped)
+            const int n = tl.n0 + col0, past = n < N_END ? N_END - 1 - n : 0;
+            const u16* const up = p.up + ((u64)(u32)ad[a] * (u32)N + (u32)(n < N_END ? n : N_END - 1)) * (u64)(u32)R;
+            // (small tiles have the registers for two pieces' loads at once)
+#pragma unroll(TM_ * TN_ <= 8 ? 2 : 1)
             for (int k = 0; k < R; k += 8) {
-                const v4f h0 = *(const v4f*)(low + k), h1 = *(const v4f*)(low + k + 4);
-                v4i w[TN_][4];
+                // opaque, so that the addresses of a piece are made where it is read and not kept for all pieces
+                const u16* piece = up + k;
+                int most_n = past, step = R;
+                asm volatile("" : "+v"(piece), "+v"(most_n), "+s"(step));
+                const v4i hi = *(const v4i*)low_of(a, k), lo = *(const v4i*)(low_of(a, k) + pitch);
+                const v4f h0 = bf16x4(v2u32{(u32)hi.x, (u32)hi.y}) + bf16x4(v2u32{(u32)lo.x, (u32)lo.y});
+                const v4f h1 = bf16x4(v2u32{(u32)hi.z, (u32)hi.w}) + bf16x4(v2u32{(u32)lo.z, (u32)lo.w});
 #pragma unroll
-                for (int b = 0; b < TN_; ++b)
+                for (int b = 0; b < TN_; ++b) {
+                    if constexpr (TM_ * TN_ > 8) __builtin_amdgcn_sched_barrier(0);
+                    v4i w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int n = tl.n0 + col0 + 16 * b + e;
-                        w[b][e] = *(const v4i*)(up + (u64)(n < N_END ? n : N_END - 1) * R + k);     // (dropped past the end)
+                        const int d = 16 * b + e < most_n ? 16 * b + e : most_n;
+                        w[e] = *(const v4i*)(piece + (u32)(d * step));
                     }
 #pragma unroll
-                for (int b = 0; b < TN_; ++b)
-#pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const v4f u0 = bf16x4(v2u32{(u32)w[b][e].x, (u32)w[b][e].y});
-                        const v4f u1 = bf16x4(v2u32{(u32)w[b][e].z, (u32)w[b][e].w});
+                        const v4f u0 = bf16x4(v2u32{(u32)w[e].x, (u32)w[e].y});
+                        const v4f u1 = bf16x4(v2u32{(u32)w[e].z, (u32)w[e].w});
                         float sum = acc[a][b][e];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum = __builtin_fmaf(u0[i], h0[i], sum);
@@ -776,6 +802,7 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
                         for (int i = 0; i < 4; ++i) sum = __builtin_fmaf(u1[i], h1[i], sum);
                         acc[a][b][e] = sum;
                     }
+                }
             }
         }
     }

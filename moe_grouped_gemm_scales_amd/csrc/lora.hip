@@ -3,8 +3,8 @@
 // added in the shared product's epilogue (kernels/fp8_gemm.hip).  The operation
 // is specified in include/dg.h.
 //
-// One workgroup takes 16 rows of A and up to 64 ranks; its eight waves take every
-// eighth 64 of K, on the matrix cores straight from global memory (an operand's 16
+// One workgroup takes 16 rows of A and up to 64 ranks; its sixteen waves take a
+// sixteenth of K each, on the matrix cores straight from global memory (an operand's 16
 // rows are 128 bytes each a step), and their sums meet in LDS.  What it reads
 // bounds it: A once, and an adapter once for each 16 rows that use it.
 #include "row_kernels.h"
@@ -15,18 +15,18 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRows = 16;
-constexpr int kWaves = 8;
+constexpr int kWaves = 16;
 
 struct DownArgs {
     const u16* A;
     const u16* down;
     const int* adapter;
     const float* scale;
-    float* low;
+    u16* low;
     int M, K, adapters, rank, pitch;
 };
 
-// SUBS: 16-rank pieces of a workgroup.  EACH: grid z is a row of the 16, and the workgroup does
+// SUBS: 16-rank pieces of a workgroup (1, 2 or 4; a workgroup has 16 SUBS ranks).  EACH: grid z is a row of the 16, and the workgroup does
 // the adapter of that row if no earlier row has the same (decode: up to 16 adapters side by side);
 // otherwise one workgroup does all adapters of its rows in turn (prompts: mostly one).
 template <int SUBS, bool EACH>
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, q = lane >> 4;
     const int m = (int)blockIdx.x * kRows + l16;
-    const int r0 = (int)blockIdx.y * 64;
+    const int r0 = (int)blockIdx.y * (16 * SUBS);
     int ad = m < a.M ? a.adapter[m] : -1;
     if ((u32)ad >= (u32)a.adapters) ad = -1;
     u32 todo = (u32)__ballot(ad >= 0) & 0xffffu;
@@ -50,26 +50,32 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
 #pragma unroll
     for (int s = 0; s < SUBS; ++s) sum[s] = f32x4{0.f, 0.f, 0.f, 0.f};
     bool done = false;                               // this lane's row
-    const u16* rows = a.A + (u64)(m < a.M ? m : a.M - 1) * (u64)a.K;
+    // a wave's share of K, in steps of 64: waves a sixteenth of a row apart read different memory channels,
+    // where neighbouring steps of all rows (4 KB apart at K = 2048) would meet in a few
+    const int steps = a.K / 64;
+    const int k_begin = steps * wave / kWaves * 64, k_end = steps * (wave + 1) / kWaves * 64;
+    const u16* rows = a.A + (u64)(m < a.M ? m : a.M - 1) * (u64)a.K + 8 * q;
     while (todo) {
         const int mine = __builtin_amdgcn_readlane(ad, __builtin_ctz(todo));
         todo &= ~((u32)__ballot(ad == mine) & 0xffffu);
-        const u16* down = a.down + (u64)mine * (u64)a.rank * (u64)a.K;
+        const u16* down[SUBS];
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) {
+            // ranks past the last read the last one; their results are not kept
+            const int r = r0 + 16 * s + l16;
+            down[s] = a.down + ((u64)mine * (u64)a.rank + (u32)(r < a.rank ? r : a.rank - 1)) * (u64)a.K + 8 * q;
+        }
         f32x4 acc[SUBS];
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int k0 = wave * 64; k0 < a.K; k0 += kWaves * 64) {
+#pragma unroll 2
+        for (int k = k_begin; k < k_end; k += 64) {
             bf16x8 x[2], d[SUBS][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int k = k0 + 32 * h + 8 * q;
-                x[h] = *(const bf16x8*)(rows + k);
+                x[h] = *(const bf16x8*)(rows + k + 32 * h);
 #pragma unroll
-                for (int s = 0; s < SUBS; ++s) {
-                    // ranks past the last read the last one; their results are not kept
-                    const int r = r0 + 16 * s + l16;
-                    d[s][h] = *(const bf16x8*)(down + (u64)(r < a.rank ? r : a.rank - 1) * (u64)a.K + k);
-                }
+                for (int s = 0; s < SUBS; ++s) d[s][h] = *(const bf16x8*)(down[s] + k + 32 * h);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -87,30 +93,44 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
 #pragma unroll
     for (int s = 0; s < SUBS; ++s) parts[wave][s][lane] = sum[s];
     __syncthreads();
-    // wave s adds piece s in wave order: lane (row l16, ranks 4 q ..)
+    // wave s adds piece s in wave order: lane (row l16, ranks 4 q ..); the last piece also clears the ranks up to the pitch
     if (wave >= SUBS || !done) return;
     f32x4 t = parts[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) t += parts[w][wave][lane];
     const int r = r0 + 16 * wave + 4 * q;
-    if (r >= a.pitch) return;
     const float scale = a.scale ? a.scale[ad] : 1.f;
+    u16* to = a.low + (u64)m * (u32)(2 * a.pitch);
+    if (r < a.pitch) {
+        u64 hi = 0, lo = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] = r + e < a.rank ? scale * t[e] : 0.f;
-    *(f32x4*)(a.low + (u64)m * (u64)a.pitch + r) = t;
+        for (int e = 0; e < 4; ++e) {
+            const float v = r + e < a.rank ? scale * t[e] : 0.f;
+            const u16 h = to_bf16(v);
+            hi |= (u64)h << (16 * e);
+            lo |= (u64)to_bf16(v - bf16_lo(h)) << (16 * e);
+        }
+        *(u64*)(to + r) = hi;
+        *(u64*)(to + a.pitch + r) = lo;
+    }
+    if constexpr (SUBS == 1) {
+        if (r + 16 < a.pitch) *(u64*)(to + r + 16) = *(u64*)(to + a.pitch + r + 16) = 0;
+    }
 }
 
 }  // namespace
 
-dg_status lora_down(const LoraArgs& l, const void* A, float* low, int M, int K, void* stream) {
+dg_status lora_down(const LoraArgs& l, const void* A, void* low, int M, int K, void* stream) {
     const int pitch = lora_pitch(l.rank);
-    const DownArgs args{static_cast<const u16*>(A), static_cast<const u16*>(l.down), l.adapter, l.scale, low, M, K,
+    const DownArgs args{static_cast<const u16*>(A), static_cast<const u16*>(l.down), l.adapter, l.scale, static_cast<u16*>(low), M, K,
                         l.adapters, l.rank, pitch};
     // side by side up to 512 rows: 16 times the workgroups, most of which end at once where prompts fill the tiles
     const bool each = M <= 512;
-    const dim3 grid((M + kRows - 1) / kRows, (pitch + 63) / 64, each ? kRows : 1);
-    auto* kernel = pitch <= 32 ? (each ? dg_lora_down_kernel<2, true> : dg_lora_down_kernel<2, false>)
-                               : (each ? dg_lora_down_kernel<4, true> : dg_lora_down_kernel<4, false>);
+    const int subs = l.rank <= 16 ? 1 : l.rank <= 32 ? 2 : 4;
+    const dim3 grid((M + kRows - 1) / kRows, (l.rank + 16 * subs - 1) / (16 * subs), each ? kRows : 1);
+    auto* kernel = subs == 1 ? (each ? dg_lora_down_kernel<1, true> : dg_lora_down_kernel<1, false>)
+                 : subs == 2 ? (each ? dg_lora_down_kernel<2, true> : dg_lora_down_kernel<2, false>)
+                             : (each ? dg_lora_down_kernel<4, true> : dg_lora_down_kernel<4, false>);
     return launch_rows("lora (down)", kernel, grid, 64 * kWaves, stream, args);
 }
 
