@@ -430,8 +430,7 @@ dg_status launch(const Problem& p, const void* A, const void* sfa, const void* B
     // low-rank adapters: their first product's result in the stream's workspace
     if (lora) {
         uint8_t* buf = nullptr;
-        const size_t need = (size_t)p.rows * (size_t)lora_pitch(lora->rank) * 2 * sizeof(uint16_t);
-        s = ensure_kmajor(*st, stream, std::max(need, size_t(8) << 20), &buf);
+        s = ensure_kmajor(*st, stream, std::max(lora_bytes(p.rows, lora->rank), size_t(8) << 20), &buf);
         if (s != DG_OK) return s;
         ep.low = buf;
         s = lora_down(*lora, A, buf, p.rows, p.k / 2, stream_ptr);

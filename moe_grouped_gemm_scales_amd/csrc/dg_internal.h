@@ -30,8 +30,8 @@ struct EpilogueArgs {
     const void* bias = nullptr;
     const void* res = nullptr;
     void* z = nullptr;
-    // low-rank adapters: scale (A down^T) of each row, [M][2][lora_pitch(rank)] BF16 (the value, and what its
-    // rounding leaves), and the second factors
+    // low-rank adapters: scale (A down^T) of each row as operands of 16 rows and 32 ranks (lora_bytes of them,
+    // layout in lora.hip), and the second factors
     const void* low = nullptr;
     const void* up = nullptr;
     const int32_t* adapter = nullptr;
@@ -45,7 +45,9 @@ struct LoraArgs {
     int adapters = 0, rank = 0;
 };
 inline int lora_pitch(int rank) { return (rank + 31) / 32 * 32; }
-// low [M][2][lora_pitch(rank)] = scale (A down[adapter]^T) of the rows that have an adapter (lora.hip)
+// ... of M rows: BF16 values and what their rounding leaves, rows and ranks filled up to 16 and 32
+inline size_t lora_bytes(int M, int rank) { return ((size_t)M + 15) / 16 * 16 * (size_t)lora_pitch(rank) * 4; }
+// low = scale (A down[adapter]^T) of the rows that have an adapter (lora.hip)
 dg_status lora_down(const LoraArgs& l, const void* A, void* low, int M, int K, void* stream);
 
 // One compiled specialisation of the kernel.  Everything here becomes a -D

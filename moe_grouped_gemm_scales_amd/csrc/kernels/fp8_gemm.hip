@@ -226,7 +226,8 @@ struct Params {
     u16* z;
 #endif
 #if DG_LORA
-    const u16* low;        // [M][2][rank, rounded up to 32]: BF16, and BF16 of what that leaves
+    const u16* low;        // [M / 16][rank / 32][2][64 lanes][8], both rounded up: the MFMA operands of 16 rows and
+                           // 32 ranks, BF16 and BF16 of what that leaves
     const u16* up;         // [adapters][N][rank]
     const int* adapter;    // [M]
     int adapters, rank;
@@ -703,10 +704,12 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
         least((u32)__builtin_amdgcn_update_dpp(0, (int)n, 0x121, 0xf, 0xf, true));
         return __builtin_amdgcn_readfirstlane((int)n);
     };
-    // low of row a's ranks k .. k + 7: BF16 and, `pitch` on, what it leaves of the FP32 value (a uniform base and
+    // low of row a's ranks k .. k + 7: BF16 and, 512 on, what it leaves of the FP32 value (a uniform base and
     // 32-bit offsets, here and below: 64-bit addresses a lane spill)
-    const u16* const low_tile = p.low + (u64)(u32)tl.m0 * (u32)(2 * pitch);
-    auto low_of = [&](int a, int k) { return low_tile + (u32)((row0 + 16 * a) * 2 * pitch + k); };
+    const u16* const low_tile = p.low + (u64)(u32)(tl.m0 / 16) * (u32)(pitch * 32);
+    auto low_of = [&](int a, int k) {
+        return low_tile + (u32)((row0 / 16 + a) * (pitch * 32) + (k / 32) * 1024 + ((k & 31) / 8 * 16 + l16) * 8);
+    };
     // (a wave of more sub-tiles has no registers for the gather: 65 of them spilled, and up to 64 turns it is)
     constexpr bool GATHER = TM_ * TN_ <= 16;
     const int most = TM_ * TN_ * R / 64 + 1;
@@ -717,36 +720,46 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
         // the factors of the next rows, in tiles with the registers for it of the next 32 ranks too, are on their way
         // while one is multiplied
         constexpr bool AHEAD = TM_ * TN_ <= 16;
-        v8bf up[TN_], up_next[TN_];
-        auto read_up = [&](int cur, int k) {
+        // (up's rows are read with four lanes a row, 64 bytes side by side, and then each lane gets the operand's
+        // piece q of row l16: read as the operand lies, every lane is a request of its own)
+        v4i up_next[TN_];
+        const int lane = 16 * q + l16, from = 4 * (4 * l16 + q);
+        auto read_up = [&](int cur, int k0) {
             const u16* const of = p.up + (u64)(u32)cur * (u64)(u32)(N * R);
+            const int k = k0 + 8 * (lane & 3);
 #pragma unroll
             for (int b = 0; b < TN_; ++b) {
-                const int n = tl.n0 + col0 - 4 * q + 16 * b + l16;
-                v4i w = {0, 0, 0, 0};
-                if (k < R && n < N_END) w = *(const v4i*)(of + (u32)(n * R + k));
-                up_next[b] = __builtin_bit_cast(v8bf, w);
+                const int n = tl.n0 + col0 - 4 * q + 16 * b + (lane >> 2);
+                up_next[b] = v4i{0, 0, 0, 0};
+                if (k < R && n < N_END) up_next[b] = *(const v4i*)(of + (u32)(n * R + k));
             }
         };
+        auto operand = [&](v4i w) {
+            v4i v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_ds_bpermute(from, w[i]);
+            return __builtin_bit_cast(v8bf, v);
+        };
         for (int cur = next_after(-1); cur >= 0; cur = next_after(cur)) {
-            if constexpr (AHEAD) read_up(cur, 8 * q);
+            if constexpr (AHEAD) read_up(cur, 0);
             for (int k0 = 0; k0 < R; k0 += 32) {
-                if constexpr (!AHEAD) read_up(cur, k0 + 8 * q);
+                if constexpr (!AHEAD) read_up(cur, k0);
                 v4i hi[3], lo[3];
                 auto read_low = [&](int a) {
                     hi[a % 3] = lo[a % 3] = v4i{0, 0, 0, 0};
                     if (ad[a] == cur) {
                         const u16* low = low_of(a, k0 + 8 * q);
                         hi[a % 3] = *(const v4i*)low;
-                        lo[a % 3] = *(const v4i*)(low + pitch);
+                        lo[a % 3] = *(const v4i*)(low + 512);
                     }
                 };
                 read_low(0);
                 if constexpr (TM_ > 1) read_low(1);
+                v8bf up[TN_];
 #pragma unroll
-                for (int b = 0; b < TN_; ++b) up[b] = up_next[b];
+                for (int b = 0; b < TN_; ++b) up[b] = operand(up_next[b]);
                 if constexpr (AHEAD) {
-                    if (k0 + 32 < R) read_up(cur, k0 + 32 + 8 * q);
+                    if (k0 + 32 < R) read_up(cur, k0 + 32);
                 }
 #pragma unroll
                 for (int a = 0; a < TM_; ++a) {
@@ -779,7 +792,7 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
                 const u16* piece = up + k;
                 int most_n = past, step = R;
                 asm volatile("" : "+v"(piece), "+v"(most_n), "+s"(step));
-                const v4i hi = *(const v4i*)low_of(a, k), lo = *(const v4i*)(low_of(a, k) + pitch);
+                const v4i hi = *(const v4i*)low_of(a, k), lo = *(const v4i*)(low_of(a, k) + 512);
                 const v4f h0 = bf16x4(v2u32{(u32)hi.x, (u32)hi.y}) + bf16x4(v2u32{(u32)lo.x, (u32)lo.y});
                 const v4f h1 = bf16x4(v2u32{(u32)hi.z, (u32)hi.w}) + bf16x4(v2u32{(u32)lo.z, (u32)lo.w});
 #pragma unroll

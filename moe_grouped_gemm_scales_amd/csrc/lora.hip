@@ -17,6 +17,17 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kRows = 16;
 constexpr int kWaves = 16;
 
+// 16 rows of 64 bytes, lane 4 r + c with 16-byte piece c of row r, as an operand of the matrix instruction: piece c of
+// row r to lane 16 c + r.  Loaded that way round, four lanes side by side read one piece of 64 bytes; a lane a row apart
+// from its neighbour each, as the operand lies, is a request of its own for each lane, which was what bounded the
+// pass (32 rows of K = 2048 with 32 adapters of rank 16 6.1 us).
+__device__ __forceinline__ bf16x8 operand(u32x4 w, int from) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (u32)__builtin_amdgcn_ds_bpermute(from, (int)w[i]);
+    return __builtin_bit_cast(bf16x8, v);
+}
+
 struct DownArgs {
     const u16* A;
     const u16* down;
@@ -54,7 +65,10 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
     // where neighbouring steps of all rows (4 KB apart at K = 2048) would meet in a few
     const int steps = a.K / 64;
     const int k_begin = steps * wave / kWaves * 64, k_end = steps * (wave + 1) / kWaves * 64;
-    const u16* rows = a.A + (u64)(m < a.M ? m : a.M - 1) * (u64)a.K + 8 * q;
+    // loads: lane 4 r + c takes piece c of row r
+    const int lr = lane >> 2, lc = 8 * (lane & 3), from = 4 * (4 * l16 + q);
+    const int mr = (int)blockIdx.x * kRows + lr;
+    const u16* rows = a.A + (u64)(mr < a.M ? mr : a.M - 1) * (u64)a.K + lc;
     while (todo) {
         const int mine = __builtin_amdgcn_readlane(ad, __builtin_ctz(todo));
         todo &= ~((u32)__ballot(ad == mine) & 0xffffu);
@@ -62,25 +76,28 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) {
             // ranks past the last read the last one; their results are not kept
-            const int r = r0 + 16 * s + l16;
-            down[s] = a.down + ((u64)mine * (u64)a.rank + (u32)(r < a.rank ? r : a.rank - 1)) * (u64)a.K + 8 * q;
+            const int r = r0 + 16 * s + lr;
+            down[s] = a.down + ((u64)mine * (u64)a.rank + (u32)(r < a.rank ? r : a.rank - 1)) * (u64)a.K + lc;
         }
         f32x4 acc[SUBS];
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
         for (int k = k_begin; k < k_end; k += 64) {
-            bf16x8 x[2], d[SUBS][2];
+            u32x4 x[2], d[SUBS][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                x[h] = *(const bf16x8*)(rows + k + 32 * h);
+                x[h] = *(const u32x4*)(rows + k + 32 * h);
 #pragma unroll
-                for (int s = 0; s < SUBS; ++s) d[s][h] = *(const bf16x8*)(down[s] + k + 32 * h);
+                for (int s = 0; s < SUBS; ++s) d[s][h] = *(const u32x4*)(down[s] + k + 32 * h);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                const bf16x8 row = operand(x[h], from);
 #pragma unroll
-                for (int s = 0; s < SUBS; ++s) acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[s][h], x[h], acc[s], 0, 0, 0);
+                for (int s = 0; s < SUBS; ++s)
+                    acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand(d[s][h], from), row, acc[s], 0, 0, 0);
+            }
         }
         // (a select: another adapter's rows keep their own sums, whatever this one made of them)
         if (ad == mine) {
@@ -93,14 +110,21 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
 #pragma unroll
     for (int s = 0; s < SUBS; ++s) parts[wave][s][lane] = sum[s];
     __syncthreads();
-    // wave s adds piece s in wave order: lane (row l16, ranks 4 q ..); the last piece also clears the ranks up to the pitch
+    // wave s adds piece s in wave order: lane (row l16, ranks 4 q ..); one piece of 16 clears the 16 behind it
     if (wave >= SUBS || !done) return;
     f32x4 t = parts[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) t += parts[w][wave][lane];
     const int r = r0 + 16 * wave + 4 * q;
     const float scale = a.scale ? a.scale[ad] : 1.f;
-    u16* to = a.low + (u64)m * (u32)(2 * a.pitch);
+    // the layout of the other product's operand: of 16 rows and 32 ranks, 1 KB of the values and 1 KB of what BF16
+    // leaves of them, each with ranks 8 c .. 8 c + 7 of row r at piece 16 c + r
+    auto store = [&](int r, u64 hi, u64 lo) {
+        u16* to = a.low + ((u64)blockIdx.x * (u32)(a.pitch / 32) + (u32)(r / 32)) * 1024 +
+                  ((r % 32) / 8 * 16 + l16) * 8 + r % 8;
+        *(u64*)to = hi;
+        *(u64*)(to + 512) = lo;
+    };
     if (r < a.pitch) {
         u64 hi = 0, lo = 0;
 #pragma unroll
@@ -110,11 +134,10 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
             hi |= (u64)h << (16 * e);
             lo |= (u64)to_bf16(v - bf16_lo(h)) << (16 * e);
         }
-        *(u64*)(to + r) = hi;
-        *(u64*)(to + a.pitch + r) = lo;
+        store(r, hi, lo);
     }
     if constexpr (SUBS == 1) {
-        if (r + 16 < a.pitch) *(u64*)(to + r + 16) = *(u64*)(to + a.pitch + r + 16) = 0;
+        if (r + 16 < a.pitch) store(r + 16, 0, 0);
     }
 }
 
