@@ -390,6 +390,48 @@ std::vector<KernelConfig> choose_structure(const Problem& p, int num_cus, const 
     return out;
 }
 
+// Dense products of few rows with low-rank adapters: the epilogue waits for the adapters' factors, so more and
+// smaller tiles win, several to a CU.  The times are as above, start + K blocks, with a start of each structure's
+// own, fitted to 1150 launches of 50 shapes (1 to 256 rows, 1024 to 7168 columns, K 512 to 4096, 32 adapters of rank 16,
+// a different one each row); over these the choice takes 2.6 % longer than the fastest of twelve structures, kStructures'
+// 8.6 %.  us: 32 x 7168 x 2048 14.8 against 17.8, 96 x 2112 x 1536 13.0 against 14.7, 256 x 1024 x 1024 10.9 against
+// 12.7.  (From 256 rows on kStructures' tiles win: 517 x 2112 x 1536 20.4 as 128 x 64, 24.0 as 64 x 64.)
+constexpr int kLoraRows = 256;
+struct LoraStructure {
+    int bm, bn, wm, wn, stages, per_cu;
+    double start, us, us_full;
+};
+const LoraStructure kLoraStructures[] = {
+    {32, 32, 2, 2, 6, 3, 1.52, 0.074, 0.087},
+    {32, 64, 1, 4, 4, 3, 2.24, 0.186, 0.129},
+    {16, 32, 1, 2, 6, 4, 1.51, 0.045, 0.059},
+    {64, 64, 2, 2, 4, 2, 4.01, 0.195, 0.225},
+};
+std::vector<KernelConfig> choose_lora_structure(const Problem& p, int num_cus, const KernelConfig& base) {
+    const int kb = p.k / 128;
+    double best = 1e30;
+    std::vector<KernelConfig> out;
+    for (const LoraStructure& st : kLoraStructures) {
+        if (st.bm > std::max(16, 2 * p.rows)) continue;      // (not among the launches)
+        const int tiles = (p.rows + st.bm - 1) / st.bm * ((p.n + st.bn - 1) / st.bn);
+        for (int sk = 1; sk <= 4; sk *= 2) {
+            if (sk > 1 && (kb / sk < 4 || tiles * sk > 2 * num_cus)) continue;
+            const double each = std::ceil((double)tiles * sk / num_cus), batches = std::ceil(each / st.per_cu);
+            const double blocks = std::ceil((double)kb / sk);
+            double t = st.start * (1 + 1.5 * (batches - 1)) + blocks * std::max(batches * st.us, each * st.us_full);
+            if (sk > 1) t += 2.8e-6 * p.rows * p.n * sk;
+            KernelConfig c = base;
+            c.bm = st.bm; c.bn = st.bn; c.wm = st.wm; c.wn = st.wn;
+            c.stages = st.stages; c.variant = 0; c.splitk = sk; c.kstep = 1;
+            if (t < best && valid(c, p)) {
+                best = t;
+                out = {c};
+            }
+        }
+    }
+    return out;
+}
+
 // DG_FORCE_CONFIG="bm,bn,wm,wn,stages,splitk[,kstep[,variant[,nb,ne]]]", or
 // several such launches over column ranges [nb, ne) separated by ';'.
 std::vector<KernelConfig> parse_forced(const KernelConfig& base) {
@@ -466,6 +508,7 @@ std::vector<KernelConfig> select_plan(const Problem& p, int num_cus) {
     // (the contiguous entries are for any large row count; the structures weigh its rounds)
     if (!uses_structures(p) || p.kind == kDense || p.kind == kMasked) table = tuned(p, num_cus, base);
     if (p.direct) table.clear();
+    if (table.empty() && p.ep.lora && p.rows <= kLoraRows) table = choose_lora_structure(p, num_cus, base);
     if (table.empty() && uses_structures(p)) table = choose_structure(p, num_cus, base);
     table = with_b_streams(table, p);
     if (valid_plan(table, p)) {
