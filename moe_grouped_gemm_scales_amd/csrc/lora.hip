@@ -3,10 +3,13 @@
 // added in the shared product's epilogue (kernels/fp8_gemm.hip).  The operation
 // is specified in include/dg.h.
 //
-// One workgroup takes 16 rows of A and up to 64 ranks; its sixteen waves take a
-// sixteenth of K each, on the matrix cores straight from global memory (an operand's 16
-// rows are 128 bytes each a step), and their sums meet in LDS.  What it reads
-// bounds it: A once, and an adapter once for each 16 rows that use it.
+// One workgroup takes 16 rows of A and up to 64 ranks; its eight waves take an
+// eighth of K each, on the matrix cores straight from global memory (an operand's 16
+// rows are 128 bytes each a step), and their sums meet in LDS.  It reads A once, and from
+// L2 an adapter once for each 16 rows that use it; a few dependent round trips bound it.
+// us (sixteen waves in brackets): 32 x 2048, 32 adapters of rank 16 4.1 (4.1), of which a launch is 2; 4096 x 2048,
+// eight of rank 64 10.9 (13.2), one alone 7.7 (10.0), 8192 x 7168 rank 64 59 (85).  With 32 rows a workgroup, which
+// reads an adapter half as often, the last takes 55, but 4096 x 2048 17.6 and 16384 x 2048 25.8 against 23.6.
 #include "row_kernels.h"
 
 namespace dg {
@@ -15,7 +18,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRows = 16;
-constexpr int kWaves = 16;
+constexpr int kWaves = 8;
 
 // 16 rows of 64 bytes, lane 4 r + c with 16-byte piece c of row r, as an operand of the matrix instruction: piece c of
 // row r to lane 16 c + r.  Loaded that way round, four lanes side by side read one piece of 64 bytes; a lane a row apart
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
 #pragma unroll
     for (int s = 0; s < SUBS; ++s) sum[s] = f32x4{0.f, 0.f, 0.f, 0.f};
     bool done = false;                               // this lane's row
-    // a wave's share of K, in steps of 64: waves a sixteenth of a row apart read different memory channels,
+    // a wave's share of K, in steps of 64: waves an eighth of a row apart read different memory channels,
     // where neighbouring steps of all rows (4 KB apart at K = 2048) would meet in a few
     const int steps = a.K / 64;
     const int k_begin = steps * wave / kWaves * 64, k_end = steps * (wave + 1) / kWaves * 64;
