@@ -5,9 +5,9 @@
 //   score p = softmax(l) or 1 / (1 + e^-l),  choice value v = p + bias
 //   topk of v (among the best groups), w = scale p / (sum of the chosen p, or 1)
 //
-// One wave a token, expert e in lane e % 64: the logits are read once, coalesced,
-// and a choice is a few cross-lane steps.  A token's logits are at most 4 KB, so
-// the pass is bound by latency and by the wave's own instructions, not by HBM.
+// One wave a token: the logits are read once, coalesced, and a choice is a few
+// cross-lane steps.  A token's logits are at most 4 KB, so the pass is bound by
+// latency and by the wave's own instructions, not by HBM.
 #include <cmath>
 #include <type_traits>
 
@@ -24,7 +24,8 @@ struct RouteArgs {
     const float* bias;
     int* ids;
     float* weights;
-    int E, k, groups, group_size, kept, best, renormalise;
+    int T, E, k, groups, group_size, kept, best, renormalise;
+    int whole_lanes;                   // lanes a group, where groups are a power of two of whole lanes; 0: not so
     float scale;
 };
 
@@ -32,21 +33,39 @@ __device__ __forceinline__ float logit(const void* p, int wide, u64 at) {
     return wide ? static_cast<const float*>(p)[at] : bf16_lo(static_cast<const u16*>(p)[at]);
 }
 
-// Sums and maxima over the wave, the same in every lane.
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+// Sums and maxima over the wave, the same in every lane: rotations within 16 lanes, then the four 16s.
+// (By shuffles through LDS each of six steps waits for the one before: about 100 clocks a step.)
+template <int D>
+__device__ __forceinline__ double rotated(double v) {
+    const u64 b = __builtin_bit_cast(u64, v);
+    return __builtin_bit_cast(double, (u64)rotate16<D>((u32)(b >> 32)) << 32 | rotate16<D>((u32)b));
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+template <int D>
+__device__ __forceinline__ float rotated(float v) {
+    return __builtin_bit_cast(float, rotate16<D>(__builtin_bit_cast(u32, v)));
+}
+__device__ __forceinline__ double of_lane(double v, int lane) {
+    const u64 b = __builtin_bit_cast(u64, v);
+    return __builtin_bit_cast(double, (u64)(u32)__builtin_amdgcn_readlane((int)(b >> 32), lane) << 32 |
+                                          (u32)__builtin_amdgcn_readlane((int)b, lane));
+}
+__device__ __forceinline__ float of_lane(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+    v += rotated<8>(v);
+    v += rotated<4>(v);
+    v += rotated<2>(v);
+    v += rotated<1>(v);
+    return (of_lane(v, 0) + of_lane(v, 16)) + (of_lane(v, 32) + of_lane(v, 48));
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    v = fmaxf(v, rotated<8>(v));
+    v = fmaxf(v, rotated<4>(v));
+    v = fmaxf(v, rotated<2>(v));
+    v = fmaxf(v, rotated<1>(v));
+    return fmaxf(fmaxf(of_lane(v, 0), of_lane(v, 16)), fmaxf(of_lane(v, 32), of_lane(v, 48)));
 }
 __device__ __forceinline__ u32 wave_max(u32 v) {
     v = max16(v);
@@ -67,24 +86,122 @@ __device__ __forceinline__ double value_of(u64 r) {
     return __builtin_bit_cast(double, (r >> 63) ? r & ~(1ull << 63) : ~r);
 }
 
+// Whether lane's group g of L neighbouring lanes is among the a.kept best, from the two largest ranks of each lane's
+// part: the sum of its best one or two values, of equals the lower group first.
+__device__ __forceinline__ bool group_kept(const RouteArgs& a, u64 b1, u64 b2, int g, int L) {
+    for (int d = 1; d < L; d *= 2) {
+        const u64 o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+        const u64 lower = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
+        b1 = o1 > b1 ? o1 : b1;
+        b2 = lower > second ? lower : second;
+    }
+    double worth = -INFINITY;
+    if (b1) worth = value_of(b1) + (a.best > 1 && b2 ? value_of(b2) : 0.0);
+    int better = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const double o = of_lane(worth, h * L);
+        better += o > worth || (o == worth && h < g);
+    }
+    return better < a.kept;
+}
+
+// What a wave's lanes wrote to LDS is read by others of the same wave: in order, without a barrier.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// e^x for x <= 0 (a NaN stays one): x = n ln 2 + r, the Taylor series of e^r to r^13 (|r| <= 0.347: 4e-18 of it
+// left), times 2^n.  Step by step for all N, so that a coefficient is one scalar operand for them; the device library's
+// function, a branch round each, took 80 instructions a value with the quotient, this 30.
+template <int N>
+__device__ __forceinline__ void exp_of(double (&x)[N]) {
+    constexpr double kFactorial[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
+                                       1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800};
+    double n[N], y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = x[i] < -800.0 ? -800.0 : x[i];                 // (0 from -746 on)
+        n[i] = __builtin_rint(x[i] * 1.4426950408889634);
+        // ln 2 in two parts, the first with zeros behind, so that n times it is exact
+        x[i] = __builtin_fma(n[i], -0x1.62e42fefa38p-1, x[i]);
+        x[i] = __builtin_fma(n[i], -0x1.ef35793c7673p-45, x[i]);
+        y[i] = kFactorial[13];
+    }
+#pragma unroll
+    for (int c = 12; c >= 0; --c)
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = __builtin_fma(y[i], x[i], kFactorial[c]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_ldexp(y[i], (int)n[i]);
+}
+// 1 / x for x from 1 to 2^10 (or NaN): the hardware's estimate (2^-22 or better) and two Newton steps
+__device__ __forceinline__ double reciprocal(double x) {
+    double r = __builtin_amdgcn_rcp(x);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+}
+
+// The lane's PER logits from expert e on; -inf past the last expert.
+template <int PER, bool WIDE>
+__device__ __forceinline__ void read_logits(const void* logits, u64 row, int e, int E, float (&l)[PER]) {
+    const int at = e < E ? e : E - 1;
+    if (E % PER == 0) {                           // whole pieces, of whatever alignment; lanes past the end read the last
+        const u64 from = row + (u32)(e < E ? e : E - PER);
+        if constexpr (WIDE) {
+            __builtin_memcpy(l, static_cast<const float*>(logits) + from, 4 * PER);
+        } else {
+            u16 w[PER];
+            __builtin_memcpy(w, static_cast<const u16*>(logits) + from, 2 * PER);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) l[i] = bf16_lo(w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) l[i] = logit(logits, WIDE, row + (u32)(at + i < E ? at + i : E - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (e + i >= E) l[i] = -INFINITY;
+}
+
+// Tokens (waves) of a workgroup: the dispatch of 8192 workgroups of one wave takes 4 us by itself; the tokens of few
+// are spread over the CUs.  (Past 256 experts four tokens' values do not fit beside other workgroups' in LDS.)
+constexpr int waves_of(int per) { return per <= 4 ? 4 : 1; }
+constexpr int kSpread = 1024;
+
+// Lane i has experts i PER to i PER + PER - 1, so that the lowest lane among equals has the lowest expert.
 // Choice values are 64-bit numbers: 256 scores of 8192 tokens hold pairs that FP32 scores
 // tell apart wrongly, and a choice is not rounded but made.
 template <int PER, bool WIDE, bool SIGMOID>
-__global__ void __launch_bounds__(64) dg_moe_route_kernel(const RouteArgs a) {
-    const int lane = threadIdx.x;
-    const u64 t = blockIdx.x;
-    const int E = a.E;
-    __shared__ double score[PER * 64];
-    __shared__ u64 shared_rank[PER * 64];
-    float l[PER];
+__global__ void __launch_bounds__(64 * waves_of(PER)) dg_moe_route_kernel(const RouteArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const u32 t = blockIdx.x * (blockDim.x >> 6) + (u32)wave;
+    if (t >= (u32)a.T) return;
+    const int E = a.E, e0 = lane * PER;
+    __shared__ double scores[waves_of(PER)][PER * 64];
+    __shared__ u64 ranks[waves_of(PER)][PER * 64];
+    double* const score = scores[wave];
+    float l[PER], bias[PER];
     double p[PER];
     u64 rank[PER];
+    read_logits<PER, WIDE>(a.logits, (u64)t * (u32)E, e0, E, l);
+    if (a.bias) {
+        read_logits<PER, true>(a.bias, 0, e0, E, bias);
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        l[i] = lane + 64 * i < E ? logit(a.logits, WIDE, t * (u64)E + (lane + 64 * i)) : -INFINITY;
+        for (int i = 0; i < PER; ++i) bias[i] = 0.f;
+    }
     if constexpr (SIGMOID) {
+        // 1 / (1 + e^-|l|), times e^-|l| below zero
 #pragma unroll
-        for (int i = 0; i < PER; ++i) p[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+        for (int i = 0; i < PER; ++i) p[i] = -(double)__builtin_fabsf(l[i]);
+        exp_of(p);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const double r = reciprocal(1.0 + p[i]);
+            p[i] = l[i] < 0.f ? p[i] * r : r;
+        }
     } else {
         float top = -INFINITY;
 #pragma unroll
@@ -92,26 +209,29 @@ __global__ void __launch_bounds__(64) dg_moe_route_kernel(const RouteArgs a) {
         top = wave_max(top);
         double sum = 0.0;
 #pragma unroll
+        for (int i = 0; i < PER; ++i) p[i] = (double)l[i] - (double)top;
+        exp_of(p);
+#pragma unroll
         for (int i = 0; i < PER; ++i) {
-            p[i] = l[i] == -INFINITY ? 0.0 : exp((double)l[i] - (double)top);
+            if (l[i] == -INFINITY) p[i] = 0.0;
             sum += p[i];
         }
-        sum = 1.0 / wave_sum(sum);
+        sum = reciprocal(wave_sum(sum));
 #pragma unroll
         for (int i = 0; i < PER; ++i) p[i] *= sum;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        const double v = a.bias && e < E ? p[i] + (double)a.bias[e] : p[i];
-        rank[i] = e >= E || l[i] == -INFINITY || v == -INFINITY ? 0ull : rank_of(v);
-        score[e] = p[i];
+        const double v = p[i] + (double)bias[i];
+        rank[i] = l[i] == -INFINITY || v == -INFINITY ? 0ull : rank_of(v);
+        score[e0 + i] = p[i];
     }
-    if (a.groups > 1) {
-        // L lanes a group: the sum of its best one or two values, then the group's place among all
+    if (a.groups > 1 && !a.whole_lanes) {
+        // groups that do not end with a lane: L lanes a group, through LDS
+        u64* const shared_rank = ranks[wave];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) shared_rank[lane + 64 * i] = rank[i];
-        __syncthreads();
+        for (int i = 0; i < PER; ++i) shared_rank[e0 + i] = rank[i];
+        wave_fence();
         int L = 64;
         while (L * a.groups > 64) L /= 2;
         const int g = lane / L, sub = lane % L;
@@ -122,37 +242,62 @@ __global__ void __launch_bounds__(64) dg_moe_route_kernel(const RouteArgs a) {
                 b2 = r > b1 ? b1 : r > b2 ? r : b2;
                 b1 = r > b1 ? r : b1;
             }
-        for (int d = 1; d < L; d *= 2) {
-            const u64 o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
-            const u64 lower = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
-            b1 = o1 > b1 ? o1 : b1;
-            b2 = lower > second ? lower : second;
-        }
-        double worth = -INFINITY;
-        if (b1) worth = value_of(b1) + (a.best > 1 && b2 ? value_of(b2) : 0.0);
-        int better = 0;
-        for (int h = 0; h < a.groups; ++h) {
-            const double o = __shfl(worth, h * L);
-            better += o > worth || (o == worth && h < g);
-        }
-        if (better >= a.kept && g < a.groups)
+        if (!group_kept(a, b1, b2, g, L) && g < a.groups)
             for (int j = sub; j < a.group_size; j += L) shared_rank[g * a.group_size + j] = 0ull;
-        __syncthreads();
+        wave_fence();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) rank[i] = shared_rank[lane + 64 * i];
-    } else {
-        __syncthreads();
+        for (int i = 0; i < PER; ++i) rank[i] = shared_rank[e0 + i];
     }
+    // a lane's values largest first (of equals the lower expert), so that each turn below looks at the first alone; of
+    // many values the sort costs more than looking at all
+    constexpr bool SORTED = PER <= 4;
+    int expert[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) expert[i] = e0 + i;
+    if constexpr (SORTED) {
+#pragma unroll
+        for (int n = PER - 1; n > 0; --n)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool swap = rank[i + 1] > rank[i];
+                const u64 r = swap ? rank[i] : rank[i + 1];
+                const int e = swap ? expert[i] : expert[i + 1];
+                rank[i] = swap ? rank[i + 1] : rank[i];
+                expert[i] = swap ? expert[i + 1] : expert[i];
+                rank[i + 1] = r;
+                expert[i + 1] = e;
+            }
+    }
+    if (a.whole_lanes) {
+        // a.whole_lanes lanes a group, whose two best are already the first of each lane's
+        u64 b1 = rank[0], b2 = 0;
+        if constexpr (SORTED && PER > 1) {
+            b2 = rank[1];
+        } else {
+#pragma unroll
+            for (int i = 1; i < PER; ++i) {
+                b2 = rank[i] > b1 ? b1 : rank[i] > b2 ? rank[i] : b2;
+                b1 = rank[i] > b1 ? rank[i] : b1;
+            }
+        }
+        if (!group_kept(a, b1, b2, lane / a.whole_lanes, a.whole_lanes)) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) rank[i] = 0ull;
+        }
+    }
+    wave_fence();                                 // (the scores)
     // the best of the wave, k times: the largest upper word, then among its lanes the largest
-    // lower word, then the lowest expert; the first step mostly leaves one lane
+    // lower word, then the lowest lane; the first step mostly leaves one lane
     int id = -1;                                  // of choice `lane`
     for (int j = 0; j < a.k; ++j) {
         u64 best = rank[0];
-        int at = lane;
+        int at = expert[0];
+        if constexpr (!SORTED) {
 #pragma unroll
-        for (int i = 1; i < PER; ++i) {
-            at = rank[i] > best ? lane + 64 * i : at;
-            best = rank[i] > best ? rank[i] : best;
+            for (int i = 1; i < PER; ++i) {
+                at = rank[i] > best ? expert[i] : at;
+                best = rank[i] > best ? rank[i] : best;
+            }
         }
         const u32 hi = wave_max((u32)(best >> 32));
         if (hi == 0u) break;                      // none is available
@@ -160,18 +305,23 @@ __global__ void __launch_bounds__(64) dg_moe_route_kernel(const RouteArgs a) {
         u64 with = __ballot(mine);
         if (with & (with - 1)) {
             const u32 lo = wave_max(mine ? (u32)best : 0u);
-            mine = mine && (u32)best == lo;
-            with = __ballot(mine);
-            if (with & (with - 1)) {
-                const u32 first = kMaxExperts - wave_max(mine ? (u32)(kMaxExperts - at) : 0u);
-                with = __ballot(mine && (u32)at == first);
-            }
+            with = __ballot(mine && (u32)best == lo);
         }
-        const int chosen = __builtin_amdgcn_readlane(at, __builtin_ctzll(with));
+        const int winner = __builtin_ctzll(with);
+        const int chosen = __builtin_amdgcn_readlane(at, winner);
         if (lane == j) id = chosen;
+        if constexpr (SORTED) {
+            const bool won = lane == winner;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 64 * i == chosen) rank[i] = 0ull;
+            for (int i = 0; i < PER; ++i) {
+                rank[i] = won ? (i + 1 < PER ? rank[i + 1 < PER ? i + 1 : i] : 0ull) : rank[i];
+                if (i + 1 < PER) expert[i] = won ? expert[i + 1] : expert[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (expert[i] == chosen) rank[i] = 0ull;
+        }
     }
     double w = id >= 0 ? score[id] : 0.0;
     if (a.renormalise) {
@@ -179,8 +329,8 @@ __global__ void __launch_bounds__(64) dg_moe_route_kernel(const RouteArgs a) {
         w = sum == 0.0 ? 0.0 : w / sum;
     }
     if (lane < a.k) {
-        a.ids[t * (u64)a.k + lane] = id;
-        a.weights[t * (u64)a.k + lane] = (float)((double)a.scale * w);
+        a.ids[(u64)t * (u32)a.k + lane] = id;
+        a.weights[(u64)t * (u32)a.k + lane] = (float)((double)a.scale * w);
     }
 }
 
@@ -194,18 +344,22 @@ struct RouteBackwardArgs {
     const int* ids;
     const float* d_weights;
     void* d_logits;
-    int E, k;
+    int T, E, k;
     float scale;
 };
 template <int PER, bool WIDE, bool SIGMOID, bool RENORM>
-__global__ void __launch_bounds__(64) dg_moe_route_backward_kernel(const RouteBackwardArgs a) {
-    const int lane = threadIdx.x;
-    const u64 t = blockIdx.x;
+__global__ void __launch_bounds__(256) dg_moe_route_backward_kernel(const RouteBackwardArgs a) {
+    const int lane = threadIdx.x & 63;
+    const u32 t = blockIdx.x * (blockDim.x >> 6) + (u32)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= (u32)a.T) return;
     const int E = a.E;
-    const u64 row = t * (u64)E;
-    int id = lane < a.k ? a.ids[t * (u64)a.k + lane] : -1;
-    if ((u32)id >= (u32)E) id = -1;
-    const float dw = id >= 0 ? a.scale * a.d_weights[t * (u64)a.k + lane] : 0.f;
+    const u64 row = (u64)t * (u32)E;
+    // (lanes past the last choice read it, so that the loads are issued together)
+    const u64 mine = (u64)t * (u32)a.k + (u32)(lane < a.k ? lane : a.k - 1);
+    int id = a.ids[mine];
+    const float given = a.d_weights[mine];
+    if (lane >= a.k || (u32)id >= (u32)E) id = -1;
+    const float dw = id >= 0 ? a.scale * given : 0.f;
     const float lj = id >= 0 ? logit(a.logits, WIDE, row + (u32)id) : -INFINITY;
     float p[PER];                              // softmax without renormalising: of every expert
     float c;                                   // choice `lane`'s term
@@ -232,8 +386,10 @@ __global__ void __launch_bounds__(64) dg_moe_route_backward_kernel(const RouteBa
     } else {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
+        for (int i = 0; i < PER; ++i) p[i] = logit(a.logits, WIDE, row + (u32)(lane + 64 * i < E ? lane + 64 * i : E - 1));
+#pragma unroll
         for (int i = 0; i < PER; ++i) {
-            p[i] = lane + 64 * i < E ? logit(a.logits, WIDE, row + (lane + 64 * i)) : -INFINITY;
+            if (lane + 64 * i >= E) p[i] = -INFINITY;
             top = fmaxf(top, p[i]);
         }
         top = wave_max(top);
@@ -273,7 +429,8 @@ template <int PER>
 dg_status launch_route(bool wide, bool sigmoid, unsigned T, void* stream, const RouteArgs& a) {
     auto* kernel = wide ? (sigmoid ? dg_moe_route_kernel<PER, true, true> : dg_moe_route_kernel<PER, true, false>)
                         : (sigmoid ? dg_moe_route_kernel<PER, false, true> : dg_moe_route_kernel<PER, false, false>);
-    return launch_rows("moe_route", kernel, dim3(T), 64, stream, a);
+    const unsigned waves = T >= kSpread ? waves_of(PER) : 1;
+    return launch_rows("moe_route", kernel, dim3((T + waves - 1) / waves), 64 * waves, stream, a);
 }
 template <int PER, bool WIDE>
 dg_status launch_route_backward(bool sigmoid, bool renorm, unsigned T, void* stream, const RouteBackwardArgs& a) {
@@ -281,7 +438,8 @@ dg_status launch_route_backward(bool sigmoid, bool renorm, unsigned T, void* str
                                      : dg_moe_route_backward_kernel<PER, WIDE, true, false>)
                            : (renorm ? dg_moe_route_backward_kernel<PER, WIDE, false, true>
                                      : dg_moe_route_backward_kernel<PER, WIDE, false, false>);
-    return launch_rows("moe_route_backward", kernel, dim3(T), 64, stream, a);
+    const unsigned waves = T >= kSpread ? 4 : 1;
+    return launch_rows("moe_route_backward", kernel, dim3((T + waves - 1) / waves), 64 * waves, stream, a);
 }
 
 dg_status check_route(const char* what, bool null, const dg_routing* r, int logits_type, int T, int E, int k) {
@@ -333,10 +491,12 @@ dg_status dg_moe_route(const void* logits, int logits_type, const float* bias, c
         if (!aligned(logits, wide ? 4 : 2) || !aligned(bias, 4) || !aligned(expert_ids, 4) || !aligned(weights, 4))
             return set_error(DG_ERR_ALIGNMENT, "moe_route: arrays must be aligned to their elements");
         if (T == 0) return DG_OK;
-        const RouteArgs a{logits, bias, expert_ids, weights, num_experts, topk,
-                          r.topk_groups < r.groups ? r.groups : 1, size, r.topk_groups, r.group_best, r.renormalise != 0, r.scale};
+        const int groups = r.topk_groups < r.groups ? r.groups : 1, per = per_lane(num_experts), lanes = size / per;
+        const bool whole = groups > 1 && size % per == 0 && (lanes & (lanes - 1)) == 0;
+        const RouteArgs a{logits, bias, expert_ids, weights, T, num_experts, topk, groups, size, r.topk_groups,
+                          r.group_best, r.renormalise != 0, whole ? lanes : 0, r.scale};
         const bool sigmoid = r.score == DG_SCORE_SIGMOID;
-        switch (per_lane(num_experts)) {
+        switch (per) {
             case 1: return launch_route<1>(wide, sigmoid, (unsigned)T, stream, a);
             case 2: return launch_route<2>(wide, sigmoid, (unsigned)T, stream, a);
             case 4: return launch_route<4>(wide, sigmoid, (unsigned)T, stream, a);
@@ -358,7 +518,7 @@ dg_status dg_moe_route_backward(const void* logits, int logits_type, const int32
             !aligned(d_weights, 4))
             return set_error(DG_ERR_ALIGNMENT, "moe_route_backward: arrays must be aligned to their elements");
         if (T == 0) return DG_OK;
-        const RouteBackwardArgs a{logits, expert_ids, d_weights, d_logits, num_experts, topk, routing->scale};
+        const RouteBackwardArgs a{logits, expert_ids, d_weights, d_logits, T, num_experts, topk, routing->scale};
         const bool sigmoid = routing->score == DG_SCORE_SIGMOID, renorm = routing->renormalise != 0;
         auto launch = [&](auto per) {
             constexpr int PER = decltype(per)::value;
