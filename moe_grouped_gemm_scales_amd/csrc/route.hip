@@ -78,29 +78,43 @@ __device__ __forceinline__ u32 wave_max(u32 v) {
 // A choice value as an integer of the same order; 0: the expert is not available.  A NaN (of
 // its logit, or of a softmax whose row holds one) ranks below every number.
 __device__ __forceinline__ u64 rank_of(double v) {
-    if (v != v) v = -1e300;
+    v = v == v ? v : -1e300;
     const u64 b = __builtin_bit_cast(u64, v);
-    return (b >> 63) ? ~b : b | (1ull << 63);
+    const u32 hi = (u32)(b >> 32), flip = (u32)((int)hi >> 31);         // negative: all bits, else the sign alone
+    return (u64)(hi ^ (flip | 0x80000000u)) << 32 | ((u32)b ^ flip);
 }
 __device__ __forceinline__ double value_of(u64 r) {
     return __builtin_bit_cast(double, (r >> 63) ? r & ~(1ull << 63) : ~r);
 }
 
+template <int CTRL>
+__device__ __forceinline__ u64 moved(u64 v) {
+    const u32 hi = (u32)__builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, 0xf, 0xf, true);
+    return (u64)hi << 32 | (u32)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
 // Whether lane's group g of L neighbouring lanes is among the a.kept best, from the two largest ranks of each lane's
 // part: the sum of its best one or two values, of equals the lower group first.
 __device__ __forceinline__ bool group_kept(const RouteArgs& a, u64 b1, u64 b2, int g, int L) {
-    for (int d = 1; d < L; d *= 2) {
-        const u64 o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+    auto merge = [&](u64 o1, u64 o2) {
         const u64 lower = o1 < b1 ? o1 : b1, second = o2 > b2 ? o2 : b2;
         b1 = o1 > b1 ? o1 : b1;
         b2 = lower > second ? lower : second;
-    }
+    };
+    // neighbours, pairs, quads and eights: the other half's lanes all hold its two, so a mirror image will do
+    if (L > 1) merge(moved<0xB1>(b1), moved<0xB1>(b2));
+    if (L > 2) merge(moved<0x4E>(b1), moved<0x4E>(b2));
+    if (L > 4) merge(moved<0x141>(b1), moved<0x141>(b2));
+    if (L > 8) merge(moved<0x140>(b1), moved<0x140>(b2));
+    for (int d = 16; d < L; d *= 2) merge(__shfl_xor(b1, d), __shfl_xor(b2, d));
     double worth = -INFINITY;
     if (b1) worth = value_of(b1) + (a.best > 1 && b2 ? value_of(b2) : 0.0);
+    // lane s of a group compares with the groups s, s + L, ...
     int better = 0;
-    for (int h = 0; h < a.groups; ++h) {
-        const double o = of_lane(worth, h * L);
-        better += o > worth || (o == worth && h < g);
+    const int sub = (int)(threadIdx.x & 63) % L;
+    for (int h = sub; h < a.groups + sub; h += L) {            // (as many turns in every lane)
+        const double o = __shfl(worth, h < a.groups ? h * L : 0);
+        const u64 ahead = __ballot(h < a.groups && (o > worth || (o == worth && h < g)));
+        better += __popcll(ahead >> (g * L) & ((1ull << L) - 1));
     }
     return better < a.kept;
 }
@@ -129,9 +143,12 @@ __device__ __forceinline__ void exp_of(double (&x)[N]) {
         y[i] = kFactorial[13];
     }
 #pragma unroll
-    for (int c = 12; c >= 0; --c)
+    for (int c = 12; c >= 0; --c) {
+        double k = kFactorial[c];
+        asm("" : "+s"(k));                                    // (a scalar pair, not moved to vector registers)
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = __builtin_fma(y[i], x[i], kFactorial[c]);
+        for (int i = 0; i < N; ++i) y[i] = __builtin_fma(y[i], x[i], k);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_ldexp(y[i], (int)n[i]);
 }
