@@ -64,7 +64,7 @@ def _near(got, want, tol):
 
 
 SHAPES = [(1, 1), (3, 7), (1, 8), (9, 127), (8, 128), (17, 500), (300, 511), (5, 512), (33, 520), (2, 1000), (7, 2048),
-          (4, 2056), (130, 2303), (32, 7168), (3, 8192), (2, 8200), (2, 20001), (1, 32768), (2, 32776), (2, 65536)]
+          (4, 2056), (130, 2303), (32, 7168), (3, 8192), (2, 8200), (2, 16384), (2, 20001), (1, 32765), (2, 32768)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
@@ -79,7 +79,7 @@ def test_norm_bf16(T, H, weight, residual):
 
 
 @pytest.mark.parametrize("T,H", [(1, 128), (9, 384), (33, 512), (64, 640), (7, 1664), (32, 7168), (1021, 1024), (3, 8320),
-                                 (2, 65536)])
+                                 (2, 32768)])
 @pytest.mark.parametrize("ue8m0", [False, True])
 @pytest.mark.parametrize("both", [False, True])
 def test_norm_e4m3(T, H, ue8m0, both):
