@@ -23,53 +23,46 @@ __device__ __forceinline__ float cut(float z, float far) { return z > far ? far 
 __device__ __forceinline__ float logistic2(float x) {      // 1 / (1 + 2^-x)
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x));
 }
-__device__ __forceinline__ float normal_tail(float z) {    // Phi(-|z|)
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.30405593f, __builtin_fabsf(z), 1.f));
-    const float e = __builtin_amdgcn_exp2f(-0.72134752f * z * z);
-    float y = __builtin_fmaf(t, 0.036534112f, -0.15392894f);
-    y = __builtin_fmaf(t, y, 0.18981865f);
-    y = __builtin_fmaf(t, y, -0.041117497f);
-    y = __builtin_fmaf(t, y, 0.12256832f);
-    y = __builtin_fmaf(t, y, 0.10271288f);
-    y = __builtin_fmaf(t, y, 0.12215308f);
-    return __builtin_fmaf(t, y, 0.12125936f) * t * e;
-}
 template <int ACT>
-__device__ __forceinline__ float slope(float z) {
-    if constexpr (ACT == DG_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
+__device__ __forceinline__ float slope(float z, float& value) {       // and the activation, with the same functions
+    if constexpr (ACT == DG_ACT_RELU) {
+        value = z > 0.f ? z : z <= 0.f ? 0.f : z;
+        return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
+    }
     if constexpr (ACT == DG_ACT_SILU) {
-        z = cut(z, 200.f);
-        const float s = logistic2(1.44269504f * z);
-        return s * __builtin_fmaf(z, 1.f - s, 1.f);
+        const float c = cut(z, 200.f);
+        const float s = logistic2(1.44269504f * c);
+        value = z * s;
+        return s * __builtin_fmaf(c, 1.f - s, 1.f);
     }
     if constexpr (ACT == DG_ACT_GELU) {
-        z = cut(z, 16.f);
-        const float tail = normal_tail(z);
-        const float e = __builtin_amdgcn_exp2f(-0.72134752f * z * z);       // (the tail's own)
-        return __builtin_fmaf(0.39894228f * z, e, z < 0.f ? tail : 1.f - tail);
-    }
-    if constexpr (ACT == DG_ACT_GELU_TANH) {
-        z = cut(z, 16.f);
-        const float s = logistic2(2.30220820f * z * __builtin_fmaf(0.044715f * z, z, 1.f));
-        return __builtin_fmaf(z * s * (1.f - s), __builtin_fmaf(0.21406445f * z, z, 1.59576912f), s);
-    }
-    return 1.f;
-}
-
-// The activation itself, with the functions of its slope.
-template <int ACT>
-__device__ __forceinline__ float activated(float z) {
-    if constexpr (ACT == DG_ACT_RELU) return z > 0.f ? z : z <= 0.f ? 0.f : z;
-    if constexpr (ACT == DG_ACT_SILU) return z * logistic2(1.44269504f * cut(z, 200.f));
-    if constexpr (ACT == DG_ACT_GELU) {
-        const float tail = normal_tail(cut(z, 16.f));
-        return z < 0.f ? z * tail : __builtin_fmaf(-z, tail, z);
+        const float c = cut(z, 16.f);
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.30405593f, __builtin_fabsf(c), 1.f));
+        const float e = __builtin_amdgcn_exp2f(-0.72134752f * c * c);
+        float y = __builtin_fmaf(t, 0.036534112f, -0.15392894f);
+        y = __builtin_fmaf(t, y, 0.18981865f);
+        y = __builtin_fmaf(t, y, -0.041117497f);
+        y = __builtin_fmaf(t, y, 0.12256832f);
+        y = __builtin_fmaf(t, y, 0.10271288f);
+        y = __builtin_fmaf(t, y, 0.12215308f);
+        const float tail = __builtin_fmaf(t, y, 0.12125936f) * t * e;       // Phi(-|z|)
+        const float phi = c < 0.f ? tail : 1.f - tail;
+        value = z * phi;
+        return __builtin_fmaf(0.39894228f * c, e, phi);
     }
     if constexpr (ACT == DG_ACT_GELU_TANH) {
         const float c = cut(z, 16.f);
-        return z * logistic2(2.30220820f * c * __builtin_fmaf(0.044715f * c, c, 1.f));
+        const float s = logistic2(2.30220820f * c * __builtin_fmaf(0.044715f * c, c, 1.f));
+        value = z * s;
+        return __builtin_fmaf(c * s * (1.f - s), __builtin_fmaf(0.21406445f * c, c, 1.59576912f), s);
     }
-    return z;
+    value = z;
+    return 1.f;
+}
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+    float value;
+    return slope<ACT>(z, value);
 }
 
 }  // namespace

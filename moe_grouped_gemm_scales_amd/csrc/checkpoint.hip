@@ -161,8 +161,12 @@ __global__ void __launch_bounds__(256) dg_checkpoint_restore_kernel(const Restor
 // ---------------------------------------------------------------- epilogue backward
 // dZ = dD slope(z) and H = activation(z) with z the kept value, and the column sums of dZ (FP32, before its
 // rounding) of the workgroup's rows: the split of dg_epilogue_backward, 512 columns of `chunk` rows a
-// workgroup, 8 columns a lane, each wave every fourth row, four rows in flight.
-constexpr int kWaveRows = 4;
+// workgroup, 8 columns a lane, each wave every fourth row; two rows in flight (four: 61.0 us against 55.4 for 8192 x
+// 4096, GELU, for want of registers; one 54.4 there, but 8192 x 1024 47 against 43 at 128 rows a workgroup).
+// Rows a workgroup: as many as still give 1024 workgroups.  us with 16, 32 and 64: 2048 x 4096 18.2, 19.7, 26.6;
+// 8192 x 4096 56.9, 55.4, 55.0, and in four experts, whose partial sums are read four times, 68.2, 63.3, 58.2.
+constexpr int kWorkgroups = 1024;
+constexpr int kWaveRows = 2;
 constexpr int kStep = 4 * kWaveRows;
 struct KeptBackwardArgs {
     const u16* dD;
@@ -183,17 +187,28 @@ __global__ void __launch_bounds__(256) dg_epilogue_backward_fp8_kernel(const Kep
     const int c0 = (int)blockIdx.y * 512, c = c0 + lane * 8;
     const int first = (int)blockIdx.x * a.chunk;
     const int last = rows - first < a.chunk ? rows : first + a.chunk;
-    const int owner = a.m_indices ? a.m_indices[first] : 0;
     const u32 block = c < N ? (u32)c / kBlock : 0u;
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    // the experts of the chunk's (at most 128) rows, two a lane: read row by row, their loads are waited for in front of
+    // each turn's
+    int index[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = first + lane + 64 * h;
+        index[h] = a.m_indices && r < last ? a.m_indices[r] : 0;
+    }
+    const int owner = __builtin_amdgcn_readlane(index[0], 0);
     for (int r0 = first + wave; r0 < last; r0 += kStep) {
         // the expert of each of this wave's four rows (below 0: padding, or no row)
         int expert[kWaveRows];
 #pragma unroll
-        for (int i = 0; i < kWaveRows; ++i)
-            expert[i] = r0 + 4 * i >= last ? kPadding - 1 : a.m_indices ? a.m_indices[r0 + 4 * i] : 0;
+        for (int i = 0; i < kWaveRows; ++i) {
+            const int in = r0 - first + 4 * i;
+            const int of = __builtin_amdgcn_readlane(in < 64 ? index[0] : index[1], in & 63);
+            expert[i] = r0 + 4 * i >= last ? kPadding - 1 : of;
+        }
         u32x4 d[kWaveRows];
         u64 z[kWaveRows];
         u32 scale[kWaveRows];
@@ -218,15 +233,13 @@ __global__ void __launch_bounds__(256) dg_epilogue_backward_fp8_kernel(const Kep
             kept_values(z[i], scale_of(scale[i]), h);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (real) v[e] *= slope<ACT>(h[e]);
+                const float s = slope<ACT>(h[e], h[e]);         // (0 of 0, so a padding row's H is cleared too)
+                if (real) v[e] *= s;
                 if (real && expert[i] == owner) acc[e] += v[e];
             }
             const u64 at = (u64)(r0 + 4 * i) * (u64)N;
             if (a.dZ) store8(a.dZ + at, c, N, pack8(v));
-            if (!a.H) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = activated<ACT>(h[e]);          // (0 at 0)
-            store8(a.H + at, c, N, pack8(h));
+            if (a.H) store8(a.H + at, c, N, pack8(h));
         }
     }
     if (!a.partial) return;
@@ -269,7 +282,7 @@ dg_status backward(const void* dD, const void* codes, const void* scales, int ac
         return set_error(DG_ERR_INVALID_ARG, "epilogue_backward_fp8: H must be an array of its own");
     if (!aligned(dZ, 16) || !aligned(H, 16) || !aligned(dbias, 4))
         return set_error(DG_ERR_ALIGNMENT, "epilogue_backward_fp8: dZ and H must be 16-byte, dbias 4-byte aligned");
-    const int chunk = backward_chunk(rows, N);
+    const int chunk = backward_chunk(rows, N, kWorkgroups);
     const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
     if (N > 65535 * 512 || !fits_launch(chunks) || !column_sums_fit(N, G))
         return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward_fp8: too many rows, groups or columns for one launch");

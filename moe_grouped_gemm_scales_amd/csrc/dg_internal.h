@@ -171,8 +171,8 @@ dg_status pad_rows_bf16(const void* x, void* xp, int rows, int cols, int pitch, 
 dg_status column_sums(const char* what, const float* partial, const int32_t* m_indices, int chunks, int chunk, int N,
                       int G, float* out, void* stream);
 bool column_sums_fit(int N, int G);
-// rows a workgroup of an epilogue's backward pass takes
-int backward_chunk(int rows, int N);
+// rows a workgroup of an epilogue's backward pass takes: 128, halved to 16 while that leaves fewer workgroups than these
+int backward_chunk(int rows, int N, int workgroups);
 std::string cache_dir();
 
 // Device address of the library's status words on the current device

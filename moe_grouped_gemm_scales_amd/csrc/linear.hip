@@ -269,7 +269,7 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
         return set_error(DG_ERR_INVALID_ARG, "epilogue_backward: sizes must be positive (M may be 0)");
     if (!aligned(dD, 16) || !aligned(Z, 16) || !aligned(dZ, 16) || !aligned(dbias, 4) || !aligned(m_indices, 4))
         return set_error(DG_ERR_ALIGNMENT, "epilogue_backward: dD, Z and dZ must be 16-byte, the rest 4-byte aligned");
-    const int chunk = backward_chunk(rows, N);
+    const int chunk = backward_chunk(rows, N, kBackwardGroups);
     const int chunks = (int)(((int64_t)rows + chunk - 1) / chunk);
     if (N > 65535 * 512 || !fits_launch(chunks) || !column_sums_fit(N, G))
         return set_error(DG_ERR_UNSUPPORTED, "epilogue_backward: too many rows, groups or columns for one launch");
@@ -295,9 +295,9 @@ dg_status epilogue_backward(const void* dD, const void* Z, int act, const int32_
 
 }  // namespace
 
-int backward_chunk(int rows, int N) {
+int backward_chunk(int rows, int N, int workgroups) {
     int chunk = 128;
-    while (chunk > kStep && ((int64_t)rows + chunk - 1) / chunk * ((N + 511) / 512) < kBackwardGroups) chunk /= 2;
+    while (chunk > kStep && ((int64_t)rows + chunk - 1) / chunk * ((N + 511) / 512) < workgroups) chunk /= 2;
     return chunk;
 }
 

@@ -23,7 +23,11 @@ constexpr int kPadding = -1;           // m_indices of a padding row inside a se
 __device__ __forceinline__ float bf16_lo(u32 w) { return __builtin_bit_cast(float, w << 16); }
 __device__ __forceinline__ float bf16_hi(u32 w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
 __device__ __forceinline__ u16 to_bf16(float f) { return __builtin_bit_cast(u16, (__bf16)f); }   // nearest-even
-__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) { return (u32)to_bf16(lo) | ((u32)to_bf16(hi) << 16); }
+__device__ __forceinline__ u32 to_bf16x2(float lo, float hi) {      // one instruction
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(u32, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
 
 // Eight BF16 of a row whose width N is no multiple of 8, 64 apart from column c, two a word;
 // zeros past N.  Past the end the last element is read instead and dropped, so that the
