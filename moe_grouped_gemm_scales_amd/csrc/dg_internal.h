@@ -95,10 +95,10 @@ struct KernelConfig {
         if (kind == kKGrouped) return (bm + bn) * 128 + (bm + 63) / 64 * 256 + (bn + 63) / 64 * 256;
         return (bm + bn) * 128 * kstep + kstep * ((bm + 63) / 64) * 256 + kstep * 256;
     }
-    // variants 0, 4 and 6 of the contiguous form: 256 bytes per wave for the experts of its rows
+    // variants 0, 4 and 6 of the contiguous form, and with adapters: 256 bytes per wave for the experts of its rows
     int row_group_bytes() const {
         const bool v046 = variant == 0 || variant == 4 || variant == 6;
-        return v046 && kind == kContiguous && bm / wm <= 64 ? 256 * wm * wn : 0;
+        return v046 && (kind == kContiguous || ep.lora) && bm / wm <= 64 ? 256 * wm * wn : 0;
     }
     int lds_bytes() const {
         if (variant == 4) {   // three A slots (tile + sfa), two B slots (tile + sfb); BF16: no scales

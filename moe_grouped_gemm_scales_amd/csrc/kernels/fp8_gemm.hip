@@ -681,15 +681,18 @@ __device__ __forceinline__ void store_pair(u16* base, u64 row_off, int n, bool o
 //   many (decode, every row its own): each lane gathers the ranks of its four columns for its own rows.
 // A turn of the first way is a chain of loads, about 2000 clocks; the gather reads TM TN rank / 2 pieces of 16 bytes a
 // lane, which the CU takes in at about 64 a clock and wave of four: 32 TM TN rank clocks.
-template <int TM_, int TN_>
-__device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4f (&acc)[TM_][TN_], int row0, int col0) {
+template <int TM_, int TN_, bool GRP_LDS>
+__device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4f (&acc)[TM_][TN_], int row0, int col0,
+                                             u32 grp_lds) {
     const int R = p.rank, pitch = (R + 31) & ~31;
     const int l16 = row0 & 15, q = (col0 >> 2) & 3;
     int ad[TM_];                            // of the lane's rows; -1: none
 #pragma unroll
     for (int a = 0; a < TM_; ++a) {
         const int r = row0 + 16 * a;
-        ad[a] = r < tl.row_limit ? p.adapter[tl.m0 + r] : -1;
+        const int of = GRP_LDS ? *(__attribute__((address_space(3))) const int*)(grp_lds + a * 64)
+                               : p.adapter[tl.m0 + (r < tl.row_limit ? r : 0)];
+        ad[a] = r < tl.row_limit ? of : -1;
         if ((u32)ad[a] >= (u32)p.adapters) ad[a] = -1;
     }
     // the least adapter above `cur` among the wave's rows (the same in all lanes); -1 past the last
@@ -744,17 +747,18 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
             if constexpr (AHEAD) read_up(cur, 0);
             for (int k0 = 0; k0 < R; k0 += 32) {
                 if constexpr (!AHEAD) read_up(cur, k0);
-                v4i hi[3], lo[3];
+                constexpr int AHEAD_ROWS = AHEAD ? 2 : 1, RING = AHEAD_ROWS + 1;
+                v4i hi[RING], lo[RING];
                 auto read_low = [&](int a) {
-                    hi[a % 3] = lo[a % 3] = v4i{0, 0, 0, 0};
+                    hi[a % RING] = lo[a % RING] = v4i{0, 0, 0, 0};
                     if (ad[a] == cur) {
                         const u16* low = low_of(a, k0 + 8 * q);
-                        hi[a % 3] = *(const v4i*)low;
-                        lo[a % 3] = *(const v4i*)(low + 512);
+                        hi[a % RING] = *(const v4i*)low;
+                        lo[a % RING] = *(const v4i*)(low + 512);
                     }
                 };
                 read_low(0);
-                if constexpr (TM_ > 1) read_low(1);
+                if constexpr (TM_ > 1 && AHEAD_ROWS > 1) read_low(1);
                 v8bf up[TN_];
 #pragma unroll
                 for (int b = 0; b < TN_; ++b) up[b] = operand(up_next[b]);
@@ -763,11 +767,11 @@ __device__ __forceinline__ void add_low_rank(const Params& p, const Tile& tl, v4
                 }
 #pragma unroll
                 for (int a = 0; a < TM_; ++a) {
-                    if (a + 2 < TM_) read_low(a + 2);
+                    if (a + AHEAD_ROWS < TM_) read_low(a + AHEAD_ROWS);
                     const u64 mine = __ballot(ad[a] == cur);
                     if (mine == 0) continue;                      // (the same for the whole wave)
                     const bool keep = mine == ~0ull || ad[a] == cur;
-                    const v8bf h = __builtin_bit_cast(v8bf, hi[a % 3]), l = __builtin_bit_cast(v8bf, lo[a % 3]);
+                    const v8bf h = __builtin_bit_cast(v8bf, hi[a % RING]), l = __builtin_bit_cast(v8bf, lo[a % RING]);
 #pragma unroll
                     for (int b = 0; b < TN_; ++b) {
                         const v4f before = acc[a][b];
@@ -930,7 +934,7 @@ __device__ __forceinline__ void fused_epilogue(const Params& p, const Tile& tl, 
 }
 #endif
 
-// GRP_LDS (contiguous form): the expert of the lane's row row0 + 16 a is the
+// GRP_LDS (contiguous form, low-rank adapters): the expert or adapter of the lane's row row0 + 16 a is the
 // int at LDS address grp_lds + 64 a, instead of being read from global memory.
 template <int TM_, int TN_, bool GRP_LDS = false>
 __device__ __forceinline__ void finish_tile(const Params& p, const Tile& tl, v4f (&acc)[TM_][TN_], int row0,
@@ -1053,7 +1057,7 @@ __device__ __forceinline__ void finish_tile(const Params& p, const Tile& tl, v4f
     else row_base = (u64)tl.m0 * N;
 #if DG_EPI
 #if DG_LORA
-    add_low_rank<TM_, TN_>(p, tl, acc, row0, col0);
+    add_low_rank<TM_, TN_, GRP_LDS>(p, tl, acc, row0, col0, grp_lds);
 #endif
     fused_epilogue<TM_, TN_, GRP_LDS>(p, tl, acc, row0, col0, grp_lds, row_base);
     return;
@@ -1211,8 +1215,8 @@ constexpr int RING_BYTES = AAHEAD ? B_RING + STAGES * B_SLOT : STAGES * STAGE_BY
 // Contiguous form: the expert of each of the wave's rows (WAVE_M <= 64 of them),
 // brought into LDS by one DMA of the wave at the start of the tile, so the
 // epilogue does not wait on global reads of the group index while every CU
-// stores its tile.
-constexpr bool ROW_GRP_LDS = kKind == 1 && WAVE_M <= 64;
+// stores its tile.  So for the adapters of the rows.
+constexpr bool ROW_GRP_LDS = (kKind == 1 || DG_LORA) && WAVE_M <= 64;
 constexpr int GRP_OFF = RING_BYTES;
 constexpr int LDS_BYTES = RING_BYTES + (ROW_GRP_LDS ? NWAVES * 256 : 0);
 static_assert(BM % RPI_A == 0 && BN % RPI_B == 0, "tiles are loaded RPI rows per instruction");
@@ -1625,10 +1629,15 @@ dg_fp8_gemm_nt_kernel(const KernArgs ka) {
             // counts only the loads issued after the group it waits for, which
             // complete in order, so a store still pending only delays a wait.
             __syncthreads();
-            // the experts of this wave's rows (contiguous form), for the epilogue;
+            // the experts of this wave's rows (contiguous form), or their adapters, for the epilogue;
             // rows past M read as 0 and are never stored
             if constexpr (ROW_GRP_LDS) {
-                dma4(make_rsrc(p.grp, (u32)p.M * 4u), (u32)(tl.m0 + wm * WAVE_M + lane) * 4u, 0u,
+#if DG_LORA
+                const int* const of_rows = p.adapter;
+#else
+                const int* const of_rows = p.grp;
+#endif
+                dma4(make_rsrc(of_rows, (u32)p.M * 4u), (u32)(tl.m0 + wm * WAVE_M + lane) * 4u, 0u,
                      __builtin_amdgcn_readfirstlane(smem_base + GRP_OFF + wave * 256));
             }
 

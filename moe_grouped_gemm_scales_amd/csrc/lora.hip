@@ -8,7 +8,7 @@
 // rows are 128 bytes each a step), and their sums meet in LDS.  It reads A once, and from
 // L2 an adapter once for each 16 rows that use it; a few dependent round trips bound it.
 // us (sixteen waves in brackets): 32 x 2048, 32 adapters of rank 16 4.1 (4.1), of which a launch is 2; 4096 x 2048,
-// eight of rank 64 10.9 (13.2), one alone 7.7 (10.0), 8192 x 7168 rank 64 59 (85).  With 32 rows a workgroup, which
+// eight of rank 64 11 (13), one alone 7.8 (10.0), 8192 x 7168 rank 64 60 (85).  With 32 rows a workgroup, which
 // reads an adapter half as often, the last takes 55, but 4096 x 2048 17.6 and 16384 x 2048 25.8 against 23.6.
 #include "row_kernels.h"
 
@@ -40,10 +40,10 @@ struct DownArgs {
     int M, K, adapters, rank, pitch;
 };
 
-// SUBS: 16-rank pieces of a workgroup (1, 2 or 4; a workgroup has 16 SUBS ranks).  EACH: grid z is a row of the 16, and the workgroup does
-// the adapter of that row if no earlier row has the same (decode: up to 16 adapters side by side);
-// otherwise one workgroup does all adapters of its rows in turn (prompts: mostly one).
-template <int SUBS, bool EACH>
+// SUBS: 16-rank pieces of a workgroup (1, 2 or 4; a workgroup has 16 SUBS ranks).  Grid z of 16: a row, whose adapter the
+// workgroup does if no earlier row has the same.  Of fewer: a place in the list of the 16 rows' adapters, the last place
+// doing all that are left, in turn.
+template <int SUBS>
 __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, q = lane >> 4;
@@ -51,15 +51,18 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
     const int r0 = (int)blockIdx.y * (16 * SUBS);
     int ad = m < a.M ? a.adapter[m] : -1;
     if ((u32)ad >= (u32)a.adapters) ad = -1;
+    // rows whose adapter is not done by an earlier place
     u32 todo = (u32)__ballot(ad >= 0) & 0xffffu;
-    if constexpr (EACH) {
-        const u32 z = blockIdx.z;
-        const int of_z = __builtin_amdgcn_readlane(ad, (int)z);
-        const u32 same = (u32)__ballot(ad == of_z) & 0xffffu;
-        if (of_z < 0 || (u32)__builtin_ctz(same) != z) return;
-        todo = same;
+    auto next_of = [&]() { return __builtin_amdgcn_readlane(ad, __builtin_ctz(todo)); };
+    if (gridDim.z == kRows) {
+        const int of_z = __builtin_amdgcn_readlane(ad, (int)blockIdx.z);
+        todo = of_z < 0 ? 0u : (u32)__ballot(ad == of_z) & 0xffffu;
+        if (todo == 0u || (u32)__builtin_ctz(todo) != blockIdx.z) return;
+    } else {
+        for (u32 z = 0; z < blockIdx.z && todo; ++z) todo &= ~(u32)__ballot(ad == next_of());
+        if (todo == 0u) return;
+        if (blockIdx.z + 1 < gridDim.z) todo &= (u32)__ballot(ad == next_of());
     }
-    if (todo == 0u) return;
     f32x4 sum[SUBS];
 #pragma unroll
     for (int s = 0; s < SUBS; ++s) sum[s] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -73,8 +76,8 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
     const int mr = (int)blockIdx.x * kRows + lr;
     const u16* rows = a.A + (u64)(mr < a.M ? mr : a.M - 1) * (u64)a.K + lc;
     while (todo) {
-        const int mine = __builtin_amdgcn_readlane(ad, __builtin_ctz(todo));
-        todo &= ~((u32)__ballot(ad == mine) & 0xffffu);
+        const int mine = next_of();
+        todo &= ~(u32)__ballot(ad == mine);
         const u16* down[SUBS];
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) {
@@ -150,13 +153,13 @@ dg_status lora_down(const LoraArgs& l, const void* A, void* low, int M, int K, v
     const int pitch = lora_pitch(l.rank);
     const DownArgs args{static_cast<const u16*>(A), static_cast<const u16*>(l.down), l.adapter, l.scale, static_cast<u16*>(low), M, K,
                         l.adapters, l.rank, pitch};
-    // side by side up to 512 rows: 16 times the workgroups, most of which end at once where prompts fill the tiles
-    const bool each = M <= 512;
+    // Up to 2048 rows every row is a place (decode: 16 adapters side by side), for more there are two (prompts, where a
+    // block that ends one and begins the next would take twice as long); most of them find nothing to do and end.  us with
+    // one place, two and 16: 600 rows of 32 adapters 28.3, 26.6, 8.6; prompts, 517 x 1536 5.5, 4.2, 4.2, 2048 x 2048
+    // 6.3, 4.9, 5.0; 4096 x 2048, rank 64, 11.6 each, with one adapter 8.0, 8.0, 9.3.
     const int subs = l.rank <= 16 ? 1 : l.rank <= 32 ? 2 : 4;
-    const dim3 grid((M + kRows - 1) / kRows, (l.rank + 16 * subs - 1) / (16 * subs), each ? kRows : 1);
-    auto* kernel = subs == 1 ? (each ? dg_lora_down_kernel<1, true> : dg_lora_down_kernel<1, false>)
-                 : subs == 2 ? (each ? dg_lora_down_kernel<2, true> : dg_lora_down_kernel<2, false>)
-                             : (each ? dg_lora_down_kernel<4, true> : dg_lora_down_kernel<4, false>);
+    const dim3 grid((M + kRows - 1) / kRows, (l.rank + 16 * subs - 1) / (16 * subs), M <= 2048 ? kRows : 2);
+    auto* kernel = subs == 1 ? dg_lora_down_kernel<1> : subs == 2 ? dg_lora_down_kernel<2> : dg_lora_down_kernel<4>;
     return launch_rows("lora (down)", kernel, grid, 64 * kWaves, stream, args);
 }
 
