@@ -8,7 +8,12 @@ Serving a few tokens, FP8 weights (masked layout): the tokens are quantised on t
 the first product is FP8 with its bias and activation in the epilogue, its BF16 result goes through
 dg_moe_dispatch_fp8 row by row to become the second product's operand.
 
-`python examples/moe_layer.py` runs both at a small size and prints how far they are from the same layer
+A whole block, y = x + experts(norm(x)), with a router that is trained and the first product's pre-activation kept in
+8 bits from the forward to the backward pass (MoEBlock):
+
+    norm -> router product -> route -> sort -> dispatch -> Z1 (kept in E4M3), h -> out -> combine with x
+
+`python examples/moe_layer.py` runs them at a small size and prints how far they are from the same layer
 in 32-bit torch operations, and the time of a step.
 """
 from __future__ import annotations
@@ -80,6 +85,98 @@ class MoELayer:
         # the dispatch's gradient is the unweighted combine; the residual path adds dy itself
         g["x"] = dg.dg_moe_combine(self.d_rows, self.pos, None, dy, torch.empty_like(dy))
         return g
+
+
+class MoEBlock(MoELayer):
+    """Training block x + experts(norm(x)).  Of Z1 and h only 8 bits of Z1 outlive the forward pass: both buffers can
+    be shared by a model's blocks, as here by all blocks that are given the same `shared`."""
+
+    def __init__(self, tokens, hidden, inner, experts, topk, activation="silu", device="cuda", seed=0, shared=None):
+        super().__init__(tokens, hidden, inner, experts, topk, activation, device, seed)
+        g = torch.Generator(device=device).manual_seed(seed + 100)
+        self.norm = (1 + 0.1 * torch.randn(hidden, generator=g, device=device)).to(BF16)
+        self.eps = 1e-6
+        self.codes = torch.zeros((self.rows.shape[0], inner), dtype=torch.uint8, device=device)
+        self.scales = torch.zeros((self.rows.shape[0], -(-inner // 128)), dtype=torch.uint8, device=device)
+        if shared is not None:
+            self.z1, self.h = shared.z1, shared.h
+
+    def forward(self, x):
+        self.x = x
+        self.xn = dg.dg_rms_norm(x, self.norm, self.eps, Y=torch.empty_like(x))
+        self.logits = dg.dg_bf16_gemm_nt(self.xn, self.router, None,
+                                         torch.empty((x.shape[0], self.experts), dtype=BF16, device=x.device))
+        self.ids = torch.empty((x.shape[0], self.topk), dtype=torch.int32, device=x.device)
+        self.weights = torch.empty((x.shape[0], self.topk), device=x.device)
+        dg.dg_moe_route(self.logits, None, self.ids, self.weights)
+        self.pos, m = torch.empty_like(self.ids), self.m_indices
+        dg.dg_moe_sort_contiguous(self.ids, self.experts, self.pos, m, self.ks)
+        dg.dg_moe_dispatch_bf16(self.xn, self.pos, m, self.rows)
+        dg.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(self.rows, self.w1, m, self.h, bias=self.b1,
+                                                         activation=self.act, Z=self.z1)
+        dg.dg_checkpoint_fp8(self.z1, self.codes, self.scales, m_indices=m)
+        dg.dg_m_grouped_bf16_gemm_nt_contiguous_epilogue(self.h, self.w2, m, self.out, bias=self.b2)
+        return dg.dg_moe_combine(self.out, self.pos, self.weights, x, torch.empty_like(x))
+
+    def backward(self, dy):
+        """Gradients of x and the parameters, as a dict."""
+        g = {n: torch.empty_like(getattr(self, n)) for n in ("w1", "w2", "b1", "b2", "router")}
+        g["norm"] = torch.empty(self.norm.shape, device=dy.device)
+        dw, m = torch.empty_like(self.weights), self.m_indices
+        dg.dg_moe_combine_backward(dy, self.out, self.pos, self.weights, m, self.d_out, dw)
+        dg.dg_epilogue_backward(self.d_out, None, "none", None, g["b2"], m)
+        dg.dg_m_grouped_bf16_gemm_nn_contiguous(self.d_out, self.w2, m, None, self.dh)
+        # dZ1 in place of dh, and h again: both with cleared padding rows, as the weight gradients need
+        dg.dg_epilogue_backward_fp8(self.dh, self.codes, self.scales, self.act, self.dh, g["b1"], H=self.h, m_indices=m)
+        dg.dg_k_grouped_bf16_gemm_tn_contiguous(self.d_out, self.h, self.ks, None, g["w2"])
+        dg.dg_m_grouped_bf16_gemm_nn_contiguous(self.dh, self.w1, m, None, self.d_rows)
+        dg.dg_k_grouped_bf16_gemm_tn_contiguous(self.dh, self.rows, self.ks, None, g["w1"])
+        # the router's share of the norm's gradient, and the dispatch's
+        d_logits = dg.dg_moe_route_backward(self.logits, self.ids, dw, torch.empty_like(self.logits))
+        dg.dg_bf16_gemm_tn(d_logits, self.xn, None, g["router"])
+        d_xn = dg.dg_bf16_gemm_nn(d_logits, self.router, None, torch.empty_like(dy))
+        d_xn = dg.dg_moe_combine(self.d_rows, self.pos, None, d_xn, d_xn)
+        g["x"] = dg.dg_rms_norm_backward(d_xn, self.x, self.norm, self.eps, d_xn, g["norm"], dS=dy)
+        return g
+
+
+def reference_block(block, x):
+    """The block in 32-bit torch operations with the block's choice of experts: (y, its inputs by name)."""
+    leaf = lambda t: t.detach().float().requires_grad_()
+    v = {n: leaf(getattr(block, n)) for n in ("w1", "w2", "b1", "b2", "router", "norm")} | {"x": leaf(x)}
+    acts = dict(none=lambda z: z, relu=torch.relu, silu=torch.nn.functional.silu, gelu=torch.nn.functional.gelu,
+                gelu_tanh=lambda z: torch.nn.functional.gelu(z, approximate="tanh"))
+    xn = v["x"] * torch.rsqrt(v["x"].pow(2).mean(1, keepdim=True) + block.eps) * v["norm"]
+    w = torch.gather(torch.softmax(xn @ v["router"].T, dim=1), 1, block.ids.long())
+    w = w / w.sum(1, keepdim=True)
+    y = v["x"]
+    for j in range(block.topk):
+        for e in range(block.experts):
+            t = torch.nonzero(block.ids[:, j] == e)[:, 0]
+            if len(t):
+                h = acts[block.act](xn[t] @ v["w1"][e].T + v["b1"][e])
+                y = y.index_add(0, t, w[t, j, None] * (h @ v["w2"][e].T + v["b2"][e]))
+    return y, v
+
+
+def check_block(tokens=300, hidden=512, inner=384, experts=6, topk=2, activation="gelu", seed=0, device="cuda"):
+    """Distances of the outputs of two blocks in a row, forward and backward, from the reference, by name."""
+    first = MoEBlock(tokens, hidden, inner, experts, topk, activation, device, seed)
+    second = MoEBlock(tokens, hidden, inner, experts, topk, activation, device, seed + 1, shared=first)
+    g = torch.Generator(device=device).manual_seed(seed + 2)
+    far = {}
+    for step in range(2):                      # the second step reuses every buffer with other routes
+        x, dy = (torch.randn((tokens, hidden), generator=g, device=device).to(BF16) for _ in range(2))
+        between = first.forward(x)
+        y = second.forward(between)
+        grads = [second.backward(dy)]
+        grads.append(first.backward(grads[0]["x"]))
+        for block, inp, out, dout, got in ((second, between, y, dy, grads[0]), (first, x, between, grads[0]["x"], grads[1])):
+            want, v = reference_block(block, inp)
+            want.backward(dout.float())
+            name = "first" if block is first else "second"
+            far |= {f"{name}.y": distance(out, want.detach())} | {f"{name}.{n}": distance(got[n], v[n].grad) for n in v}
+    return far
 
 
 def quantise_weight(w):
@@ -165,8 +262,8 @@ def check(tokens=300, hidden=512, inner=384, experts=6, topk=2, activation="gelu
 
 
 def main():
-    for name, d in check().items():
-        print(f"{name:6s} {d:.2e}")
+    for name, d in (check() | check_block()).items():
+        print(f"{name:14s} {d:.2e}")
     layer = MoELayer(8192, 4096, 2048, 8, 2)
     x = torch.randn((8192, 4096), device="cuda").to(BF16)
     ids, weights = route(x, layer.router, 2)

@@ -390,10 +390,11 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue(const void *A, const in
  *   adapter int32 [M]: in any order, one a row; outside [0, num_adapters): none, the row's
  *         plain product
  *   scale FP32 [num_adapters] or NULL (1)
- * FP32 throughout up to the one rounding of D and of Z; the inner product, low =
- * scale (A down^T), stays FP32 (as two BF16 where matrix instructions take it, 2^-17).
+ * FP32 throughout up to the one rounding of D and of Z, but for the inner product,
+ * low = scale (A down^T), which is kept as the sum of two BF16 numbers (2^-17).
  * Rows of other adapters see nothing of one that holds an infinity or NaN.
- * down and up must be 16-byte, adapter and scale 4-byte aligned; M at most 2^24.
+ * down and up must be 16-byte, adapter and scale 4-byte aligned; M at most 2^24,
+ * N * rank below 2^31.
  * low stands in the stream's workspace, M * rank (rounded up to 32) * 4 bytes.
  */
 typedef struct {

@@ -926,7 +926,9 @@ dg_status dg_bf16_gemm_nt_lora(const void* A, const void* B, const dg_lora* lora
         if (l.rank % 8 || l.rank > 256) return set_error(DG_ERR_UNSUPPORTED, "lora: rank must be a multiple of 8 up to 256");
         if (!aligned(l.down, 16) || !aligned(l.up, 16) || !aligned(l.adapter, 4) || !aligned(l.scale, 4))
             return set_error(DG_ERR_ALIGNMENT, "lora: down and up must be 16-byte, adapter and scale 4-byte aligned");
-        if (M > (1 << 24)) return set_error(DG_ERR_UNSUPPORTED, "lora: more than 2^24 rows");
+        // (an adapter's second factor is addressed with 32-bit offsets)
+        if (M > (1 << 24) || (int64_t)N * l.rank > INT_MAX)
+            return set_error(DG_ERR_UNSUPPORTED, "lora: more than 2^24 rows, or N * rank of 2^31 and more");
         Epilogue ep;
         EpilogueArgs args;
         const dg_epilogue plain{};

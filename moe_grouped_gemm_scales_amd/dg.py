@@ -15,6 +15,7 @@ group dimension as documented in include/dg.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -1161,11 +1162,12 @@ class _Norm(ctypes.Structure):      # dg_norm
 
 def _rows_of(t, name):
     """(T, H) of the call's BF16 rows."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be [T, H]")
-    if max(t.shape) > _INT_MAX:
-        _too_many(f"rows of {name}", max(t.shape))
-    return t.shape
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+        _too_many(f"rows of {name}", max(shape))
+    return shape
 
 
 def _weight(weight, H, dev):
@@ -1189,13 +1191,17 @@ def dg_rms_norm(X, weight, eps, Y=None, residual=None, S=None, Q=None, sf=None, 
     if (Q is None) != (sf is None):
         raise ValueError("Q and sf go together")
     w, wide = _weight(weight, H, dev)
-    ue8m0 = sf is not None and sf.dtype is _I32
-    x = _arg(X, "X", _BF, shape, dev)
-    norm = _Norm(_opt(residual, "residual", _BF, shape, dev), w, wide, eps, _opt(S, "S", _BF, shape, dev),
-                 _opt(Y, "Y", _BF, shape, dev), None if Q is None else _fp8_arg(Q, "Q", shape, dev),
-                 _opt(sf, "sf", _I32 if ue8m0 else _F32, ((H + 511) // 512 if ue8m0 else H // 128, T), dev), ue8m0)
-    if norm.S and norm.S == norm.Y:
-        raise ValueError("S and Y must not be the same tensor")
+    x, norm = _arg(X, "X", _BF, shape, dev), _Norm(None, w, wide, eps)
+    if residual is not None:
+        norm.residual = _arg(residual, "residual", _BF, shape, dev)
+    if S is not None:
+        norm.S = _arg(S, "S", _BF, shape, dev)
+    if Y is not None:
+        norm.Y = _arg(Y, "Y", _BF, shape, dev)
+    if Q is not None:
+        norm.Q = _fp8_arg(Q, "Q", shape, dev)
+        norm.ue8m0 = ue8m0 = sf.dtype is _I32
+        norm.sf = _arg(sf, "sf", _I32 if ue8m0 else _F32, ((H + 511) // 512 if ue8m0 else H // 128, T), dev)
     status = lib.dg_rms_norm(x, ctypes.byref(norm), T, H, _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -1226,30 +1232,29 @@ class _Routing(ctypes.Structure):       # dg_routing
                 ("group_best", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+@functools.lru_cache(maxsize=64)
+def _routing(score, groups, topk_groups, group_best, renormalise, scale):
+    """The dg_routing of these settings, which a model's calls repeat (it is only read)."""
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
+    if max(groups, topk_groups, group_best) > _INT_MAX:
+        _too_many("groups", max(groups, topk_groups, group_best))
+    return ctypes.byref(_Routing(SCORES[score], groups, topk_groups, group_best, bool(renormalise), scale))
+
+
 def _logits(logits, others):
-    """((T, E), dtype, topk) of a router's logits [T,E] and an array [T,topk]."""
-    if logits.dtype is not _F32 and logits.dtype is not _BF:
-        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    if logits.dim() != 2 or others.dim() != 2:
+    """(shape [T, E], dtype, shape [T, topk], device) of a router's logits and an array of its choices."""
+    dtype, shape, chosen = logits.dtype, logits.shape, others.shape
+    if dtype is not _F32 and dtype is not _BF:
+        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
+    if len(shape) != 2 or len(chosen) != 2:
         raise ValueError("logits must be [T, num_experts], ids and weights [T, topk]")
-    if max(*logits.shape, others.shape[1]) > _INT_MAX:
-        _too_many("logits", max(*logits.shape, others.shape[1]))
-    return logits.shape, logits.dtype, others.shape[1]
-
-
-def _score(name) -> int:
-    score = SCORES.get(name)
-    if score is None:
-        raise ValueError(f"score must be one of {', '.join(SCORES)}, got {name!r}")
-    return score
-
-
-def _routed_on(logits) -> int:
-    """The device of the logits, which has to be the current one."""
-    d = logits.get_device()
-    if d < 0 or d != _cur_device():
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX or chosen[1] > _INT_MAX:
+        _too_many("logits", max(*shape, chosen[1]))
+    dev = logits.get_device()
+    if dev < 0 or dev != _cur_device():
         _dev(logits, "logits")
-    return d
+    return shape, dtype, (shape[0], chosen[1]), dev
 
 
 def dg_moe_route(logits, bias, expert_ids, weights, score="softmax", groups=1, topk_groups=1, group_best=1,
@@ -1261,13 +1266,12 @@ def dg_moe_route(logits, bias, expert_ids, weights, score="softmax", groups=1, t
     into weights float32 [T,topk].  bias float32 [num_experts] or None.  With groups > 1 only experts of the topk_groups
     groups with the largest sum of their group_best (1, 2) largest p + bias are chosen from.  Experts at -inf are not
     available: id -1 and weight 0 where too few are."""
-    (T, E), dtype, k = _logits(logits, expert_ids)
-    dev = _routed_on(logits)
-    routing = _Routing(_score(score), groups, topk_groups, group_best, bool(renormalise), scale)
+    shape, dtype, chosen, dev = _logits(logits, expert_ids)
     status = lib.dg_moe_route(
-        _arg(logits, "logits", dtype, (T, E), dev), dtype is _BF, _opt(bias, "bias", _F32, (E,), dev),
-        ctypes.byref(routing), _arg(expert_ids, "expert_ids", _I32, (T, k), dev),
-        _arg(weights, "weights", _F32, (T, k), dev), T, E, k, _raw_stream(stream, dev))
+        _arg(logits, "logits", dtype, shape, dev), dtype is _BF, _opt(bias, "bias", _F32, shape[1:], dev),
+        _routing(score, groups, topk_groups, group_best, renormalise, scale),
+        _arg(expert_ids, "expert_ids", _I32, chosen, dev), _arg(weights, "weights", _F32, chosen, dev), *shape, chosen[1],
+        _raw_stream(stream, dev))
     if status:
         _check(status)
     return expert_ids
@@ -1277,33 +1281,30 @@ def dg_moe_route_backward(logits, expert_ids, d_weights, d_logits, score="softma
                           stream=None):
     """d_logits [T,num_experts] (the logits' type; may be logits itself) from d_weights float32 [T,topk], with the ids,
     score, renormalise and scale of the forward call."""
-    (T, E), dtype, k = _logits(logits, expert_ids)
-    dev = _routed_on(logits)
-    routing = _Routing(_score(score), 1, 1, 1, bool(renormalise), scale)
+    shape, dtype, chosen, dev = _logits(logits, expert_ids)
     status = lib.dg_moe_route_backward(
-        _arg(logits, "logits", dtype, (T, E), dev), dtype is _BF, _arg(expert_ids, "expert_ids", _I32, (T, k), dev),
-        _arg(d_weights, "d_weights", _F32, (T, k), dev), ctypes.byref(routing),
-        _arg(d_logits, "d_logits", dtype, (T, E), dev), T, E, k, _raw_stream(stream, dev))
+        _arg(logits, "logits", dtype, shape, dev), dtype is _BF, _arg(expert_ids, "expert_ids", _I32, chosen, dev),
+        _arg(d_weights, "d_weights", _F32, chosen, dev), _routing(score, 1, 1, 1, renormalise, scale),
+        _arg(d_logits, "d_logits", dtype, shape, dev), *shape, chosen[1], _raw_stream(stream, dev))
     if status:
         _check(status)
     return d_logits
 
 
 # ---------------------------------------------------------------- 8-bit checkpoints
-def _kept_args(x, name, codes, scales, dev):
+def _kept_args(x, name, shape, codes, scales, dev):
     """(address of x [M,N], codes, scales)."""
-    M, N = x.shape
-    return (_arg(x, name, _BF, (M, N), dev), _fp8_arg(codes, "codes", (M, N), dev),
-            _arg(scales, "scales", torch.uint8, (M, _cdiv(N, 128)), dev))
+    return (_arg(x, name, _BF, shape, dev), _fp8_arg(codes, "codes", shape, dev),
+            _arg(scales, "scales", torch.uint8, (shape[0], (shape[1] + 127) // 128), dev))
 
 
 def dg_checkpoint_fp8(X, codes, scales, m_indices=None, stream=None):
     """Keep X [M,N] bfloat16 in 8 bits: codes [M,N] E4M3, scales uint8 [M,ceil(N/128)] (E8M0, one per 1x128 block).
 
     m_indices int32 [M] (contiguous layout): rows with -1 are kept as zeros, other negative ones are left alone."""
-    M, N = _rows_of(X, "X")
+    shape = M, N = _rows_of(X, "X")
     dev = _on(X, "X")
-    x, c, s = _kept_args(X, "X", codes, scales, dev)
+    x, c, s = _kept_args(X, "X", shape, codes, scales, dev)
     status = lib.dg_checkpoint_fp8(x, _opt(m_indices, "m_indices", _I32, (M,), dev), c, s, M, N, _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -1312,9 +1313,9 @@ def dg_checkpoint_fp8(X, codes, scales, m_indices=None, stream=None):
 
 def dg_checkpoint_restore(codes, scales, X, m_indices=None, stream=None):
     """X [M,N] bfloat16 from what dg_checkpoint_fp8 kept of it."""
-    M, N = _rows_of(X, "X")
+    shape = M, N = _rows_of(X, "X")
     dev = _on(X, "X")
-    x, c, s = _kept_args(X, "X", codes, scales, dev)
+    x, c, s = _kept_args(X, "X", shape, codes, scales, dev)
     status = lib.dg_checkpoint_restore(c, s, _opt(m_indices, "m_indices", _I32, (M,), dev), x, M, N,
                                        _raw_stream(stream, dev))
     if status:
@@ -1326,16 +1327,18 @@ def dg_epilogue_backward_fp8(dD, codes, scales, activation, dZ, dbias, H=None, m
                              num_experts=None):
     """dg_epilogue_backward on a Z kept by dg_checkpoint_fp8: dZ = dD * activation'(Z), dbias = its column sums, and
     H = activation(Z) bfloat16 [M,N]; each may be None.  num_experts as there."""
-    M, N = _rows_of(dD, "dD")
+    shape = M, N = _rows_of(dD, "dD")
     act, dev = _activation(activation), _on(dD, "dD")
-    args = (*_kept_args(dD, "dD", codes, scales, dev), act)
-    out = (_opt(dZ, "dZ", _BF, (M, N), dev), _opt(H, "H", _BF, (M, N), dev))
+    args = (*_kept_args(dD, "dD", shape, codes, scales, dev), act)
+    out = (_opt(dZ, "dZ", _BF, shape, dev), _opt(H, "H", _BF, shape, dev))
     if m_indices is None:
         status = lib.dg_epilogue_backward_fp8(*args, *out, _opt(dbias, "dbias", _F32, (N,), dev), M, N,
                                               _raw_stream(stream, dev))
     else:
         # (65535: the most that the library takes)
         G = num_experts if num_experts is not None else 65535 if dbias is None else dbias.shape[0]
+        if G > _INT_MAX:
+            _too_many("num_experts", G)
         status = lib.dg_m_grouped_epilogue_backward_fp8_contiguous(
             *args, _arg(m_indices, "m_indices", _I32, (M,), dev), *out, _opt(dbias, "dbias", _F32, (G, N), dev), M, N, G,
             _raw_stream(stream, dev))

@@ -16,7 +16,7 @@ INVALID, UNSUPPORTED, ALIGNMENT = -1, -2, -3
     (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(d=None), INVALID), (dict(down=None), INVALID),
     (dict(up=None), INVALID), (dict(adapter=None), INVALID), (dict(M=-1), INVALID), (dict(N=0), INVALID),
     (dict(K=0), INVALID), (dict(L=0), INVALID), (dict(R=0), INVALID), (dict(act=9), INVALID), (dict(K=96), UNSUPPORTED),
-    (dict(R=12), UNSUPPORTED), (dict(R=264), UNSUPPORTED), (dict(M=(1 << 24) + 1), UNSUPPORTED),
+    (dict(R=12), UNSUPPORTED), (dict(R=264), UNSUPPORTED), (dict(M=(1 << 24) + 1), UNSUPPORTED), (dict(N=1 << 27, R=16), UNSUPPORTED),
     (dict(a=FAKE + 8), ALIGNMENT), (dict(down=FAKE + 8), ALIGNMENT), (dict(up=FAKE + 2), ALIGNMENT),
     (dict(adapter=FAKE + 2), ALIGNMENT), (dict(scale=FAKE + 1), ALIGNMENT), (dict(bias=FAKE + 4), ALIGNMENT)])
 def test_lora_refusals(kw, status):

@@ -53,6 +53,11 @@ def test_route_binding_refuses_wrong_tensors():
         dg.dg_moe_route(l, None, i.reshape(-1), w)
     with pytest.raises(ValueError):
         dg.dg_moe_route_backward(l, i, w, l)
+    from moe_grouped_gemm_scales_amd.dg import _routing
+    with pytest.raises(ValueError):
+        _routing("relu", 1, 1, 1, True, 1.0)
+    with pytest.raises(ValueError):
+        _routing("softmax", 2 ** 32 + 1, 1, 1, True, 1.0)           # would wrap to one group
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
