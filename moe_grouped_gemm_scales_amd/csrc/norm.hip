@@ -424,7 +424,7 @@ dg_status dg_rms_norm_backward(const void* dY, const void* S, const void* weight
         int teams = 1024 / shape.threads, groups = kBackwardGroups;
         while (teams > 1 && (int64_t)groups * teams > T) teams /= 2;
         if (shape.threads < 1024 && T >= (int64_t)4 * groups * teams) groups *= 2;
-        const unsigned grid = (unsigned)std::min((T + teams - 1) / teams, groups);
+        const unsigned grid = (unsigned)std::min(((int64_t)T + teams - 1) / teams, (int64_t)groups);
         const int turns = grid ? (int)(((int64_t)T + (int64_t)grid * teams - 1) / ((int64_t)grid * teams)) : 0;
         float* partial = nullptr;
         StreamScratch scratch;               // held until both kernels are launched

@@ -247,3 +247,14 @@ def test_norm_same_bits_every_time():
         runs.append((dx, dw))
     for dx, dw in runs[1:]:
         assert torch.equal(dx, runs[0][0]) and torch.equal(dw, runs[0][1])
+
+
+def test_norm_backward_of_the_most_rows():
+    """2^31 - 1 rows of one element: s = 1 and dY = 1 give dX = 0 and a sum of ones (at most 512 partial sums, each
+    exact, so 512 roundings of 2^-24)."""
+    T = 2 ** 31 - 1
+    ones = torch.ones((T, 1), dtype=torch.bfloat16, device="cuda")
+    dx, dw = torch.full_like(ones, float("nan")), torch.empty(1, device="cuda")
+    dg.dg_rms_norm_backward(ones, ones, None, 0.0, dx, dw)
+    assert bool((dx == 0).all())
+    assert abs(float(dw) - T) <= 2 ** -15 * T
