@@ -1239,6 +1239,7 @@ def _routing(score, groups, topk_groups, group_best, renormalise, scale):
         raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
     if max(groups, topk_groups, group_best) > _INT_MAX:
         _too_many("groups", max(groups, topk_groups, group_best))
+    groups, topk_groups, group_best = max(groups, -1), max(topk_groups, -1), max(group_best, -1)     # (not wrapped)
     return ctypes.byref(_Routing(SCORES[score], groups, topk_groups, group_best, bool(renormalise), scale))
 
 

@@ -78,3 +78,10 @@ def test_route_gradient_against_differences(score, renormalise):
             d = torch.zeros_like(l)
             d[t, e] = step
             assert abs((loss(l + d) - loss(l - d)) / (2 * step) - float(got[t, e])) < 1e-8
+
+
+def test_negative_groups_do_not_wrap():
+    """-2^32 + 1 groups are refused by the library as -1, not taken as one."""
+    from moe_grouped_gemm_scales_amd.dg import _routing
+    assert _routing("softmax", 1 - 2 ** 32, 1, 1, True, 1.0)._obj.groups < 0
+    assert _routing("softmax", 1, 1 - 2 ** 32, 2 - 2 ** 32, True, 1.0)._obj.group_best < 0
