@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional
 
@@ -1232,15 +1233,25 @@ class _Routing(ctypes.Structure):       # dg_routing
                 ("group_best", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
-@functools.lru_cache(maxsize=64)
 def _routing(score, groups, topk_groups, group_best, renormalise, scale):
-    """The dg_routing of these settings, which a model's calls repeat (it is only read)."""
+    """The dg_routing of these settings.  They become plain numbers here, so that what is kept goes by their values: a
+    zero-dimensional tensor is read at every call."""
+    if not (type(scale) is float and type(renormalise) is bool and type(groups) is type(topk_groups) is
+            type(group_best) is int):
+        groups, topk_groups, group_best = map(operator.index, (groups, topk_groups, group_best))
+        renormalise, scale = bool(renormalise), float(scale)
+    return _routing_of(score, groups, topk_groups, group_best, renormalise, scale)
+
+
+@functools.lru_cache(maxsize=64)
+def _routing_of(score, groups, topk_groups, group_best, renormalise, scale):
+    """The same of plain numbers, which a model's calls repeat (it is only read)."""
     if score not in SCORES:
         raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
     if max(groups, topk_groups, group_best) > _INT_MAX:
         _too_many("groups", max(groups, topk_groups, group_best))
     groups, topk_groups, group_best = max(groups, -1), max(topk_groups, -1), max(group_best, -1)     # (not wrapped)
-    return ctypes.byref(_Routing(SCORES[score], groups, topk_groups, group_best, bool(renormalise), scale))
+    return ctypes.byref(_Routing(SCORES[score], groups, topk_groups, group_best, renormalise, scale))
 
 
 def _logits(logits, others):

@@ -85,3 +85,23 @@ def test_negative_groups_do_not_wrap():
     from moe_grouped_gemm_scales_amd.dg import _routing
     assert _routing("softmax", 1 - 2 ** 32, 1, 1, True, 1.0)._obj.groups < 0
     assert _routing("softmax", 1, 1 - 2 ** 32, 2 - 2 ** 32, True, 1.0)._obj.group_best < 0
+
+
+def test_settings_are_read_at_every_call():
+    """A scale or renormalise held in a tensor that changes in place counts as it is now; equal numbers of other types
+    do not decide what is taken."""
+    from moe_grouped_gemm_scales_amd.dg import _routing
+    scale, renormalise, groups = torch.tensor(2.5), torch.tensor(True), torch.tensor(2)
+    first = _routing("softmax", groups, 1, 1, renormalise, scale)._obj
+    assert (first.groups, first.renormalise, first.scale) == (2, 1, 2.5)
+    scale.fill_(3.0), renormalise.fill_(False), groups.fill_(4)
+    now = _routing("softmax", groups, 1, 1, renormalise, scale)._obj
+    assert (now.groups, now.renormalise, now.scale) == (4, 0, 3.0)
+    weight = torch.nn.Parameter(torch.tensor(0.5), requires_grad=False)
+    assert _routing("sigmoid", 1, 1, 1, True, weight)._obj.scale == 0.5
+    weight += 1
+    assert _routing("sigmoid", 1, 1, 1, True, weight)._obj.scale == 1.5
+    for _ in range(2):                                              # before and after an equal whole number is kept
+        with pytest.raises(TypeError):
+            _routing("softmax", 1.0, 1, 1, True, 1.0)
+        _routing("softmax", 1, 1, 1, True, 1)
