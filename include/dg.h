@@ -391,7 +391,8 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_ue8m0_epilogue(const void *A, const in
  *         plain product
  *   scale FP32 [num_adapters] or NULL (1)
  * FP32 throughout up to the one rounding of D and of Z, but for the inner product,
- * low = scale (A down^T), which is kept as the sum of two BF16 numbers (2^-17).
+ * low = scale (A down^T), which is kept as the sum of two BF16 numbers (2^-17): with an
+ * infinity in up, the rows of its adapter get an infinity or NaN in its column.
  * Rows of other adapters see nothing of one that holds an infinity or NaN.
  * down and up must be 16-byte, adapter and scale 4-byte aligned; M at most 2^24,
  * N * rank below 2^31.

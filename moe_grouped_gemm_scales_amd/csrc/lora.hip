@@ -10,6 +10,8 @@
 // us (sixteen waves in brackets): 32 x 2048, 32 adapters of rank 16 4.1 (4.1), of which a launch is 2; 4096 x 2048,
 // eight of rank 64 11 (13), one alone 7.8 (10.0), 8192 x 7168 rank 64 60 (85).  With 32 rows a workgroup, which
 // reads an adapter half as often, the last takes 55, but 4096 x 2048 17.6 and 16384 x 2048 25.8 against 23.6.
+#include <cmath>
+
 #include "row_kernels.h"
 
 namespace dg {
@@ -136,9 +138,12 @@ __global__ void __launch_bounds__(64 * kWaves) dg_lora_down_kernel(const DownArg
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float v = r + e < a.rank ? scale * t[e] : 0.f;
-            const u16 h = to_bf16(v);
+            u16 h = to_bf16(v);
+            // a number past BF16's range keeps what of it BF16 holds and the rest; an infinity or NaN has no rest
+            if ((h & 0x7fffu) == 0x7f80u && __builtin_fabsf(v) < INFINITY) h -= 1;
+            const float rest = (h & 0x7fffu) < 0x7f80u ? v - bf16_lo(h) : 0.f;
             hi |= (u64)h << (16 * e);
-            lo |= (u64)to_bf16(v - bf16_lo(h)) << (16 * e);
+            lo |= (u64)to_bf16(rest) << (16 * e);
         }
         store(r, hi, lo);
     }

@@ -171,3 +171,35 @@ def test_lora_on_two_streams():
     for D, o in zip(alone, out):
         for t in o:
             assert torch.equal(t, D)
+
+
+@pytest.mark.parametrize("M,L,R", [(40, 3, 128), (40, 40, 8)])          # adapter after adapter, and gathered
+def test_lora_low_past_bf16(M, L, R):
+    """Where low is infinite D is what the formula gives; where it is finite, but past BF16's numbers (3.39e38), D is as
+    near as elsewhere.  An infinity in up stays in its column of its adapter's rows."""
+    N, K = 136, 64
+    c = _case(M, N, K, R, L, "rows", 21)
+    c["adapter"] = (torch.arange(M) % L).to(torch.int32)
+    sound = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    _run(c, sound)
+    c["a"] = c["a"].abs() + 2 ** -6                              # (no zero meets an infinity)
+    c["down"][0, 3, 5] = float("inf")
+    c["a"][:, 0] = 1
+    c["down"][1] = 0
+    c["down"][1, :, 0] = torch.tensor([1, -1, 1, -1, 1, 1, -1, -1]).repeat(R // 8)     # low: +-scale
+    c["scale"][1] = 3.4e38
+    c["up"][1] *= 2.0 ** -100
+    D = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    _run(c, D)
+    want, base, low = ref.lora(c["a"], c["b"], c["down"], c["up"], c["adapter"], c["scale"], None)
+    got, first = D.cpu(), c["adapter"] == 0
+    assert torch.equal(got[first].double(), want[first]) and torch.isinf(want[first]).all()
+    _near(got[~first], want[~first], (2 ** -8 * want.abs() + _tolerance(c, base, low))[~first])
+    c = _case(M, N, K, R, L, "rows", 21)
+    c["adapter"] = (torch.arange(M) % L).to(torch.int32)
+    c["up"][2, 7, 3] = float("inf")
+    _run(c, D)
+    got, mine = D.cpu(), c["adapter"] == 2
+    assert not torch.isfinite(got[mine][:, 7]).any()
+    got[mine, 7] = sound.cpu()[mine, 7]
+    assert torch.equal(got, sound.cpu())
