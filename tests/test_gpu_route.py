@@ -219,3 +219,21 @@ def test_route_replayed():
             stream.synchronize()
             for a, b in zip(got, (ids, w, dl)):
                 assert torch.equal(a, b)
+
+
+# experts, groups, groups kept: lanes with 1, 2 and 4 experts, groups of whole lanes and others, rows that are not
+# read in whole pieces
+PROMPTS = [(7, 1, 1), (60, 5, 2), (96, 3, 2), (160, 8, 3), (250, 5, 2), (256, 8, 4)]
+
+
+@pytest.mark.parametrize("T,E,groups,kept", [(1027, *c) for c in PROMPTS] + [(2049, 256, 8, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_of_prompts(T, E, groups, kept, score, bf16):
+    """From 1024 tokens on a workgroup has four, the last one fewer; the gradient in the same sizes."""
+    k = min(6, E // groups * kept)
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(12))
+    l = _logits(T, E, E + T, bf16)
+    ids = _check(l, bias, k, score=score, groups=groups, topk_groups=kept, group_best=2 if E // groups > 1 else 1)
+    for renormalise in (True, False):
+        _backward(l, ids, score, renormalise)
