@@ -258,3 +258,37 @@ def test_norm_backward_of_the_most_rows():
     dg.dg_rms_norm_backward(ones, ones, None, 0.0, dx, dw)
     assert bool((dx == 0).all())
     assert abs(float(dw) - T) <= 2 ** -15 * T
+
+
+@pytest.mark.parametrize("T,H", [(600, 2303), (600, 4096), (600, 2432), (513, 2049), (2100, 1025)])
+def test_norm_of_prompts(T, H):
+    """More than 512 rows of 1025 to 4096 elements: two chunks a lane; E4M3 where the width has whole blocks."""
+    x, r, w = _bf((T, H), 51, 2.0), _bf((T, H), 52), _weight(H, "f32", 53)
+    y = Fenced((T, H), torch.bfloat16)
+    out = dict(Y=y.t)
+    e4m3 = H % 128 == 0
+    if e4m3:
+        q, sf = Fenced((T, H), torch.uint8), Fenced((H // 128, T), torch.float32)
+        out |= dict(Q=q.t, sf=sf.t)
+    dg.dg_rms_norm(x.cuda(), w.cuda(), EPS, residual=r.cuda(), **out)
+    _, wy = ref.rms_norm(x, r, w, EPS)
+    _near(y.check(), wy, 2 ** -8 * (1 + 2 ** -8) * wy.abs())
+    if e4m3:
+        scale = sf.check().t().double()
+        top = wy.reshape(T, -1, 128).abs().amax(-1)
+        _near(scale, top / 448, 2 ** -17 * scale)
+        _near(ref.e4m3_values(q.check(), scale), wy,
+              2 ** -4 * (1 + 2 ** -8) * wy.abs() + 2 ** -10 * scale.repeat_interleave(128, 1))
+
+
+@pytest.mark.parametrize("T,H", [(600, 2303), (2100, 4096), (700, 7168), (600, 8200), (300, 20001), (520, 32768), (2100, 1025)])
+@pytest.mark.parametrize("past", [True, False])
+def test_norm_backward_of_prompts(T, H, past):
+    """Teams of 512 lanes and of 1024 over several turns, and the weight's gradient kept in LDS from turn to turn."""
+    dy, s, w = _bf((T, H), 54), _bf((T, H), 55, 1.5), _weight(H, "bf16", 56)
+    ds = _bf((T, H), 57) if past else None
+    dx, dw = Fenced((T, H), torch.bfloat16), Fenced((H,), torch.float32)
+    dg.dg_rms_norm_backward(dy.cuda(), s.cuda(), w.cuda(), EPS, dx.t, dw.t, dS=_cuda(ds))
+    wx, ww, mx, mw = ref.rms_norm_backward(dy, s, w, EPS, ds)
+    _near(dx.check(), wx, 2 ** -8 * wx.abs() + 2 ** -16 * mx)
+    _near(dw.check(), ww, 2 ** -16 * mw)
