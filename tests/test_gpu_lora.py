@@ -203,3 +203,32 @@ def test_lora_low_past_bf16(M, L, R):
     assert not torch.isfinite(got[mine][:, 7]).any()
     got[mine, 7] = sound.cpu()[mine, 7]
     assert torch.equal(got, sound.cpu())
+
+
+# tiles of the planner, and whether a wave's rows are gathered (many adapters, up to 16 sub-tiles of 16 x 16) or go
+# adapter after adapter
+STRUCTURES = [("256n256", 2560, 5120, 256, 24, 6, "prompts"), ("256n256", 2500, 5001, 256, 64, 40, "rows"),
+              ("128n256", 3000, 2111, 1024, 64, 5, "prompts"), ("128n256", 3000, 2111, 1024, 24, 50, "rows"),
+              ("128n128", 2049, 2111, 64, 8, 100, "rows"), ("128n128", 2049, 2111, 64, 136, 9, "prompts")]
+
+
+@pytest.mark.parametrize("tile,M,N,K,R,L,kind", STRUCTURES)
+@pytest.mark.parametrize("full", [False, True])
+def test_lora_on_large_tiles(tile, M, N, K, R, L, kind, full):
+    flags = dg.EPI_BIAS_F32 | dg.EPI_RESIDUAL | dg.EPI_Z | dg.ACTIVATIONS["silu"] << 12 if full else 0
+    assert f"_m{tile}_" in dg.describe_config(dg.KIND_BF16 | dg.EPI_LORA | flags, M, N, K, 1, 0, 256)
+    c = _case(M, N, K, R, L, kind, 31)
+    D = Fenced((M, N), torch.bfloat16)
+    if not full:
+        _run(c, D.t)
+        z, base, low = ref.lora(c["a"], c["b"], c["down"], c["up"], c["adapter"], c["scale"], None)
+        _near(D.check(), z, 2 ** -8 * z.abs() + _tolerance(c, base, low))
+        return
+    bias, res = 0.3 * torch.randn(N, generator=torch.Generator().manual_seed(9)), _bf((M, N), 10)
+    Z = Fenced((M, N), torch.bfloat16)
+    _run(c, D.t, bias=bias.cuda(), activation="silu", residual=res.cuda(), Z=Z.t)
+    z, base, low = ref.lora(c["a"], c["b"], c["down"], c["up"], c["adapter"], c["scale"], bias)
+    tol = _tolerance(c, base, low)
+    _near(Z.check(), z, 2 ** -8 * z.abs() + tol)
+    want = ref.activation(z, "silu")[0] + res.double()
+    _near(D.check(), want, 2 ** -8 * want.abs() + 1.2 * tol + 2 ** -18 * (1 + z.abs()))

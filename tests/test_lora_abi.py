@@ -1,11 +1,17 @@
 """Argument checks of the low-rank adapters on the CPU: refused before any HIP call; their kernels' names."""
 import ctypes
+import glob
+import os
+import re
+import subprocess
 
 import pytest
 import torch
 
 import moe_grouped_gemm_scales_amd as dg
 from moe_grouped_gemm_scales_amd.dg import _Epilogue, _Lora, lib
+from tests.test_jit import PRECOMPILE, READELF, _notes, _run
+from tests.test_jit_epilogue import ACT, ALL, BF16
 
 FAKE = 0x100000   # a 16-byte aligned address that is never dereferenced
 P = ctypes.c_void_p
@@ -53,3 +59,26 @@ def test_lora_kernels_compile_ahead(M, N, K):
     for other in (dg.EPI_LORA, kind | 1, kind | 2, kind | 3, kind | dg.LAYOUT_NN):
         with pytest.raises(dg.DGError):
             dg.describe_config(other, 128, N, 128, 1, 0, 256)
+
+
+@pytest.mark.skipif(not os.path.exists(READELF), reason="LLVM tools not installed")
+def test_lora_kernels_compile_without_scratch(tmp_path):
+    """On every tile structure, with no other part of the epilogue and with all of them; the kernel's argument ends
+    with the adapters."""
+    kind, full = BF16 | dg.EPI_LORA, ALL | ACT["gelu"]
+    shapes = {"256n256": (4096, 7168, 2048), "128n256": (3000, 2111, 1024), "128n192": (2560, 7001, 64),
+              "192n128": (2049, 8000, 64), "128n128": (2049, 2111, 64), "128n64": (517, 2112, 1536), "64n128": (1000, 2111, 64),
+              "64n64": (1000, 1100, 64), "32n64": (600, 768, 256), "32n32": (32, 7168, 2048), "16n32": (16, 640, 256)}
+    plans = [(kind | extra, *s, 1, 0) for s in shapes.values() for extra in (0, full)]
+    for tile, s in shapes.items():
+        assert f"_m{tile}_" in dg.describe_config(kind, *s, 1, 0, 256)
+    r = _run(PRECOMPILE.format(plans=repr(plans)), tmp_path)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert all(line.split(")")[1].split()[0] == "0" for line in r.stdout.strip().splitlines()), r.stdout
+    objs = glob.glob(str(tmp_path / "*.hsaco"))
+    assert len(objs) == len(plans)
+    for path in objs:
+        name, v = os.path.basename(path), _notes(path)
+        assert not max(v["vgpr_spill_count"]) and not max(v["private_segment_fixed_size"]), (name, v)
+        out = subprocess.run([READELF, "--notes", path], capture_output=True, text=True).stdout
+        assert re.search(r"\.size:\s+152\s+\.value_kind:\s+by_value", out), name
