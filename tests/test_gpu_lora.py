@@ -232,3 +232,26 @@ def test_lora_on_large_tiles(tile, M, N, K, R, L, kind, full):
     _near(Z.check(), z, 2 ** -8 * z.abs() + tol)
     want = ref.activation(z, "silu")[0] + res.double()
     _near(D.check(), want, 2 ** -8 * want.abs() + 1.2 * tol + 2 ** -18 * (1 + z.abs()))
+
+
+def _adapters_by_block(M, L, counts):
+    """Block b of 16 rows has counts[b mod len(counts)] adapters, in turn over its rows; some of the rows have none."""
+    row = torch.arange(M)
+    n = torch.tensor(counts)[(row // 16) % len(counts)]
+    a = (3 * (row // 16) + (row % 16) % n) % L
+    a[row % 29 == 7] = -1
+    return a.to(torch.int32)
+
+
+@pytest.mark.parametrize("M,R", [(2048, 64), (2049, 16), (2100, 64), (4117, 136)])
+@pytest.mark.parametrize("counts", [(2,), (1, 3, 2), (16, 1, 5)])
+def test_lora_blocks_of_many_adapters(M, R, counts):
+    """Blocks of 16 rows with 1 to 16 adapters on both sides of the row count from which a block has two workgroups,
+    the second of which does every adapter but the first in turn."""
+    N, K, L = 264, 192, 37
+    c = _case(M, N, K, R, L, "none", 41)
+    c["adapter"] = _adapters_by_block(M, L, counts)
+    D = Fenced((M, N), torch.bfloat16)
+    _run(c, D.t)
+    want, base, low = ref.lora(c["a"], c["b"], c["down"], c["up"], c["adapter"], c["scale"], None)
+    _near(D.check(), want, 2 ** -8 * want.abs() + _tolerance(c, base, low))
