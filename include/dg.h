@@ -589,8 +589,9 @@ dg_status dg_rms_norm_backward(const void *dY, const void *S, const void *weight
  *   v = p + bias[expert]     bias FP32 [num_experts] or NULL: what keeps the experts' loads
  *                            balanced; it takes part in the choice alone
  *   The experts are groups runs of the same number of experts; a group is worth the sum of
- *   its group_best (1 or 2) largest v, and only experts of the topk_groups most worthy
- *   groups can be chosen (groups 1: of all).
+ *   its group_best (1 or 2) largest v, of its available experts (see below: a second that is
+ *   missing counts 0, a group without any is the least worthy), and only experts of the
+ *   topk_groups most worthy groups can be chosen (groups 1: of all).
  *   expert_ids [T][topk]: the experts of the topk largest v, largest first; of equals (groups
  *   too) the one of the lowest index first
  *   weights [T][topk] FP32: scale * p, or with renormalise scale * p / (sum of the chosen p)

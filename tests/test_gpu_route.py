@@ -237,3 +237,15 @@ def test_route_of_prompts(T, E, groups, kept, score, bf16):
     ids = _check(l, bias, k, score=score, groups=groups, topk_groups=kept, group_best=2 if E // groups > 1 else 1)
     for renormalise in (True, False):
         _backward(l, ids, score, renormalise)
+
+
+def test_route_group_that_lacks_its_second_expert():
+    """What is missing counts 0, so a group with one expert of 0.5 beats one of 0.6 and -0.2; a group without any is
+    kept last."""
+    inf = float("inf")
+    l = torch.zeros((1, 8))                       # sigmoid: 0.5 each
+    bias = torch.tensor([0.0, 0, 0.1, -0.7, 0, 0, -0.35, -0.35])
+    l[0, 1] = l[0, 4] = l[0, 5] = -inf            # worth 0.5, 0.6 - 0.2, nothing, 0.15 + 0.15
+    for kept, want in ((1, [0, -1]), (2, [2, 0, 3, -1]), (3, [2, 0, 6, 7, 3]), (4, [2, 0, 6, 7, 3, -1])):
+        ids, _ = _route(l, bias, len(want), score="sigmoid", groups=4, topk_groups=kept, group_best=2)
+        assert ids[0].tolist() == want
