@@ -557,7 +557,8 @@ dg_status dg_moe_combine_backward(const void *dY, const void *rows_in, const int
  * overflow it and give zeros (and gradients of zero or NaN).  Any H up to 32768.
  *
  * dg_rms_norm_backward, with S the norm's input (X without a residual) and dY
- * the gradient of y:
+ * the gradient of y.  It is the gradient at S as stored: with a residual, at s but for
+ * the rounding of S, which y does not have:
  *   dX = gradient of s through the norm + dS    BF16 [T][H] (dX, and the residual's
  *        gradient too; may be dY or dS itself, or NULL).  dS BF16 [T][H] or NULL: the
  *        gradient that reaches S past the norm
