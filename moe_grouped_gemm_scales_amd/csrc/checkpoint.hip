@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256) dg_epilogue_backward_fp8_kernel(const Kep
     }
     const int owner = __builtin_amdgcn_readlane(index[0], 0);
     for (int r0 = first + wave; r0 < last; r0 += kStep) {
-        // the expert of each of this wave's four rows (below 0: padding, or no row)
+        // the expert of each of this wave's two rows (below 0: padding, or no row)
         int expert[kWaveRows];
 #pragma unroll
         for (int i = 0; i < kWaveRows; ++i) {

@@ -161,7 +161,9 @@ dg_status lora_down(const LoraArgs& l, const void* A, void* low, int M, int K, v
     // Up to 2048 rows every row is a place (decode: 16 adapters side by side), for more there are two (prompts, where a
     // block that ends one and begins the next would take twice as long); most of them find nothing to do and end.  us with
     // one place, two and 16: 600 rows of 32 adapters 28.3, 26.6, 8.6; prompts, 517 x 1536 5.5, 4.2, 4.2, 2048 x 2048
-    // 6.3, 4.9, 5.0; 4096 x 2048, rank 64, 11.6 each, with one adapter 8.0, 8.0, 9.3.
+    // 6.3, 4.9, 5.0; 4096 x 2048, rank 64, 11.6 each, with one adapter 8.0, 8.0, 9.3.  The rule sees the number of rows
+    // alone: where more than 2048 rows have an adapter each, the second place does fifteen in turn (with the product, 2048 x
+    // 2112 x 2048 of rank 16 61 us, 2064 rows 76).
     const int subs = l.rank <= 16 ? 1 : l.rank <= 32 ? 2 : 4;
     const dim3 grid((M + kRows - 1) / kRows, (l.rank + 16 * subs - 1) / (16 * subs), M <= 2048 ? kRows : 2);
     auto* kernel = subs == 1 ? dg_lora_down_kernel<1> : subs == 2 ? dg_lora_down_kernel<2> : dg_lora_down_kernel<4>;
