@@ -554,7 +554,9 @@ dg_status dg_moe_combine_backward(const void *dY, const void *rows_in, const int
  *           power-of-two scales
  * A row that holds an infinity or NaN gives NaN in places of that row alone.
  * The sum of squares is an FP32 number: rows with |s| of 1e19 and more
- * overflow it and give zeros (and gradients of zero or NaN).  Any H up to 32768.
+ * overflow it and give zeros (and gradients of zero or NaN); rows of nothing but |s| under
+ * 1e-19 underflow it and, with an eps that does not outweigh them (below 1e-36), come out
+ * inexact, infinite or NaN.  Any H up to 32768.
  *
  * dg_rms_norm_backward, with S the norm's input (X without a residual) and dY
  * the gradient of y.  It is the gradient at S as stored: with a residual, at s but for
